@@ -79,8 +79,15 @@ typedef struct ihipStream_t* nvfp4moe_stream_t; /* == hipStream_t */
 #define NVFP4MOE_EPI_NONE 0
 #define NVFP4MOE_EPI_SILU_GATE 1 /* c receives H = silu(gate) * up, see below */
 
+/* moe_router scores (the softmax that gives the routing weights) */
+#define NVFP4MOE_ROUTER_TOPK_SOFTMAX 0 /* over the chosen logits: the weights sum to scale */
+#define NVFP4MOE_ROUTER_SOFTMAX 1      /* over all experts */
+
+/* elements that share a scale in the 8-bit optimizer states */
+#define NVFP4MOE_ADAMW_BLOCK 256
+
 /* ABI version of this header; returned by nvfp4moe_abi_version(). */
-#define NVFP4MOE_ABI_VERSION 2
+#define NVFP4MOE_ABI_VERSION 3
 
 int nvfp4moe_abi_version(void);
 /* Static string for a status code (never NULL). */
@@ -148,6 +155,53 @@ size_t nvfp4_quantize_onepass_workspace_size(int64_t rows, int64_t K, int64_t gr
 int nvfp4_quantize_onepass(const void* x, int x_dtype, int64_t rows, int64_t K, int64_t groups, float* amax_out,
                            uint8_t* q, uint8_t* scales, float* gscale, void* workspace, size_t workspace_bytes,
                            nvfp4moe_stream_t stream);
+
+/*
+ * moe_router -- the router: top-k experts of each token's logits and their
+ * softmax weights, ready for moe_permute* and moe_unpermute ([JA] fourth
+ * paragraph: device-side metadata; the pages do not describe the router).
+ *   key = logit + bias (fp32); a token's ids are its k largest keys, largest
+ *   first, ties to the lower expert.  A key that is -inf or NaN is never
+ *   chosen: slots left over get id -1 (which moe_permute* skip and
+ *   moe_unpermute ignores) and weight 0.  The bias only selects; weights,
+ *   lse and probabilities come from the logits.
+ *   score NVFP4MOE_ROUTER_TOPK_SOFTMAX: w = scale * softmax over the chosen
+ *   logits; NVFP4MOE_ROUTER_SOFTMAX: w = scale * softmax over all experts.
+ *   NaN and +inf logits give NaN wherever they enter a sum, as the formulas do.
+ *   logits    [T][E] of logits_dtype (F32 or BF16), element-aligned.
+ *   bias      [E] fp32 or NULL.
+ *   topk_ids  [T][k] int32 out, topk_w [T][k] fp32 out.
+ *   lse       [T] fp32 out or NULL: log sum_e exp(logit) (-inf for a row of
+ *             -inf), for a z-loss.
+ *   prob_sum  [E] fp32 out or NULL: sum over the tokens of the softmax over
+ *             all experts (a row of -inf adds nothing), for a load-balancing
+ *             loss.  Summed in a fixed order: the same bits on every run.
+ *   workspace needed with prob_sum only: moe_router_workspace_size(T, E, k)
+ *             bytes, 4-byte aligned; contents on entry do not matter; calls
+ *             that share one must not overlap.
+ * Errors: EINVAL (NULL, negative, bad dtype or score), ESHAPE (E > 4096,
+ * k > 64, k > E, T*k >= 2^31, alignment), EWORKSPACE.
+ */
+size_t moe_router_workspace_size(int64_t T, int E, int k);
+int moe_router(const void* logits, int logits_dtype, int64_t T, int E, int k, const float* bias, int score,
+               float scale, int32_t* topk_ids, float* topk_w, float* lse, float* prob_sum, void* workspace,
+               size_t ws_bytes, nvfp4moe_stream_t stream);
+
+/*
+ * moe_router_bwd -- gradient of moe_router's weights, lse and prob_sum with
+ * respect to the logits (the choice itself has none, nor has the bias).
+ *   logits, topk_ids, score, scale: as in the forward call (ids outside
+ *             [0, E) contribute nothing; a repeated id adds up).
+ *   d_topk_w  [T][k] fp32 or NULL (zeros); d_lse [T] or NULL; d_prob_sum [E]
+ *             or NULL.
+ *   lse       [T] fp32 of the forward, or NULL (then it is computed again).
+ *   d_logits  [T][E] of d_dtype (F32 or BF16) out, every element written; fp32
+ *             arithmetic.  Must not overlap the logits.
+ * Errors: as moe_router.
+ */
+int moe_router_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, const int32_t* topk_ids, int score,
+                   float scale, const float* d_topk_w, const float* lse, const float* d_lse, const float* d_prob_sum,
+                   void* d_logits, int d_dtype, nvfp4moe_stream_t stream);
 
 /*
  * moe_permute -- routing metadata for the contiguous per-expert layout and
@@ -251,6 +305,17 @@ int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, const void*
                    size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream);
 
 /*
+ * moe_permute_mxfp4 -- moe_permute_mx with MXFP4 (E2M1) codes: the
+ * activations of grouped_gemm_mxfp4.  q [T*k][D/2] (8-byte aligned), element
+ * 2j in the low nibble; equal, bit for bit, to mx_quantize(x,
+ * NVFP4MOE_MX_E2M1) followed by the row gather of codes and scales.  Other
+ * arguments and errors as moe_permute_mx.
+ */
+int moe_permute_mxfp4(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D,
+                      uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
+                      size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream);
+
+/*
  * moe_gather -- out[p] = w[src[p]] * x[src[p] / k] for p < R (w = 1 when
  * topk_w is NULL); rows with src[p] < 0 are written as zeros.  With
  * topk_w == NULL any dtype is copied verbatim (NVFP4MOE_U8 row payloads,
@@ -295,6 +360,28 @@ int moe_scatter(const void* x, int x_dtype, int64_t row_elems, const int32_t* de
  */
 int moe_unpermute(const void* y_perm, int y_dtype, const int32_t* dest, const float* topk_w,
                   int64_t T, int k, int64_t D, void* out, int out_dtype, nvfp4moe_stream_t stream);
+
+/*
+ * moe_unpermute_bwd -- the gradient of moe_unpermute in one pass:
+ *   dy_perm[dest[t*k+j]] = w[t][j] * dout[t]          (as moe_scatter, same bits)
+ *   d_topk_w[t][j]       = sum_d dout[t][d] * y_perm[dest[t*k+j]][d]
+ * the second being what the router's gradient needs ([JA] first paragraph: the
+ * backward; fourth: op fusion).  Products and sums in fp32, in a fixed order.
+ *   dout      [T][D] of dout_dtype, y_perm [T*k][D] of y_dtype (F32/BF16).
+ *   dest [T*k], offsets [E+1] (device) of the permutation; topk_w [T][k] fp32
+ *             or NULL (ones).  Assignments with dest outside [0, T*k) get
+ *             weight gradient 0 and write no row.
+ *   dy_perm   [T*k][D] of dy_dtype out, or NULL; rows past offsets[E] are
+ *             written as zeros.  Must not overlap y_perm or dout.
+ *   d_topk_w  [T][k] fp32 out, or NULL (then y_perm may be NULL); not both NULL.
+ *   amax_out  fp32 [1] or NULL: max |dy_perm| over the stored values (as
+ *             moe_scatter; needs dy_perm).
+ * D % 8 == 0; 16-byte aligned rows.  Errors: EINVAL (NULL, negative, bad
+ * dtype), ESHAPE (D % 8, k > 64, T*k >= 2^31, alignment).
+ */
+int moe_unpermute_bwd(const void* dout, int dout_dtype, const void* y_perm, int y_dtype, const int32_t* dest,
+                      const float* topk_w, const int32_t* offsets, int E, int64_t T, int k, int64_t D, void* dy_perm,
+                      int dy_dtype, float* d_topk_w, float* amax_out, nvfp4moe_stream_t stream);
 
 /*
  * grouped_gemm_w4a4 -- the grouped NVFP4 x NVFP4 GEMM over the contiguous
@@ -525,6 +612,41 @@ int grouped_gemm_w4a8_silu_gate_mx(const uint8_t* a_q, const uint8_t* a_s, const
                                    uint8_t* s_h, nvfp4moe_stream_t stream);
 
 /*
+ * grouped_gemm_mxfp4 -- the grouped GEMM with both operands MXFP4 (E2M1
+ * elements, E8M0 scale per 32 along K), the 4-bit format that gfx950's scaled
+ * MFMA multiplies as stored ([JA] third paragraph: W4A4; fourth: contiguous
+ * layout, grouped GEMM):
+ *   C[r][n] = sum_k deq(A)[r][k] * deq(B_e)[n][k],  r in [offsets[e], offsets[e+1])
+ * with deq = element * 2^(S-127); fp32 accumulation.  Rows >= offsets[E] are
+ * not written.  Scale bytes of 255 (NaN) are never produced by mx_quantize.
+ *   a_q [M_total][K/2], a_s [M_total][K/32]  (moe_permute_mxfp4, mx_quantize)
+ *   b_q [E][N][K/2],    b_s [E][N][K/32]     (mx_quantize E2M1)
+ *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).
+ * K % 128 == 0, N % 32 == 0; a_q, b_q, c 16-byte aligned, a_s, b_s 4-byte
+ * aligned; M_total, N < 2^31, K <= 2^22.  K == 0 gives zeros.  Errors: EINVAL
+ * (NULL, negative, bad dtype), ESHAPE (shape and alignment rules).
+ */
+int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,
+                       const int32_t* expert_offsets, int E, int64_t M_total, int64_t N, int64_t K, void* c,
+                       int c_dtype, nvfp4moe_stream_t stream);
+
+/*
+ * grouped_gemm_mxfp4_silu_gate -- the gate+up GEMM in MXFP4 with the SiLU gate
+ * in the epilogue and, when q_h is given, H quantized to MXFP4 there too ([JA]
+ * fourth paragraph: op fusion): equal, bit for bit, to grouped_gemm_mxfp4
+ * (N = 2F, B_e = [gate; up] rows, bf16 C), silu_gate_fwd and mx_quantize(H,
+ * NVFP4MOE_MX_E2M1).
+ *   y1 [M_total][2F] bf16 or NULL, h [M_total][F] bf16 or NULL, amax_out fp32
+ *   [1] or NULL (max |H|); q_h [M_total][F/2] (4-byte aligned) and s_h
+ *   [M_total][F/32], both or neither; h or q_h is required.
+ * F % 128 == 0, K % 128 == 0, F * K < 2^31.  Other rules and errors as
+ * grouped_gemm_mxfp4.
+ */
+int grouped_gemm_mxfp4_silu_gate(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,
+                                 const int32_t* expert_offsets, int E, int64_t M_total, int64_t F, int64_t K, void* y1,
+                                 void* h, float* amax_out, uint8_t* q_h, uint8_t* s_h, nvfp4moe_stream_t stream);
+
+/*
  * grouped_gemm_bf16 -- grouped BF16 GEMM, fp32 accumulation (the BF16
  * backward, [JA] first paragraph; also the BF16 baseline of the forward).
  *   NVFP4MOE_NT: a [M_total][K], b [E][N][K] -> c [M_total][N]
@@ -586,6 +708,67 @@ int silu_gate_fwd(const void* y1, int64_t R, int64_t F, void* h, float* amax_out
  */
 int silu_gate_bwd(const void* y1, const void* dh, int64_t R, int64_t F, void* dy1, float* amax_out,
                   nvfp4moe_stream_t stream);
+
+/*
+ * adamw_step -- one AdamW step (decoupled weight decay) over `count` tensors,
+ * the learner's weight update ([RU] intro: the learner; the pages name no
+ * optimizer).  Per element, in fp32 with one rounding per operation:
+ *   g = grad * grad_scale
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g g
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * All tensors of a call share the dtypes and hyperparameters.  Element
+ * pointers need only their element's alignment (16-byte aligned tensors are
+ * faster); no two tensors of a call may overlap.
+ *   tensors      HOST array, read before the call returns:
+ *     param      [n] F32 or BF16 (param_dtype), updated in place.  BF16
+ *                parameters are rounded stochastically (see seed).
+ *     param_bf16 [n] bf16 out or NULL: the new F32 parameter rounded to
+ *                nearest even (the GEMMs' copy).  F32 parameters only.
+ *     grad       [n] F32 or BF16 (grad_dtype).
+ *     exp_avg, exp_avg_sq  state_bits 32: [n] fp32.  state_bits 8: [n] bytes
+ *                with one fp32 scale per NVFP4MOE_ADAMW_BLOCK elements in
+ *                avg_scale, avg_sq_scale [ceil(n / 256)]: m = E4M3(code) *
+ *                scale; v = 2^((c >> 3) - 32) * (1 + (c & 7)/8) * scale with
+ *                c = code + 2, code 0 meaning 0 (255 is NaN; 254 is scale).
+ *                Scales are the block's max |m| times fp32(1/448) and max v,
+ *                over finite values; codes are rounded stochastically, a positive v never
+ *                to 0.  The update uses the moments before rounding.  Zero
+ *                bytes and scales are zero moments.
+ *   step, step_dev  t >= 1 on the host, or a device int64 [1] (then step is
+ *                not read): a captured graph counts its own steps.
+ *   lr, lr_dev   likewise (fp32 [1] on the device, NULL: lr).
+ *   grad_scale   fp32 [1] device or NULL (1): a clipping or unscaling factor.
+ *   skip         int32 [1] device or NULL: when not 0 nothing is changed.
+ *   seed         of the stochastic rounding: its bits are a function of
+ *                (seed, step, the tensor's place in the list, element).
+ * Errors: EINVAL (NULL, negative n, bad dtype or state_bits, param_bf16 with
+ * BF16 parameters, betas outside [0, 1), eps < 0, step < 1), ESHAPE
+ * (alignment).
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* avg_scale;    /* state_bits 8 only */
+  float* avg_sq_scale; /* state_bits 8 only */
+  void* param_bf16;    /* or NULL */
+  int64_t n;
+} nvfp4moe_adamw_tensor;
+
+int adamw_step(const nvfp4moe_adamw_tensor* tensors, int count, int param_dtype, int grad_dtype, int state_bits,
+               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+               const int64_t* step_dev, const float* lr_dev, const float* grad_scale, const int32_t* skip,
+               uint32_t seed, nvfp4moe_stream_t stream);
+
+/*
+ * adamw_read_state -- the fp32 values of 8-bit moments (for checkpoints and
+ * inspection): avg_out[i][j] and avg_sq_out[i][j], host arrays of device
+ * pointers [n] fp32.  Of each tensor only exp_avg, exp_avg_sq, avg_scale,
+ * avg_sq_scale and n are read.  Errors as adamw_step.
+ */
+int adamw_read_state(const nvfp4moe_adamw_tensor* tensors, int count, float* const* avg_out,
+                     float* const* avg_sq_out, nvfp4moe_stream_t stream);
 
 #ifdef __cplusplus
 }

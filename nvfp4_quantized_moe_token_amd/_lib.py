@@ -11,6 +11,14 @@ from .build import LIB_PATH
 
 c_int, c_i64, c_size, c_vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 c_char_p = ctypes.c_char_p
+c_float, c_double, c_u32 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32
+
+
+class AdamWTensor(ctypes.Structure):
+    """nvfp4moe_adamw_tensor of the header."""
+    _fields_ = [(n, c_vp) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "avg_scale", "avg_sq_scale",
+                                    "param_bf16")] + [("n", c_i64)]
+
 
 # name -> (restype, argtypes), in header order.
 SIGNATURES = {
@@ -55,6 +63,21 @@ SIGNATURES = {
                                   c_vp, c_size, c_vp]),
     "grouped_gemm_bf16_tn_gather": (c_int, [c_vp, c_vp, c_vp, c_int, c_i64, c_vp, c_int, c_i64, c_i64, c_i64,
                                             c_vp, c_int, c_int, c_vp]),
+    "moe_router_workspace_size": (c_size, [c_i64, c_int, c_int]),
+    "moe_router": (c_int, [c_vp, c_int, c_i64, c_int, c_int, c_vp, c_int, c_float, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
+                           c_vp]),
+    "moe_router_bwd": (c_int, [c_vp, c_int, c_i64, c_int, c_int, c_vp, c_int, c_float, c_vp, c_vp, c_vp, c_vp, c_vp,
+                               c_int, c_vp]),
+    "moe_permute_mxfp4": (c_int, [c_vp, c_i64, c_int, c_int, c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                  c_size, c_vp, c_vp]),
+    "moe_unpermute_bwd": (c_int, [c_vp, c_int, c_vp, c_int, c_vp, c_vp, c_vp, c_int, c_i64, c_int, c_i64, c_vp, c_int,
+                                  c_vp, c_vp, c_vp]),
+    "grouped_gemm_mxfp4": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_int, c_vp]),
+    "grouped_gemm_mxfp4_silu_gate": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_vp]),
+    "adamw_step": (c_int, [c_vp, c_int, c_int, c_int, c_int, c_double, c_double, c_double, c_double, c_double, c_i64,
+                           c_vp, c_vp, c_vp, c_vp, c_u32, c_vp]),
+    "adamw_read_state": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp]),
     "silu_gate_fwd": (c_int, [c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "silu_gate_bwd": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
 }
@@ -65,7 +88,9 @@ F32, BF16, U8 = 0, 1, 2
 NT, NN, TN = 0, 1, 2
 EPI_NONE, EPI_SILU_GATE = 0, 1
 MX_E4M3, MX_E2M1 = 0, 1
-ABI_VERSION = 2
+ROUTER_TOPK_SOFTMAX, ROUTER_SOFTMAX = 0, 1
+ADAMW_BLOCK = 256
+ABI_VERSION = 3
 NOALLOC_SCRATCH_BYTES = 2 << 20
 STATUS_BAD_EXPERT = 1
 

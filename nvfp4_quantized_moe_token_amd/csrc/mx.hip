@@ -19,6 +19,8 @@
 // so a wave stores one contiguous run; the even lane of a pair stores the
 // scale byte.  The grid covers the tensor once (grid-stride only past the
 // launch limit), as the NVFP4 quantizer does.
+#include <type_traits>
+
 #include "mx_codec.hpp"
 
 namespace nvfp4moe {
@@ -29,23 +31,9 @@ __device__ __forceinline__ uint4 encode16_e4m3(const float (&v)[16], int se) {
   return make_uint4(encode4_e4m3(v, se), encode4_e4m3(v + 4, se), encode4_e4m3(v + 8, se), encode4_e4m3(v + 12, se));
 }
 
-// 16 fp32 values to E2M1 codes (8 bytes, element 2j in the low nibble of
-// pair j): scaled by 2^-se, rounded by the hardware converter with a unit
-// scale (RNE, saturating to 6, sign kept).
+// 16 fp32 values to E2M1 codes (8 bytes).
 __device__ __forceinline__ uint2 encode16_e2m1(const float (&v)[16], int se) {
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#define MXQ_PAIR(I, SEL)                                                                                       \
-  w[h] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[h], __builtin_ldexpf(v[8 * h + (I)], -se),                  \
-                                                  __builtin_ldexpf(v[8 * h + (I) + 1], -se), 1.0f, SEL)
-    MXQ_PAIR(0, 0);
-    MXQ_PAIR(2, 1);
-    MXQ_PAIR(4, 2);
-    MXQ_PAIR(6, 3);
-#undef MXQ_PAIR
-  }
-  return make_uint2(w[0], w[1]);
+  return make_uint2(encode8_e2m1(v, se), encode8_e2m1(v + 8, se));
 }
 
 // One thread per 16-element half-block; half-blocks 2b and 2b+1 (lanes of
@@ -87,19 +75,21 @@ __global__ __launch_bounds__(NT) void mx_quantize_kernel(const uint4* __restrict
   }
 }
 
-// MXFP8 (E4M3) quantization fused with the token permutation, by scatter:
+// MX quantization (MXFP8 or MXFP4) fused with the token permutation, by scatter:
 // each 16-element half-block of X is read once, encoded once, and its codes
 // (and, from the even lane of the pair, its block's scale byte) are written
 // to the k permuted rows dest[t*k+j] of its token.  Rows past offsets[E]
 // (skipped assignments) are written as zeros, the encoding of a zero row.
 // Equal bit for bit to mx_quantize of X followed by the row gathers of the
 // codes and of the scales.
-template <int NT, bool BF16>
+template <int NT, bool BF16, bool E4M3>
 __global__ __launch_bounds__(NT) void mx_quantize_scatter_kernel(const uint4* __restrict__ x, int64_t T, int k,
                                                                  int64_t hpr, const int32_t* __restrict__ dest,
                                                                  const int32_t* __restrict__ offsets, int E,
-                                                                 int64_t R, uint4* __restrict__ q,
+                                                                 int64_t R, void* __restrict__ q,
                                                                  uint8_t* __restrict__ scales) {
+  using Codes = std::conditional_t<E4M3, uint4, uint2>;  // of one half-block: 16 or 8 bytes
+  Codes* qc = reinterpret_cast<Codes*>(q);
   const int64_t nhalf = T * hpr;
   const int64_t tid = blockIdx.x * (int64_t)NT + threadIdx.x, stride = (int64_t)gridDim.x * NT;
   for (int64_t hb = tid; hb < nhalf; hb += stride) {
@@ -127,40 +117,48 @@ __global__ __launch_bounds__(NT) void mx_quantize_scatter_kernel(const uint4* __
 #pragma unroll
     for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));
     a = fmaxf(a, __shfl_xor(a, 1, 64));  // the partner half of the block (hpr is even)
-    const int se = shared_exp<8>(a);
-    const uint4 codes = encode16_e4m3(v, se);
+    const int se = shared_exp<E4M3 ? 8 : 2>(a);
+    Codes codes;
+    if constexpr (E4M3) codes = encode16_e4m3(v, se);
+    else codes = encode16_e2m1(v, se);
     for (int jj = 0; jj < k; ++jj) {
       const int32_t r = dest[t * k + jj];
       if (r < 0) continue;
       const int64_t oh = (int64_t)r * hpr + j;
-      q[oh] = codes;
+      qc[oh] = codes;
       if ((j & 1) == 0) scales[oh >> 1] = (uint8_t)(se + 127);
     }
   }
   int64_t valid = offsets[E];
   valid = valid < 0 ? 0 : valid > R ? R : valid;
   for (int64_t h = valid * hpr + tid; h < R * hpr; h += stride) {
-    q[h] = make_uint4(0u, 0u, 0u, 0u);
+    qc[h] = Codes{};
     if ((h & 1) == 0) scales[h >> 1] = 0;
   }
 }
 
 }  // namespace
 
-// Enqueue the MXFP8 quantize-scatter of T token rows of D elements into the
+// Enqueue the MX quantize-scatter of T token rows of D elements into the
 // permuted rows given by dest (metadata already enqueued; D % 32 == 0).
-int mx_quantize_scatter_launch(const void* x, int x_dtype, int64_t T, int k, int64_t D, const int32_t* dest,
+int mx_quantize_scatter_launch(const void* x, int x_dtype, int64_t T, int k, int64_t D, int elem, const int32_t* dest,
                                const int32_t* offsets, int E, uint8_t* q, uint8_t* scales, hipStream_t st) {
   constexpr int NT = 256;
   const int64_t R = T * k, hpr = D / 16;
   int64_t grid = cdiv(T * hpr > 0 ? T * hpr : 1, NT);
   if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
-  if (x_dtype == NVFP4MOE_BF16)
-    mx_quantize_scatter_kernel<NT, true><<<(unsigned)grid, NT, 0, st>>>(
-        reinterpret_cast<const uint4*>(x), T, k, hpr, dest, offsets, E, R, reinterpret_cast<uint4*>(q), scales);
-  else
-    mx_quantize_scatter_kernel<NT, false><<<(unsigned)grid, NT, 0, st>>>(
-        reinterpret_cast<const uint4*>(x), T, k, hpr, dest, offsets, E, R, reinterpret_cast<uint4*>(q), scales);
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  const bool bf = x_dtype == NVFP4MOE_BF16;
+#define MXS(B, E4) \
+  mx_quantize_scatter_kernel<NT, B, E4><<<(unsigned)grid, NT, 0, st>>>(xv, T, k, hpr, dest, offsets, E, R, q, scales)
+  if (elem == NVFP4MOE_MX_E4M3) {
+    if (bf) MXS(true, true);
+    else MXS(false, true);
+  } else {
+    if (bf) MXS(true, false);
+    else MXS(false, false);
+  }
+#undef MXS
   return launch_status();
 }
 

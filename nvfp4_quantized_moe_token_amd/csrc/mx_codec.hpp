@@ -40,4 +40,20 @@ __device__ __forceinline__ uint32_t encode4_e4m3(const float* v, int se) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
+// 8 fp32 values to E2M1 codes (one word, element 2j in the low nibble of pair
+// j): scaled by 2^-se (exact), rounded to nearest even and saturated to 6 by
+// the hardware converter with a unit scale, sign kept.
+__device__ __forceinline__ uint32_t encode8_e2m1(const float* v, int se) {
+  uint32_t w = 0u;
+#define MXQ_PAIR(I, SEL)                                                                              \
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, __builtin_ldexpf(v[I], -se),                         \
+                                               __builtin_ldexpf(v[(I) + 1], -se), 1.0f, SEL)
+  MXQ_PAIR(0, 0);
+  MXQ_PAIR(2, 1);
+  MXQ_PAIR(4, 2);
+  MXQ_PAIR(6, 3);
+#undef MXQ_PAIR
+  return w;
+}
+
 }  // namespace nvfp4moe

@@ -751,6 +751,150 @@ __global__ __launch_bounds__(256) void unpermute_kernel(const uint8_t* __restric
   }
 }
 
+// The gradient of the weighted combine out[t] = sum_j w[t][j] * y[dest[t*k+j]]:
+//   dy[dest[t*k+j]] = w[t][j] * dout[t]     (the rows scatter_kernel writes)
+//   dw[t][j]        = <dout[t], y[dest[t*k+j]]>
+// in one pass: each dout row and each y row is read once, each dy row written
+// once, so the bound is HBM.  WPT waves share a token (a whole wave of 64
+// lanes takes 512 consecutive elements per step, 8 per lane); the k loads of a
+// step are issued before its stores, because a wave's memory counter retires
+// in order.  The k partial dot products stay in fp32 registers; their 64-lane
+// sums are taken together, halving the number of values a lane carries at
+// each exchange (7 + 3 exchanges for 8 sums instead of 48).  Assignments are
+// taken kCombineK at a time (dout is read again, from cache, for k > 8).
+constexpr int kCombineK = 8;
+
+// Sums v[0..7] over the 64 lanes; lane l returns the sum of v[l % 8].
+__device__ __forceinline__ float wave_sum8(const float (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // bit 0 of the lane picks the odd values
+    const float keep = lane & 1 ? v[2 * i + 1] : v[2 * i], give = lane & 1 ? v[2 * i] : v[2 * i + 1];
+    a[i] = keep + __shfl_xor(give, 1, 64);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = lane & 2 ? a[2 * i + 1] : a[2 * i], give = lane & 2 ? a[2 * i] : a[2 * i + 1];
+    b[i] = keep + __shfl_xor(give, 2, 64);
+  }
+  const float keep = lane & 4 ? b[1] : b[0], give = lane & 4 ? b[0] : b[1];
+  float s = keep + __shfl_xor(give, 4, 64);
+  s += __shfl_xor(s, 8, 64);
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  return s;
+}
+
+template <int IN, int Y, int OUT, int WPT, bool DY, bool DW>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(const uint8_t* __restrict__ dout,
+                                                          const uint8_t* __restrict__ y,
+                                                          const int32_t* __restrict__ dest,
+                                                          const float* __restrict__ w,
+                                                          const int32_t* __restrict__ offsets, int E, int64_t T, int k,
+                                                          int64_t D, uint8_t* __restrict__ dy, float* __restrict__ dw,
+                                                          float* __restrict__ amax_out) {
+  constexpr int ib = IN == NVFP4MOE_F32 ? 4 : 2, yb = Y == NVFP4MOE_F32 ? 4 : 2, ob = OUT == NVFP4MOE_F32 ? 4 : 2;
+  constexpr int TPB = 4 / WPT;  // tokens per workgroup of four waves
+  __shared__ float part[4][kCombineK];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, sub = wid % WPT;
+  const int64_t R = T * k;
+  float m = 0.0f;
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < T; t0 += (int64_t)gridDim.x * TPB) {
+    const int64_t t = t0 + wid / WPT;
+    if (WPT == 1 && t >= T) break;  // (WPT > 1: one token per workgroup, so t < T)
+    for (int j0 = 0; j0 < k; j0 += kCombineK) {
+      int32_t row[kCombineK];
+      float wt[kCombineK], dot[8];
+#pragma unroll
+      for (int j = 0; j < kCombineK; ++j) {
+        const int64_t a = t * k + (j0 + j < k ? j0 + j : k - 1);
+        const int32_t r = dest[a];
+        row[j] = j0 + j < k && r >= 0 && r < R ? r : -1;
+        wt[j] = w ? w[a] : 1.0f;
+        dot[j] = 0.0f;
+      }
+      for (int64_t c = (int64_t)sub * 512 + lane * 8; c < D; c += 512 * WPT) {
+        float g[8], v[DW ? kCombineK : 1][8];
+        load8<IN>(dout + (t * D + c) * ib, g);
+        if constexpr (DW) {
+#pragma unroll
+          for (int j = 0; j < kCombineK; ++j) {
+            if (row[j] >= 0) {
+              load8<Y>(y + ((int64_t)row[j] * D + c) * yb, v[j]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[j][q] = 0.0f;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kCombineK; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dot[j] = fmaf(g[q], v[j][q], dot[j]);
+        }
+        if constexpr (DY) {
+#pragma unroll
+          for (int j = 0; j < kCombineK; ++j) {
+            if (row[j] < 0) continue;
+            float o[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              o[q] = g[q] * wt[j];
+              m = fmaxf(m, fabsf(o[q]));
+            }
+            store8<OUT>(dy + ((int64_t)row[j] * D + c) * ob, o);
+          }
+        }
+      }
+      if constexpr (DW) {
+        // a dropped assignment's dot is 0 by its zero row, unless dout is not finite
+        float s = wave_sum8(dot);
+        if constexpr (WPT > 1) {
+          if (lane < kCombineK) part[wid][lane] = s;
+          __syncthreads();
+          s = part[0][lane & 7];
+#pragma unroll
+          for (int q = 1; q < WPT; ++q) s += part[q][lane & 7];
+          __syncthreads();
+        }
+        if (sub == 0 && lane < kCombineK && j0 + lane < k) {
+          const int32_t r = dest[t * k + j0 + lane];
+          dw[t * k + j0 + lane] = r >= 0 && r < R ? s : 0.0f;
+        }
+      }
+    }
+  }
+  if constexpr (DY) {
+    int64_t valid = offsets[E];
+    valid = valid < 0 ? 0 : valid > R ? R : valid;
+    const int64_t n8 = D / 8;
+    for (int64_t i = valid * n8 + blockIdx.x * 256ll + threadIdx.x; i < R * n8; i += (int64_t)gridDim.x * 256) {
+      const float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      store8<OUT>(dy + i * 8 * ob, z);
+    }
+    if (amax_out) block_atomic_max<256>(amax_out, OUT == NVFP4MOE_BF16 ? bf16_lo(pack_bf16x2(m, m)) : m);
+  }
+}
+
+template <int IN, int Y, int OUT, bool DY, bool DW>
+void launch_combine_bwd(const void* dout, const void* y, const int32_t* dest, const float* w, const int32_t* offsets,
+                        int E, int64_t T, int k, int64_t D, void* dy, float* dw, float* amax_out, hipStream_t st) {
+  // Four waves per token while one wave each would leave compute units idle
+  // (fewer than 8 waves per CU).
+  const bool split = T < (int64_t)device_cu_count() * 8;
+  int64_t grid = split ? T : cdiv(T, 4);
+  const int64_t cap = amax_out ? kAmaxGrid : kMaxStreamGrid;
+  if (grid > cap) grid = cap;
+  if (split)
+    combine_bwd_kernel<IN, Y, OUT, 4, DY, DW><<<(unsigned)grid, 256, 0, st>>>(
+        reinterpret_cast<const uint8_t*>(dout), reinterpret_cast<const uint8_t*>(y), dest, w, offsets, E, T, k, D,
+        reinterpret_cast<uint8_t*>(dy), dw, amax_out);
+  else
+    combine_bwd_kernel<IN, Y, OUT, 1, DY, DW><<<(unsigned)grid, 256, 0, st>>>(
+        reinterpret_cast<const uint8_t*>(dout), reinterpret_cast<const uint8_t*>(y), dest, w, offsets, E, T, k, D,
+        reinterpret_cast<uint8_t*>(dy), dw, amax_out);
+}
+
 }  // namespace
 }  // namespace nvfp4moe
 
@@ -955,16 +1099,18 @@ int permute_nvfp4_impl(const int32_t* topk_ids, int64_t T, int k, int E, const v
 
 }  // namespace
 
-extern "C" int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
-                              int64_t D, uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src,
-                              void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
+namespace {
+// Shared by both MX permutations: routing metadata, then the quantize-scatter.
+int permute_mx_impl(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D, int elem,
+                    uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
+                    size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
   if (T < 0 || k < 1 || E < 1 || D < 0) return NVFP4MOE_EINVAL;
   if (x_dtype != NVFP4MOE_BF16 && x_dtype != NVFP4MOE_F32) return NVFP4MOE_EINVAL;
   if (E > kMaxExperts || k > 64) return NVFP4MOE_ESHAPE;
   if (!offsets || (T > 0 && (!topk_ids || !dest || !src))) return NVFP4MOE_EINVAL;
   if (T > 0 && D > 0 && (!x || !q || !scales)) return NVFP4MOE_EINVAL;
   if (D % 32 != 0) return NVFP4MOE_ESHAPE;
-  if (T > 0 && D > 0 && (!aligned(x, 16) || !aligned(q, 16))) return NVFP4MOE_ESHAPE;
+  if (T > 0 && D > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E4M3 ? 16 : 8))) return NVFP4MOE_ESHAPE;
   const int64_t R = T * k;
   if (R > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
   if (ws_bytes < moe_permute_workspace_size(T, k, E) || (R > 0 && !workspace)) return NVFP4MOE_EWORKSPACE;
@@ -978,7 +1124,68 @@ extern "C" int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, 
   const int rc = launch_metadata(topk_ids, R, E, nullptr, workspace, offsets, dest, src, status, st);
   if (rc != NVFP4MOE_OK) return rc;
   if (D == 0) return NVFP4MOE_OK;
-  return mx_quantize_scatter_launch(x, x_dtype, T, k, D, dest, offsets, E, q, scales, st);
+  return mx_quantize_scatter_launch(x, x_dtype, T, k, D, elem, dest, offsets, E, q, scales, st);
+}
+}  // namespace
+
+extern "C" int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
+                              int64_t D, uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src,
+                              void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
+  return permute_mx_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E4M3, q, scales, offsets, dest, src, workspace,
+                         ws_bytes, status, stream);
+}
+
+extern "C" int moe_permute_mxfp4(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
+                                 int64_t D, uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src,
+                                 void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
+  return permute_mx_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E2M1, q, scales, offsets, dest, src, workspace,
+                         ws_bytes, status, stream);
+}
+
+extern "C" int moe_unpermute_bwd(const void* dout, int dout_dtype, const void* y_perm, int y_dtype,
+                                 const int32_t* dest, const float* topk_w, const int32_t* offsets, int E, int64_t T,
+                                 int k, int64_t D, void* dy_perm, int dy_dtype, float* d_topk_w, float* amax_out,
+                                 nvfp4moe_stream_t stream) {
+  const auto is_float = [](int d) { return d == NVFP4MOE_F32 || d == NVFP4MOE_BF16; };
+  if (T < 0 || k < 1 || E < 1 || D < 0) return NVFP4MOE_EINVAL;
+  if (!is_float(dout_dtype) || (d_topk_w && !is_float(y_dtype)) || (dy_perm && !is_float(dy_dtype)))
+    return NVFP4MOE_EINVAL;
+  // (empty tensors may come as NULL)
+  if (T > 0 && D > 0 && ((!dy_perm && !d_topk_w) || (amax_out && !dy_perm))) return NVFP4MOE_EINVAL;
+  if (T > 0 && (!dest || (dy_perm && !offsets) || (D > 0 && (!dout || (d_topk_w && !y_perm)))))
+    return NVFP4MOE_EINVAL;
+  if (k > 64 || D % 8 != 0 || T * k > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
+  if (!aligned(dout, 16) || !aligned(y_perm, 16) || !aligned(dy_perm, 16) || !aligned(dest, 4) ||
+      !aligned(topk_w, 4) || !aligned(offsets, 4) || !aligned(d_topk_w, 4) || !aligned(amax_out, 4))
+    return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  hipStream_t st = as_stream(stream);
+  if (amax_out) fill_u32_kernel<<<1, 64, 0, st>>>(reinterpret_cast<uint32_t*>(amax_out), 0u, 1);
+  if (T == 0 || (!dy_perm && !d_topk_w)) return launch_status();
+#define NVC(I, Y, O)                                                                                             \
+  if (dout_dtype == I && (!d_topk_w || y_dtype == Y) && (!dy_perm || dy_dtype == O)) {                           \
+    if (dy_perm && d_topk_w)                                                                                     \
+      launch_combine_bwd<I, Y, O, true, true>(dout, y_perm, dest, topk_w, offsets, E, T, k, D, dy_perm,          \
+                                              d_topk_w, amax_out, st);                                           \
+    else if (dy_perm)                                                                                            \
+      launch_combine_bwd<I, NVFP4MOE_BF16, O, true, false>(dout, nullptr, dest, topk_w, offsets, E, T, k, D,     \
+                                                           dy_perm, nullptr, amax_out, st);                      \
+    else                                                                                                         \
+      launch_combine_bwd<I, Y, NVFP4MOE_BF16, false, true>(dout, y_perm, dest, topk_w, nullptr, E, T, k, D,      \
+                                                           nullptr, d_topk_w, nullptr, st);                      \
+    return launch_status();                                                                                      \
+  }
+  NVC(NVFP4MOE_BF16, NVFP4MOE_BF16, NVFP4MOE_BF16)
+  NVC(NVFP4MOE_BF16, NVFP4MOE_BF16, NVFP4MOE_F32)
+  NVC(NVFP4MOE_BF16, NVFP4MOE_F32, NVFP4MOE_BF16)
+  NVC(NVFP4MOE_BF16, NVFP4MOE_F32, NVFP4MOE_F32)
+  NVC(NVFP4MOE_F32, NVFP4MOE_BF16, NVFP4MOE_BF16)
+  NVC(NVFP4MOE_F32, NVFP4MOE_BF16, NVFP4MOE_F32)
+  NVC(NVFP4MOE_F32, NVFP4MOE_F32, NVFP4MOE_BF16)
+  NVC(NVFP4MOE_F32, NVFP4MOE_F32, NVFP4MOE_F32)
+#undef NVC
+  return NVFP4MOE_EINVAL;
 }
 
 extern "C" int moe_permute_nvfp4(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int64_t D,

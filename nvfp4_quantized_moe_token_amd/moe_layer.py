@@ -26,11 +26,17 @@ row):
   mx_quantize(X, E4M3)  ->  moe_permute (metadata + gather of the code rows)
   + moe_gather (scale rows)  ->  grouped_gemm_w4a8_silu_gate  ->
   mx_quantize(H, E4M3)  ->  grouped_gemm_w4a8 (down)  ->  moe_unpermute.
+MXFP4 forward (both operands in the 4-bit format that gfx950 multiplies as
+stored):
+  moe_permute_mxfp4  ->  grouped_gemm_mxfp4_silu_gate (H quantized in its
+  epilogue)  ->  grouped_gemm_mxfp4 (down)  ->  moe_unpermute.
+``Learner`` is the layer as a learner trains it: router, MXFP4 forward, BF16
+backward down to the router's weights, AdamW.
 """
 
 import torch
 
-from . import ops
+from . import ops, optim
 
 
 def quantize_expert_weights(w):
@@ -110,7 +116,7 @@ def forward(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep_y1=True, keep_x_perm=Tr
     return meta
 
 
-def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None):
+def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None, d_topk_w=None):
     """BF16 backward of ``forward`` (weight gradients in fp32).  Each
     elementwise consumer runs right after its producer, before a weight-
     gradient GEMM streams its fp32 output through the caches.  With ``x``
@@ -121,7 +127,11 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None):
     With ``wgrad_stream`` (a torch stream) the two weight-gradient GEMMs run
     there, each after the op whose output it reads, overlapping the rest of
     the backward; the current stream waits for them before returning, so the
-    caller's next step cannot overwrite their inputs early."""
+    caller's next step cannot overwrite their inputs early.
+
+    With ``d_topk_w`` (fp32 [T, k]) the gradient of the routing weights is
+    written there, in the pass that scatters dY (moe_unpermute_bwd; buf.y2
+    must still hold the forward's)."""
     main = torch.cuda.current_stream()
     off = meta["offsets"]
 
@@ -141,7 +151,10 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None):
         with torch.cuda.stream(wgrad_stream):
             tn(a, b, out, gather)
 
-    ops.moe_scatter(dy, meta["dest"], meta["offsets"], buf.k, topk_w=topk_w, out=buf.dy2)
+    if d_topk_w is not None:
+        ops.moe_unpermute_bwd(dy, buf.y2, meta["dest"], off, buf.k, topk_w=topk_w, dy_perm=buf.dy2, d_topk_w=d_topk_w)
+    else:
+        ops.moe_scatter(dy, meta["dest"], meta["offsets"], buf.k, topk_w=topk_w, out=buf.dy2)
     if wgrad_stream is not None:
         wgrad(buf.dy2, buf.h, buf.dw_dn)
     ops.grouped_gemm_bf16(ops.NN, buf.dy2, w_dn, off, out=buf.dh)
@@ -160,11 +173,13 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None):
         main.wait_event(done)
 
 
-def quantize_expert_weights_mx(w):
+def quantize_expert_weights_mx(w, out=None):
     """MXFP4 weights of stacked experts [E, N, K] (E8M0 scale per 32 along
-    K; no per-expert scale).  Once per optimizer step."""
+    K; no per-expert scale), into ``out`` (an earlier result) when given.
+    Once per optimizer step."""
     E, N, K = w.shape
-    q, sc = ops.mx_quantize(w.reshape(E * N, K), ops.MX_E2M1)
+    into = {} if out is None else dict(q=out["q"].view(E * N, K // 2), scales=out["s"].view(E * N, K // 32))
+    q, sc = ops.mx_quantize(w.reshape(E * N, K), ops.MX_E2M1, **into)
     return dict(q=q.view(E, N, K // 2), s=sc.view(E, N, K // 32))
 
 
@@ -225,18 +240,23 @@ class NVFP4BackwardBuffers:
         self.c_x = (e(D, Kp // 2), e(D, Kp // 16), e(1, dt=f32))
 
 
-def backward_nvfp4(dy, topk_w, wt_gu, wt_dn, meta, buf, nb, amax_x=None):
+def backward_nvfp4(dy, topk_w, wt_gu, wt_dn, meta, buf, nb, amax_x=None, d_topk_w=None):
     """The NVFP4 backward variant of ``backward``: the same dataflow with the
     four grouped GEMMs in W4A4.  Each gradient's amax comes out of the kernel
     that writes the gradient (the weighted scatter for dY2, the SiLU backward
     for dY1) and is reused by its row-wise and column-wise quantizations; H
     and X_perm reuse the forward's amaxes (buf.amax, or ``amax_x`` when the
     forward was given a fixed one).  wt_gu / wt_dn: quantize_expert_weights_t
-    of the bf16 weights.  Weight gradients fp32, activation gradients bf16."""
+    of the bf16 weights.  Weight gradients fp32, activation gradients bf16.
+    ``d_topk_w``: as in ``backward``."""
     off = meta["offsets"]
     R = buf.T * buf.k
     amax_x = buf.amax[0:1] if amax_x is None else amax_x
-    ops.moe_scatter(dy, meta["dest"], off, buf.k, topk_w=topk_w, out=buf.dy2, amax_out=nb.amax[0:1])
+    if d_topk_w is not None:
+        ops.moe_unpermute_bwd(dy, buf.y2, meta["dest"], off, buf.k, topk_w=topk_w, dy_perm=buf.dy2, d_topk_w=d_topk_w,
+                              amax_out=nb.amax[0:1])
+    else:
+        ops.moe_scatter(dy, meta["dest"], off, buf.k, topk_w=topk_w, out=buf.dy2, amax_out=nb.amax[0:1])
     q, sc, g = nb.a_dy2
     ops.nvfp4_quantize(buf.dy2, amax_in=nb.amax[0:1], q=q, scales=sc, gscale=g)
     ops.grouped_gemm_w4a4(q, sc, g, wt_dn["q"], wt_dn["s"], wt_dn["g"], off, out=buf.dh)
@@ -253,3 +273,98 @@ def backward_nvfp4(dy, topk_w, wt_gu, wt_dn, meta, buf, nb, amax_x=None):
                                gscale=nb.c_dy1[2])
     ops.nvfp4_quantize_colwise(buf.x_perm, off, amax_x, Kp=nb.Kp, q_t=nb.c_x[0], s_t=nb.c_x[1], gscale=nb.c_x[2])
     ops.grouped_gemm_w4a4_wgrad(nb.c_dy1, nb.c_x, off, R, out=buf.dw_gu)
+
+
+class BuffersMXFP4:
+    """Device buffers of one MXFP4 forward step, allocated once and reused;
+    with ``backward`` also those of ``backward`` (dx in ``dx_dtype``)."""
+
+    def __init__(self, T, k, E, D, F, device, backward=False, dx_dtype=torch.bfloat16):
+        R = T * k
+        bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+        e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        self.T, self.k, self.E, self.D, self.F = T, k, E, D, F
+        self.ws = e(max(ops.moe_permute_workspace_size(T, k, E), 1), dt=u8)
+        self.a1_q, self.a1_s = e(R, D // 2, dt=u8), e(R, D // 32, dt=u8)
+        self.a2_q, self.a2_s = e(R, F // 2, dt=u8), e(R, F // 32, dt=u8)
+        self.y2 = e(R, D)
+        self.out = e(T, D)
+        if backward:
+            self.y1, self.h = e(R, 2 * F), e(R, F)
+            self.dy2, self.dh, self.dy1, self.dx_perm = e(R, D), e(R, F), e(R, 2 * F), e(R, D)
+            self.dx = e(T, D, dt=dx_dtype)
+            self.dw_dn, self.dw_gu = e(E, D, F, dt=f32), e(E, 2 * F, D, dt=f32)
+
+
+def forward_mxfp4(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep=False):
+    """MXFP4 MoE forward (weights from quantize_expert_weights_mx); returns
+    the routing metadata dict.  X is quantized inside the permutation and H
+    inside the gate+up epilogue.  ``keep``: bf16 Y1 and H are stored too
+    (buf.y1, buf.h), for ``backward``, which then gathers its activation rows
+    from x."""
+    meta = ops.moe_permute_mxfp4(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
+    ops.grouped_gemm_mxfp4_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"],
+                                     y1=buf.y1 if keep else None, want_y1=keep, h=buf.h if keep else None,
+                                     want_h=keep, q_h=buf.a2_q, s_h=buf.a2_s)
+    ops.grouped_gemm_mxfp4(buf.a2_q, buf.a2_s, wq_dn["q"], wq_dn["s"], meta["offsets"], out=buf.y2)
+    ops.moe_unpermute(buf.y2, meta["dest"], buf.T, buf.k, topk_w=topk_w, out=buf.out)
+    return meta
+
+
+class Learner:
+    """One MoE layer trained in MXFP4: fp32 master weights with bf16 and
+    MXFP4 copies, ``forward``, ``backward`` (to the input, the experts' and
+    the router's weights) and ``update`` (one AdamW step, copies renewed).
+
+    w_r [E, D], w_gu [E, 2F, D], w_dn [E, D, F]: fp32 master weights on the
+    GPU, updated in place.  T: tokens per step.  E, D % 32 == 0 (the router's
+    GEMM), D, F % 128 == 0.  ``adamw``: keyword arguments of optim.AdamW."""
+
+    def __init__(self, w_r, w_gu, w_dn, T, k, router_bias=None, score=ops.ROUTER_TOPK_SOFTMAX, **adamw):
+        E, D = w_r.shape
+        F = w_dn.shape[2]
+        dev = w_r.device
+        self.k, self.score, self.router_bias = k, score, router_bias
+        self.master = [w_r, w_gu, w_dn]
+        self.w_r, self.w_gu, self.w_dn = self.copies = [w.to(torch.bfloat16) for w in self.master]
+        self.buf = BuffersMXFP4(T, k, E, D, F, dev, backward=True, dx_dtype=torch.float32)
+        e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        self.logits, self.d_logits = e(T, E), e(T, E, dt=torch.bfloat16)
+        self.topk_ids, self.topk_w, self.d_topk_w = e(T, k, dt=torch.int32), e(T, k), e(T, k)
+        self.lse, self.prob_sum = e(T), e(E)
+        self.router_ws = e(max(ops._lib.load().moe_router_workspace_size(T, E, k), 1), dt=torch.uint8)
+        self.dw_r = e(1, E, D)
+        self.one_group = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        self.opt = optim.AdamW(self.master, params_bf16=self.copies, **adamw)
+        self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
+
+    def forward(self, x):
+        """The layer's output [T, D] (bf16) for x [T, D] bf16; the router's
+        lse and prob_sum stay in ``lse`` and ``prob_sum`` for its losses."""
+        self.x = x
+        ops.grouped_gemm_bf16(ops.NT, x, self.w_r.unsqueeze(0), self.one_group, out=self.logits)
+        ops.moe_router(self.logits, self.k, bias=self.router_bias, score=self.score, topk_ids=self.topk_ids,
+                       topk_w=self.topk_w, lse=self.lse, prob_sum=self.prob_sum, workspace=self.router_ws)
+        self.meta = forward_mxfp4(x, self.topk_ids, self.topk_w, self.wq_gu, self.wq_dn, self.buf, keep=True)
+        return self.buf.out
+
+    def backward(self, dy, d_lse=None, d_prob_sum=None):
+        """Gradient of the input (fp32 [T, D]) for dy [T, D] bf16 and the
+        gradients of the router's losses; the weights' gradients stay in
+        ``grads()``."""
+        b = self.buf
+        backward(dy, self.topk_w, self.w_gu, self.w_dn, self.meta, b, x=self.x, d_topk_w=self.d_topk_w)
+        ops.moe_router_bwd(self.logits, self.topk_ids, self.d_topk_w, score=self.score, lse=self.lse, d_lse=d_lse,
+                           d_prob_sum=d_prob_sum, out=self.d_logits)
+        ops.grouped_gemm_bf16(ops.TN, self.d_logits, self.x, self.one_group, out=self.dw_r)
+        ops.grouped_gemm_bf16(ops.NN, self.d_logits, self.w_r.unsqueeze(0), self.one_group, out=b.dx, accumulate=True)
+        return b.dx
+
+    def grads(self):
+        return [self.dw_r[0], self.buf.dw_gu, self.buf.dw_dn]
+
+    def update(self, grad_scale=None, skip=None):
+        """One optimizer step; the bf16 and MXFP4 weights follow."""
+        self.opt.step(self.grads(), grad_scale=grad_scale, skip=skip)
+        quantize_expert_weights_mx(self.w_gu, out=self.wq_gu)
+        quantize_expert_weights_mx(self.w_dn, out=self.wq_dn)

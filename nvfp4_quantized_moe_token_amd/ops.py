@@ -6,6 +6,8 @@ the computation runs in the library's HIP kernels.  Argument marshalling
 only: no arithmetic happens in Python.
 """
 
+import contextlib
+
 import torch
 
 from . import _lib
@@ -45,6 +47,31 @@ def _dev(*ts):
                 raise ValueError("nvfp4moe ops take contiguous tensors")
 
 
+def _need(t, name, dtype, *shape):
+    """Checks one argument: dtype (or one of several) and shape (None: any extent)."""
+    if t is None:
+        return
+    if t.dtype != dtype if isinstance(dtype, torch.dtype) else t.dtype not in dtype:
+        raise ValueError("%s: dtype %s is not supported" % (name, t.dtype))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _on_device(*ts):
+    """Checks that the tensors are contiguous and share one GPU, and returns a
+    context in which that GPU is the current one (its current stream is then
+    the one the library is given)."""
+    _dev(*ts)
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) != 1:
+        raise ValueError("nvfp4moe ops take tensors of one GPU, got %s" % sorted(map(str, devs)))
+    dev = devs.pop()
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
 def nvfp4_quantize(x, groups=1, amax_in=None, amax_out=None, q=None, scales=None, gscale=None):
     """NVFP4-quantize a [rows, K] fp32/bf16 tensor.  Returns (q, scales,
     gscale, amax) where amax is amax_in when given, else the computed one."""
@@ -82,6 +109,67 @@ def nvfp4_quantize_onepass(x, groups=1, amax_out=None, q=None, scales=None, gsca
                                     _ptr(gscale), _ptr(workspace), workspace.numel(), _stream())
     _check("nvfp4_quantize_onepass", rc)
     return q, scales, gscale, amax_out
+
+
+ROUTER_TOPK_SOFTMAX, ROUTER_SOFTMAX = _lib.ROUTER_TOPK_SOFTMAX, _lib.ROUTER_SOFTMAX
+
+
+def moe_router(logits, k, bias=None, score=ROUTER_TOPK_SOFTMAX, scale=1.0, want_lse=False, want_prob_sum=False,
+               topk_ids=None, topk_w=None, lse=None, prob_sum=None, workspace=None):
+    """Top-k experts of logits [T, E] (fp32 or bf16; plus the fp32 selection
+    bias [E]) and their softmax weights.  Returns a dict with topk_ids [T, k]
+    int32, topk_w [T, k] fp32, lse [T] and prob_sum [E] (None unless wanted
+    or given)."""
+    _need(logits, "logits", _FLOATS, None, None)
+    T, E = logits.shape
+    _need(bias, "bias", torch.float32, E)
+    _need(topk_ids, "topk_ids", torch.int32, T, k)
+    _need(topk_w, "topk_w", torch.float32, T, k)
+    _need(lse, "lse", torch.float32, T)
+    _need(prob_sum, "prob_sum", torch.float32, E)
+    with _on_device(logits, bias, topk_ids, topk_w, lse, prob_sum, workspace):
+        dev, f32 = logits.device, torch.float32
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
+        topk_w = torch.empty((T, k), dtype=f32, device=dev) if topk_w is None else topk_w
+        if lse is None and want_lse:
+            lse = torch.empty((T,), dtype=f32, device=dev)
+        if prob_sum is None and want_prob_sum:
+            prob_sum = torch.empty((E,), dtype=f32, device=dev)
+        lib = _lib.load()
+        ws_bytes = 0
+        if prob_sum is not None:
+            if workspace is None:
+                workspace = torch.empty((lib.moe_router_workspace_size(T, E, k),), dtype=torch.uint8, device=dev)
+            ws_bytes = workspace.numel() * workspace.element_size()
+        rc = lib.moe_router(_ptr(logits), _DT[logits.dtype], T, E, k, _ptr(bias), score, scale, _ptr(topk_ids),
+                            _ptr(topk_w), _ptr(lse), _ptr(prob_sum), _ptr(workspace), ws_bytes, _stream())
+    _check("moe_router", rc)
+    return dict(topk_ids=topk_ids, topk_w=topk_w, lse=lse, prob_sum=prob_sum)
+
+
+def moe_router_bwd(logits, topk_ids, d_topk_w, score=ROUTER_TOPK_SOFTMAX, scale=1.0, lse=None, d_lse=None,
+                   d_prob_sum=None, out=None, out_dtype=None):
+    """Gradient of moe_router's topk_w, lse and prob_sum with respect to the
+    logits (d_topk_w, d_lse, d_prob_sum: None for zeros).  Returns d_logits
+    [T, E] of out_dtype (default: the logits' dtype)."""
+    _need(logits, "logits", _FLOATS, None, None)
+    T, E = logits.shape
+    _need(topk_ids, "topk_ids", torch.int32, T, None)
+    k = topk_ids.shape[1]
+    _need(d_topk_w, "d_topk_w", torch.float32, T, k)
+    _need(lse, "lse", torch.float32, T)
+    _need(d_lse, "d_lse", torch.float32, T)
+    _need(d_prob_sum, "d_prob_sum", torch.float32, E)
+    _need(out, "out", _FLOATS, T, E)
+    with _on_device(logits, topk_ids, d_topk_w, lse, d_lse, d_prob_sum, out):
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype if out_dtype is None else out_dtype, device=logits.device)
+        rc = _lib.load().moe_router_bwd(_ptr(logits), _DT[logits.dtype], T, E, k, _ptr(topk_ids), score, scale,
+                                        _ptr(d_topk_w), _ptr(lse), _ptr(d_lse), _ptr(d_prob_sum), _ptr(out),
+                                        _DT[out.dtype], _stream())
+    _check("moe_router_bwd", rc)
+    return out
+
 
 def moe_permute_workspace_size(T, k, E):
     return _lib.load().moe_permute_workspace_size(T, k, E)
@@ -142,6 +230,34 @@ def moe_permute_mx(topk_ids, num_experts, x, q=None, scales=None, status=None, w
                             _stream())
     _check("moe_permute_mx", rc)
     return dict(offsets=offsets, dest=dest, src=src, q=q, scales=scales)
+
+
+def moe_permute_mxfp4(topk_ids, num_experts, x, q=None, scales=None, status=None, workspace=None):
+    """moe_permute fused with the MXFP4 (E2M1) quantization of the permuted
+    rows: codes [T*k, D/2] and E8M0 scales [T*k, D/32].  Returns a dict with
+    offsets, dest, src, q and scales."""
+    _need(topk_ids, "topk_ids", torch.int32, None, None)
+    T, k = topk_ids.shape
+    _need(x, "x", _FLOATS, T, None)
+    D, R = x.shape[1], T * k
+    _need(q, "q", torch.uint8, R, D // 2)
+    _need(scales, "scales", torch.uint8, R, D // 32)
+    with _on_device(topk_ids, x, q, scales, status, workspace):
+        dev, i32, u8 = x.device, torch.int32, torch.uint8
+        lib = _lib.load()
+        offsets = torch.empty((num_experts + 1,), dtype=i32, device=dev)
+        dest = torch.empty((R,), dtype=i32, device=dev)
+        src = torch.empty((R,), dtype=i32, device=dev)
+        q = torch.empty((R, D // 2), dtype=u8, device=dev) if q is None else q
+        scales = torch.empty((R, D // 32), dtype=u8, device=dev) if scales is None else scales
+        if workspace is None:
+            workspace = torch.empty((max(lib.moe_permute_workspace_size(T, k, num_experts), 1),), dtype=u8, device=dev)
+        rc = lib.moe_permute_mxfp4(_ptr(topk_ids), T, k, num_experts, _ptr(x), _DT[x.dtype], D, _ptr(q),
+                                   _ptr(scales), _ptr(offsets), _ptr(dest), _ptr(src), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(status), _stream())
+    _check("moe_permute_mxfp4", rc)
+    return dict(offsets=offsets, dest=dest, src=src, q=q, scales=scales)
+
 
 def moe_permute_nvfp4(topk_ids, num_experts, x, x_perm=None, want_x_perm=True, amax_in=None, amax_out=None,
                       q=None, scales=None, gscale=None, status=None, workspace=None):
@@ -247,6 +363,40 @@ def moe_unpermute(y_perm, dest, T, k, topk_w=None, out=None, out_dtype=torch.bfl
                                    _DT[out.dtype], _stream())
     _check("moe_unpermute", rc)
     return out
+
+
+def moe_unpermute_bwd(dout, y_perm, dest, offsets, k, topk_w=None, dy_perm=None, want_dy=True, dy_dtype=None,
+                      d_topk_w=None, want_dw=True, amax_out=None):
+    """Gradient of moe_unpermute in one pass: dy_perm[dest[t*k+j]] = w[t, j] *
+    dout[t] (rows past offsets[E] are zeros) and d_topk_w[t, j] =
+    <dout[t], y_perm[dest[t*k+j]]> (fp32).  y_perm may be None without the
+    weight gradient.  amax_out (fp32 [1], optional) receives max |dy_perm|.
+    Returns (dy_perm or None, d_topk_w or None)."""
+    _need(dout, "dout", _FLOATS, None, None)
+    T, D = dout.shape
+    R = T * k
+    want_dw = want_dw or d_topk_w is not None
+    want_dy = want_dy or dy_perm is not None
+    if want_dw and y_perm is None:
+        raise ValueError("the weight gradient needs y_perm")
+    _need(y_perm, "y_perm", _FLOATS, R, D)
+    _need(dest, "dest", torch.int32, R)
+    _need(offsets, "offsets", torch.int32, None)
+    _need(topk_w, "topk_w", torch.float32, T, k)
+    _need(dy_perm, "dy_perm", _FLOATS, R, D)
+    _need(d_topk_w, "d_topk_w", torch.float32, T, k)
+    _need(amax_out, "amax_out", torch.float32, 1)
+    with _on_device(dout, y_perm, dest, offsets, topk_w, dy_perm, d_topk_w, amax_out):
+        if dy_perm is None and want_dy:
+            dy_perm = torch.empty((R, D), dtype=dout.dtype if dy_dtype is None else dy_dtype, device=dout.device)
+        if d_topk_w is None and want_dw:
+            d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+        rc = _lib.load().moe_unpermute_bwd(
+            _ptr(dout), _DT[dout.dtype], _ptr(y_perm), _DT[y_perm.dtype] if y_perm is not None else BF16, _ptr(dest),
+            _ptr(topk_w), _ptr(offsets), offsets.numel() - 1, T, k, D, _ptr(dy_perm),
+            _DT[dy_perm.dtype] if dy_perm is not None else BF16, _ptr(d_topk_w), _ptr(amax_out), _stream())
+    _check("moe_unpermute_bwd", rc)
+    return dy_perm, d_topk_w
 
 
 def grouped_gemm_w4a4(a_q, a_s, a_g, b_q, b_s, b_g, offsets, out=None, out_dtype=torch.float32):
@@ -448,6 +598,61 @@ def grouped_gemm_w4a8_silu_gate_mx(a_q, a_s, b_q, b_s, offsets, q_h=None, s_h=No
                                                     _stream())
     _check("grouped_gemm_w4a8_silu_gate_mx", rc)
     return q_h, s_h
+
+
+def _mxfp4_operands(a_q, a_s, b_q, b_s, offsets):
+    _need(a_q, "a_q", torch.uint8, None, None)
+    M, K = a_q.shape[0], a_q.shape[1] * 2
+    _need(a_s, "a_s", torch.uint8, M, K // 32)
+    _need(b_q, "b_q", torch.uint8, None, None, K // 2)
+    E, N = b_q.shape[0], b_q.shape[1]
+    _need(b_s, "b_s", torch.uint8, E, N, K // 32)
+    _need(offsets, "offsets", torch.int32, E + 1)
+    return M, K, E, N
+
+
+def grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets, out=None, out_dtype=torch.float32):
+    """C[r] = deq(A)[r] . deq(B_e)^T for rows r of expert e; A MXFP4
+    [M, K/2], B MXFP4 [E, N, K/2], E8M0 scales per 32."""
+    M, K, E, N = _mxfp4_operands(a_q, a_s, b_q, b_s, offsets)
+    _need(out, "out", _FLOATS, M, N)
+    with _on_device(a_q, a_s, b_q, b_s, offsets, out):
+        out = torch.empty((M, N), dtype=out_dtype, device=a_q.device) if out is None else out
+        rc = _lib.load().grouped_gemm_mxfp4(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M, N, K,
+                                            _ptr(out), _DT[out.dtype], _stream())
+    _check("grouped_gemm_mxfp4", rc)
+    return out
+
+
+def grouped_gemm_mxfp4_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=True, h=None, want_h=True,
+                                 amax_out=None, q_h=None, s_h=None, want_q=False):
+    """Gate+up MXFP4 GEMM (B_e = [gate; up] rows) with the SiLU gate and,
+    when wanted, the MXFP4 quantization of H in its epilogue.  Returns a dict
+    with y1 [M, 2F] and h [M, F] (bf16), q_h [M, F/2] and s_h [M, F/32] (None
+    unless wanted or given).  amax_out (fp32 [1], optional) receives max |H|."""
+    M, K, E, N = _mxfp4_operands(a_q, a_s, b_q, b_s, offsets)
+    if N % 2:
+        raise ValueError("b_q: gate and up rows, an even number")
+    F = N // 2
+    bf, u8 = torch.bfloat16, torch.uint8
+    _need(y1, "y1", bf, M, N)
+    _need(h, "h", bf, M, F)
+    _need(amax_out, "amax_out", torch.float32, 1)
+    _need(q_h, "q_h", u8, M, F // 2)
+    _need(s_h, "s_h", u8, M, F // 32)
+    want_q = want_q or q_h is not None or s_h is not None
+    with _on_device(a_q, a_s, b_q, b_s, offsets, y1, h, amax_out, q_h, s_h):
+        dev = a_q.device
+        y1 = torch.empty((M, N), dtype=bf, device=dev) if y1 is None and want_y1 else y1
+        h = torch.empty((M, F), dtype=bf, device=dev) if h is None and want_h else h
+        if want_q:
+            q_h = torch.empty((M, F // 2), dtype=u8, device=dev) if q_h is None else q_h
+            s_h = torch.empty((M, F // 32), dtype=u8, device=dev) if s_h is None else s_h
+        rc = _lib.load().grouped_gemm_mxfp4_silu_gate(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M,
+                                                      F, K, _ptr(y1), _ptr(h), _ptr(amax_out), _ptr(q_h), _ptr(s_h),
+                                                      _stream())
+    _check("grouped_gemm_mxfp4_silu_gate", rc)
+    return dict(y1=y1, h=h, q_h=q_h, s_h=s_h)
 
 
 def grouped_gemm_bf16(layout, a, b, offsets, num_experts=None, out=None, out_dtype=torch.float32, accumulate=False):

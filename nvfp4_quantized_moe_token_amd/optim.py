@@ -1,0 +1,134 @@
+"""AdamW for the learner's weights on the library's adamw_step: one launch for
+up to 48 tensors, moments in fp32 or in 8 bits.
+
+The class owns the moments and the list of pointers that the C entry point
+takes; every step of the arithmetic runs in the HIP kernel.
+"""
+
+import ctypes
+
+import torch
+
+from . import _lib
+from .ops import _DT, _check, _on_device, _ptr, _stream
+
+BLOCK = _lib.ADAMW_BLOCK
+
+
+class AdamW:
+    """AdamW (decoupled weight decay) over a list of contiguous parameters of
+    one dtype (fp32, or bf16 rounded stochastically) on one GPU.
+
+    params_bf16: for each fp32 parameter a bf16 tensor that every step
+    overwrites with its rounded value (or None, for all or for one).
+    state_bits: 32, or 8 (codes with one fp32 scale per 256 elements, rounded
+    stochastically).  seed: of that rounding.  step: steps already taken.
+    state: moments to go on with, a dict of lists: exp_avg, exp_avg_sq, and
+    for 8 bits avg_scale, avg_sq_scale (kept, not copied); zeros otherwise.
+    capturable: the step count and the learning rate live on the device
+    (``step_dev`` int64 [1], ``lr_dev`` fp32 [1]), so a captured step counts
+    on at every replay.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params_bf16=None,
+                 state_bits=32, seed=0, step=0, state=None, capturable=False):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW needs at least one parameter")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits: 8 or 32, got %r" % (state_bits,))
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits, self.seed, self.steps = state_bits, seed & 0xFFFFFFFF, step
+        n = len(self.params)
+        dt = self.params[0].dtype
+        if dt not in (torch.float32, torch.bfloat16) or any(p.dtype != dt for p in self.params):
+            raise ValueError("AdamW takes parameters of one dtype, fp32 or bf16")
+        self.params_bf16 = [None] * n if params_bf16 is None else list(params_bf16)
+        self._same_sizes("params_bf16", self.params_bf16, torch.bfloat16)
+        if dt != torch.float32 and any(c is not None for c in self.params_bf16):
+            raise ValueError("params_bf16 goes with fp32 parameters")
+        if state is None:
+            state = self._new_state()
+        names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
+        self.state = {k: list(state[k]) for k in names}
+        for k in names[:2]:
+            self._same_sizes(k, self.state[k], torch.uint8 if state_bits == 8 else torch.float32, required=True)
+        for k in names[2:]:
+            self._same_sizes(k, self.state[k], torch.float32, required=True, blocks=True)
+        tensors = self.params + self.params_bf16 + [t for k in names for t in self.state[k]]
+        _on_device(*tensors)
+        dev = self.params[0].device
+        self.step_dev = torch.full((1,), step, dtype=torch.int64, device=dev) if capturable else None
+        self.lr_dev = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
+        self._list = (_lib.AdamWTensor * n)()
+        for i, (d, p, c) in enumerate(zip(self._list, self.params, self.params_bf16)):
+            d.param, d.param_bf16, d.n = _ptr(p), _ptr(c), p.numel()
+            for k in names:
+                setattr(d, k, _ptr(self.state[k][i]))
+
+    def _same_sizes(self, name, ts, dtype, required=False, blocks=False):
+        if len(ts) != len(self.params):
+            raise ValueError("%s: %d tensors for %d parameters" % (name, len(ts), len(self.params)))
+        for p, t in zip(self.params, ts):
+            if t is None and not required:
+                continue
+            if t is None or t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+                raise ValueError("%s: %s tensors expected" % (name, dtype))
+            if t.numel() != (-(-p.numel() // BLOCK) if blocks else p.numel()):
+                raise ValueError("%s: %d elements for a parameter of %d" % (name, t.numel(), p.numel()))
+
+    def _new_state(self):
+        def z(dtype, blocks=False):
+            return [torch.zeros((-(-p.numel() // BLOCK),) if blocks else p.shape, dtype=dtype, device=p.device)
+                    for p in self.params]
+
+        if self.state_bits == 32:
+            return dict(exp_avg=z(torch.float32), exp_avg_sq=z(torch.float32))
+        return dict(exp_avg=z(torch.uint8), exp_avg_sq=z(torch.uint8), avg_scale=z(torch.float32, True),
+                    avg_sq_scale=z(torch.float32, True))
+
+    def step(self, grads, grad_scale=None, skip=None):
+        """One step with one gradient per parameter (fp32 or bf16, all the
+        same).  grad_scale (fp32 [1], device): a factor on every gradient.
+        skip (int32 [1], device): nothing changes when it is not 0 (the step
+        still counts)."""
+        grads = list(grads)
+        self._same_sizes("grads", grads, (torch.float32, torch.bfloat16), required=True)
+        if any(g.dtype != grads[0].dtype for g in grads):
+            raise ValueError("grads: one dtype for all")
+        for name, t, dt in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
+            if t is not None and (t.dtype != dt or t.numel() != 1):
+                raise ValueError("%s: one %s on the GPU" % (name, dt))
+        with _on_device(self.params[0], grad_scale, skip, *grads):
+            self.steps += 1
+            if self.step_dev is not None:
+                self.step_dev.add_(1)
+            for d, g in zip(self._list, grads):
+                d.grad = g.data_ptr()
+            rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[grads[0].dtype],
+                                        self.state_bits, self.lr, self.betas[0], self.betas[1], self.eps,
+                                        self.weight_decay, self.steps, _ptr(self.step_dev), _ptr(self.lr_dev),
+                                        _ptr(grad_scale), _ptr(skip), self.seed, _stream())
+        _check("adamw_step", rc)
+
+    def state_values(self, out=None):
+        """The moments as fp32 tensors, two lists (exp_avg, exp_avg_sq):
+        written to ``out`` (two lists of fp32 tensors) when given.  With fp32
+        moments and no ``out`` these are the moments themselves."""
+        if self.state_bits == 32:
+            m, v = self.state["exp_avg"], self.state["exp_avg_sq"]
+            if out is None:
+                return m, v
+            for d, s in zip((*out[0], *out[1]), (*m, *v)):
+                d.copy_(s)
+            return out
+        if out is None:
+            out = tuple([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
+                        for _ in range(2))
+        for t in out:
+            self._same_sizes("out", t, torch.float32, required=True)
+        with _on_device(self.params[0], *out[0], *out[1]):
+            ptrs = [(ctypes.c_void_p * len(t))(*[x.data_ptr() for x in t]) for t in out]
+            rc = _lib.load().adamw_read_state(self._list, len(self.params), ptrs[0], ptrs[1], _stream())
+        _check("adamw_read_state", rc)
+        return out

@@ -32,6 +32,8 @@ Modules:
   moe     -- permutation metadata, gather, unpermute, SiLU gate (fp64)
   mx      -- MX formats (MXFP8 / MXFP4, E8M0 per 32) of the W4A8 variant
   gemm    -- grouped W4A4, W4A8 and BF16 GEMMs (fp64 on exact operands)
+  router  -- top-k routing, its weights and gradient      (fp64)
+  adamw   -- the AdamW step and its 8-bit moments         (fp64; fp32 as defined)
   layer   -- the MoE layer forward / BF16 backward composed from the above
 
 Parity pins: every function here is checked in ``tests/test_oracle_*.py``
@@ -39,4 +41,4 @@ against hand-worked values (``tests/golden/``), brute force on tiny inputs,
 library routines and invariants -- never against itself.
 """
 
-from . import nvfp4, mx, moe, gemm, layer  # noqa: F401
+from . import nvfp4, mx, moe, gemm, router, adamw, layer  # noqa: F401
