@@ -34,8 +34,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch's handle of the current stream, without the Stream object that
+# torch.cuda.current_stream() builds (which takes longer than the rest of a
+# small operator's call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 def _dev(*ts):
@@ -51,22 +60,30 @@ def _need(t, name, dtype, *shape):
     """Checks one argument: dtype (or one of several) and shape (None: any extent)."""
     if t is None:
         return
-    if t.dtype != dtype if isinstance(dtype, torch.dtype) else t.dtype not in dtype:
-        raise ValueError("%s: dtype %s is not supported" % (name, t.dtype))
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    dt, sh = t.dtype, t.shape
+    if dt is not dtype and (isinstance(dtype, torch.dtype) or dt not in dtype):
+        raise ValueError("%s: dtype %s is not supported" % (name, dt))
+    if sh != shape and (len(sh) != len(shape) or any(n is not None and n != m for n, m in zip(shape, sh))):
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(sh), tuple(shape)))
 
 
-def _on_device(*ts):
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on_device(first, *ts):
     """Checks that the tensors are contiguous and share one GPU, and returns a
     context in which that GPU is the current one (its current stream is then
     the one the library is given)."""
-    _dev(*ts)
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) != 1:
-        raise ValueError("nvfp4moe ops take tensors of one GPU, got %s" % sorted(map(str, devs)))
-    dev = devs.pop()
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    dev = first.get_device()
+    ok = dev >= 0 and first.is_contiguous()
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            ok = False
+    if not ok:
+        _dev(first, *ts)
+        raise ValueError("nvfp4moe ops take tensors of one GPU, got %s"
+                         % sorted({str(t.device) for t in (first, *ts) if t is not None}))
+    return _SAME_DEVICE if dev == _device() else torch.cuda.device(dev)
 
 
 _FLOATS = (torch.float32, torch.bfloat16)

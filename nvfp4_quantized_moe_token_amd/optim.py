@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .ops import _DT, _check, _on_device, _ptr, _stream
+from .ops import _DT, _FLOATS, _check, _on_device, _ptr, _stream
 
 BLOCK = _lib.ADAMW_BLOCK
 
@@ -61,10 +61,12 @@ class AdamW:
         self.step_dev = torch.full((1,), step, dtype=torch.int64, device=dev) if capturable else None
         self.lr_dev = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
         self._list = (_lib.AdamWTensor * n)()
-        for i, (d, p, c) in enumerate(zip(self._list, self.params, self.params_bf16)):
+        self._entries = list(self._list)  # views of it, made once
+        for i, (d, p, c) in enumerate(zip(self._entries, self.params, self.params_bf16)):
             d.param, d.param_bf16, d.n = _ptr(p), _ptr(c), p.numel()
             for k in names:
                 setattr(d, k, _ptr(self.state[k][i]))
+        self._numel = [p.numel() for p in self.params]
 
     def _same_sizes(self, name, ts, dtype, required=False, blocks=False):
         if len(ts) != len(self.params):
@@ -93,8 +95,10 @@ class AdamW:
         skip (int32 [1], device): nothing changes when it is not 0 (the step
         still counts)."""
         grads = list(grads)
-        self._same_sizes("grads", grads, (torch.float32, torch.bfloat16), required=True)
-        if any(g.dtype != grads[0].dtype for g in grads):
+        gdt = grads[0].dtype if grads and grads[0] is not None else None
+        if gdt not in _FLOATS or len(grads) != len(self._numel) or any(
+                g is None or g.dtype is not gdt or g.numel() != n for g, n in zip(grads, self._numel)):
+            self._same_sizes("grads", grads, _FLOATS, required=True)
             raise ValueError("grads: one dtype for all")
         for name, t, dt in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
             if t is not None and (t.dtype != dt or t.numel() != 1):
@@ -103,9 +107,9 @@ class AdamW:
             self.steps += 1
             if self.step_dev is not None:
                 self.step_dev.add_(1)
-            for d, g in zip(self._list, grads):
+            for d, g in zip(self._entries, grads):
                 d.grad = g.data_ptr()
-            rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[grads[0].dtype],
+            rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[gdt],
                                         self.state_bits, self.lr, self.betas[0], self.betas[1], self.eps,
                                         self.weight_decay, self.steps, _ptr(self.step_dev), _ptr(self.lr_dev),
                                         _ptr(grad_scale), _ptr(skip), self.seed, _stream())
