@@ -31,19 +31,20 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kRouterThreads = 256;
-constexpr int kProbSumBlocks = 512;  // workgroups that leave partial sums of the probabilities
+constexpr int kProbSumBlocks = 256;  // workgroups that leave partial sums of the probabilities
 
 constexpr float kNegInf = -__builtin_inff();
 
-// Reductions over a token's L lanes; every lane receives the result.
+// Reductions over a token's L lanes; every lane receives the result.  (With a
+// zero for lanes that have no source, which do not occur, the compiler folds
+// the rotation into the operation.)
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v) {
-  const int i = __float_as_int(v);
-  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 template <int CTRL>
-__device__ __forceinline__ int dpp_i(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 constexpr int kRor = 0x120;  // row_ror:n is 0x120 + n (rows of 16 lanes)
 
@@ -59,16 +60,29 @@ __device__ __forceinline__ float group_max(float v) {
   }
   return v;
 }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 template <int L>
-__device__ __forceinline__ int group_min(int v) {
-  int o;
-  o = dpp_i<kRor + 8>(v); v = o < v ? o : v;
-  o = dpp_i<kRor + 4>(v); v = o < v ? o : v;
-  o = dpp_i<kRor + 2>(v); v = o < v ? o : v;
-  o = dpp_i<kRor + 1>(v); v = o < v ? o : v;
+__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+  v = umax(v, dpp_u<kRor + 8>(v));
+  v = umax(v, dpp_u<kRor + 4>(v));
+  v = umax(v, dpp_u<kRor + 2>(v));
+  v = umax(v, dpp_u<kRor + 1>(v));
   if constexpr (L == 64) {
-    o = __shfl_xor(v, 16, 64); v = o < v ? o : v;
-    o = __shfl_xor(v, 32, 64); v = o < v ? o : v;
+    v = umax(v, __shfl_xor(v, 16, 64));
+    v = umax(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_umin(uint32_t v) {
+  v = umin(v, dpp_u<kRor + 8>(v));
+  v = umin(v, dpp_u<kRor + 4>(v));
+  v = umin(v, dpp_u<kRor + 2>(v));
+  v = umin(v, dpp_u<kRor + 1>(v));
+  if constexpr (L == 64) {
+    v = umin(v, __shfl_xor(v, 16, 64));
+    v = umin(v, __shfl_xor(v, 32, 64));
   }
   return v;
 }
@@ -83,6 +97,17 @@ __device__ __forceinline__ float group_sum(float v) {
     v += __shfl_xor(v, 32, 64);
   }
   return v;
+}
+
+// Keys as unsigned integers of the same order; 0 is "never chosen" (-inf, NaN
+// and what has been taken).
+__device__ __forceinline__ uint32_t sortable(float s) {
+  const int b = __float_as_int(s);
+  return s > kNegInf ? (uint32_t)(b ^ ((b >> 31) | (int)0x80000000)) : 0u;
+}
+__device__ __forceinline__ float unsortable(uint32_t u) {
+  const int b = (int)u;
+  return __int_as_float(b ^ (~(b >> 31) | (int)0x80000000));
 }
 
 // Expert of register v of group lane i.
@@ -156,66 +181,72 @@ __device__ __forceinline__ float load_logit(const void* __restrict__ base, int64
   else return reinterpret_cast<const float*>(base)[at];
 }
 
-// max and sum of exp(l - max) over a token's logits.  All -inf: sum 0.
+// max and sum of exp(l - max) over a token's logits, which become exp(l -
+// max).  All -inf: zeros.
 template <int L, int V>
-__device__ __forceinline__ void row_softmax(const float (&l)[V], float& m, float& sum) {
+__device__ __forceinline__ void row_softmax(float (&l)[V], float& m, float& sum) {
   m = l[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
   m = group_max<L>(m);
   sum = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) sum += m > kNegInf || l[v] != l[v] ? __expf(l[v] - m) : 0.0f;
+  for (int v = 0; v < V; ++v) {
+    l[v] = m > kNegInf || l[v] != l[v] ? __expf(l[v] - m) : 0.0f;
+    sum += l[v];
+  }
   sum = group_sum<L>(sum);
 }
 
-// AUX: the lse and/or the per-expert sums of probabilities are wanted.
-// Without them one token per group; with the sums the groups walk the tokens
-// so that every workgroup leaves one partial row.
-template <int L, int V, int W, bool BF16, bool AUX>
-__global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __restrict__ logits, int64_t T, int E,
-                                                                int k, const float* __restrict__ bias, int score,
-                                                                float scale, int32_t* __restrict__ ids,
-                                                                float* __restrict__ w, float* __restrict__ lse,
-                                                                float* __restrict__ partial) {
-  constexpr int G = kRouterThreads / L;  // tokens in flight per workgroup
+// SUM: the per-expert sums of probabilities are wanted.  Without them one
+// token per group; with them large workgroups walk the tokens, so that few
+// partial rows are left to add up.
+template <int L, int V, int W, bool BF16, bool SUM, int THREADS>
+__global__ __launch_bounds__(THREADS) void router_kernel(const void* __restrict__ logits, int64_t T, int E, int k,
+                                                         const float* __restrict__ bias, int score, float scale,
+                                                         int32_t* __restrict__ ids, float* __restrict__ w,
+                                                         float* __restrict__ lse, float* __restrict__ partial) {
+  constexpr int G = THREADS / L;  // tokens in flight per workgroup
   const int i = threadIdx.x % L, g = threadIdx.x / L;
-  float acc[AUX ? V : 1];
+  float acc[SUM ? V : 1];
 #pragma unroll
-  for (int v = 0; v < (AUX ? V : 1); ++v) acc[v] = 0.0f;
+  for (int v = 0; v < (SUM ? V : 1); ++v) acc[v] = 0.0f;
 
   for (int64_t t = (int64_t)blockIdx.x * G + g; t < T; t += (int64_t)gridDim.x * G) {
     float l[V];
     load_row<L, V, W, BF16>(logits, t, E, i, kNegInf, l);
     // Selection: k rounds of "largest key, lowest expert", each taking the
     // winner out.
-    float key[V];
+    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = expert_of<L, W>(v, i);
-      const float s = l[v] + (bias && e < E ? bias[e] : 0.0f);  // (+0 also turns -0 into +0)
-      key[v] = s == s ? s : kNegInf;
+      key[v] = sortable(l[v] + (bias && e < E ? bias[e] : 0.0f));  // (+0 also turns -0 into +0)
     }
-    int mine = -1;  // lane j keeps the j-th choice
+    int mine = -1;  // lane j keeps the j-th choice and its logit
+    float c = kNegInf;
     for (int j = 0; j < k; ++j) {
-      float best = key[0];
+      uint32_t best = key[0];
 #pragma unroll
-      for (int v = 1; v < V; ++v) best = fmaxf(best, key[v]);
-      best = group_max<L>(best);
-      if (!(best > kNegInf)) break;  // uniform in the group: nothing is left
-      int at = 0x7FFFFFFF;
+      for (int v = 1; v < V; ++v) best = umax(best, key[v]);
+      best = group_umax<L>(best);
+      if (best == 0) break;  // uniform in the group: nothing is left
+      uint32_t at = 0xFFFFFFFFu;
 #pragma unroll
       for (int v = V - 1; v >= 0; --v)
-        if (key[v] == best) at = expert_of<L, W>(v, i);
-      at = group_min<L>(at);
+        if (key[v] == best) at = (uint32_t)expert_of<L, W>(v, i);
+      at = group_umin<L>(at);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (expert_of<L, W>(v, i) == at) key[v] = kNegInf;
-      if (i == j) mine = at;
+        if ((uint32_t)expert_of<L, W>(v, i) == at) key[v] = 0u;
+      if (i == j) {
+        mine = (int)at;
+        c = unsortable(best);
+      }
     }
+    if (bias && mine >= 0) c = load_logit<BF16>(logits, t * E + mine);
     float m = 0.0f, sum = 1.0f;
-    if (AUX || score == NVFP4MOE_ROUTER_SOFTMAX) row_softmax<L, V>(l, m, sum);
-    const float c = mine >= 0 ? load_logit<BF16>(logits, t * E + mine) : kNegInf;
+    if (SUM || lse || score == NVFP4MOE_ROUTER_SOFTMAX) row_softmax<L, V>(l, m, sum);
     float wt;
     if (score == NVFP4MOE_ROUTER_TOPK_SOFTMAX) {
       const float mc = group_max<L>(c);
@@ -229,42 +260,56 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(const void* __re
       ids[t * k + i] = mine;
       w[t * k + i] = wt;
     }
-    if constexpr (AUX) {
-      if (lse && i == 0) lse[t] = sum == 0.0f ? kNegInf : m + __logf(sum);
+    if (lse && i == 0) lse[t] = sum == 0.0f ? kNegInf : m + __logf(sum);
+    if constexpr (SUM) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += m > kNegInf || l[v] != l[v] ? __expf(l[v] - m) * inv : 0.0f;
+      for (int v = 0; v < V; ++v) acc[v] += l[v] * inv;
     }
   }
 
-  if constexpr (AUX) {
-    if (partial) {
-      // The groups' sums meet in LDS, in the order of the groups.
-      __shared__ float red[kRouterThreads * V];
+  if constexpr (SUM) {
+    // A wave's groups meet in its lanes, the waves in LDS, always in the same
+    // order.
+    constexpr int NW = THREADS / 64;
+    __shared__ float red[NW * L * V];
+    const int lane = threadIdx.x & 63, wid = threadIdx.x / 64;
 #pragma unroll
-      for (int v = 0; v < V; ++v) red[v * kRouterThreads + threadIdx.x] = acc[v];
-      __syncthreads();
-      for (int x = threadIdx.x; x < L * V; x += kRouterThreads) {
-        const int v = x / L, ii = x % L, e = expert_of<L, W>(v, ii);
-        float s = 0.0f;
-        for (int q = 0; q < G; ++q) s += red[v * kRouterThreads + q * L + ii];
-        if (e < E) partial[(int64_t)blockIdx.x * E + e] = s;
+    for (int v = 0; v < V; ++v) {
+      if constexpr (L == 16) {
+        acc[v] += __shfl_xor(acc[v], 16, 64);
+        acc[v] += __shfl_xor(acc[v], 32, 64);
       }
+      if (lane < L) red[(wid * V + v) * L + i] = acc[v];
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < L * V; x += THREADS) {
+      const int e = expert_of<L, W>(x / L, x % L);
+      float s = red[x];
+#pragma unroll
+      for (int q = 1; q < NW; ++q) s += red[q * L * V + x];
+      if (e < E) partial[(int64_t)blockIdx.x * E + e] = s;
     }
   }
 }
 
-// prob_sum[e] = sum of the workgroups' partial rows, in a fixed order.
-__global__ __launch_bounds__(256) void prob_sum_kernel(const float* __restrict__ partial, int rows, int E,
-                                                       float* __restrict__ out) {
-  __shared__ float red[256];
+// prob_sum[e] = sum of the workgroups' partial rows, in a fixed order: 16
+// experts per workgroup, 64 rows at a time.
+__global__ __launch_bounds__(1024) void prob_sum_kernel(const float* __restrict__ partial, int rows, int E,
+                                                        float* __restrict__ out) {
+  __shared__ float red[16 * 16];
   const int c = threadIdx.x & 15, r = threadIdx.x >> 4, e = blockIdx.x * 16 + c;
   float s = 0.0f;
   if (e < E)
-    for (int q = r; q < rows; q += 16) s += partial[(int64_t)q * E + e];
-  red[threadIdx.x] = s;
+#pragma unroll 4
+    for (int q = r; q < rows; q += 64) s += partial[(int64_t)q * E + e];
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if ((threadIdx.x & 63) < 16) red[(threadIdx.x >> 6) * 16 + c] = s;
   __syncthreads();
-  if (r == 0 && e < E) {
+  if (threadIdx.x < 16 && e < E) {
+    s = red[c];
+#pragma unroll
     for (int q = 1; q < 16; ++q) s += red[q * 16 + c];
     out[e] = s;
   }
@@ -299,8 +344,10 @@ __global__ __launch_bounds__(kRouterThreads) void router_bwd_kernel(
     if (lse) {
       L_t = lse[t];
     } else {
-      float m, sum;
-      row_softmax<L, V>(p, m, sum);
+      float m, sum, ex[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) ex[v] = p[v];
+      row_softmax<L, V>(ex, m, sum);
       L_t = sum == 0.0f ? kNegInf : m + __logf(sum);
     }
     empty = L_t == kNegInf;
@@ -372,8 +419,11 @@ void with_layout(int E, int k, bool vec, F f) {
 
 constexpr int kRouterMaxExperts = 4096;
 
+// Workgroup sizes with probability sums: as large as the registers allow.
+constexpr int sum_threads(int V) { return V <= 16 ? 1024 : 256; }
+
 int64_t prob_sum_rows(int64_t T, int E, int k) {
-  const int64_t per = k <= 16 && E <= 256 ? kRouterThreads / 16 : kRouterThreads / 64;
+  const int64_t per = k <= 16 && E <= 256 ? 1024 / 16 : E <= 1024 ? 1024 / 64 : 256 / 64;
   const int64_t n = cdiv(T, per);
   return n < kProbSumBlocks ? n : kProbSumBlocks;
 }
@@ -409,27 +459,28 @@ extern "C" int moe_router(const void* logits, int logits_dtype, int64_t T, int E
     if (prob_sum) fill_u32_kernel<<<1, 256, 0, st>>>(reinterpret_cast<uint32_t*>(prob_sum), 0u, E);
     return launch_status();
   }
-  const bool bf = logits_dtype == NVFP4MOE_BF16, aux = lse || prob_sum;
+  const bool bf = logits_dtype == NVFP4MOE_BF16;
   float* partial = prob_sum ? reinterpret_cast<float*>(workspace) : nullptr;
   with_layout(E, k, E % 4 == 0 && aligned(logits, 4 * lb), [&](auto Lc, auto Vc, auto Wc) {
     constexpr int L = decltype(Lc)::value, V = decltype(Vc)::value, W = decltype(Wc)::value;
     int64_t grid = cdiv(T, kRouterThreads / L);
     if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
     if (prob_sum) grid = prob_sum_rows(T, E, k);
-#define NVR_GO(B, A)                                                                                          \
-  router_kernel<L, V, W, B, A><<<(unsigned)grid, kRouterThreads, 0, st>>>(logits, T, E, k, bias, score, scale, \
-                                                                          topk_ids, topk_w, lse, partial)
+#define NVR_GO(B, S, N)                                                                                             \
+  router_kernel<L, V, W, B, S, N><<<(unsigned)grid, N, 0, st>>>(logits, T, E, k, bias, score, scale, topk_ids, topk_w, \
+                                                                lse, partial)
+    constexpr int N = sum_threads(V);
     if (bf) {
-      if (aux) NVR_GO(true, true);
-      else NVR_GO(true, false);
+      if (prob_sum) NVR_GO(true, true, N);
+      else NVR_GO(true, false, kRouterThreads);
     } else {
-      if (aux) NVR_GO(false, true);
-      else NVR_GO(false, false);
+      if (prob_sum) NVR_GO(false, true, N);
+      else NVR_GO(false, false, kRouterThreads);
     }
 #undef NVR_GO
   });
   if (prob_sum)
-    prob_sum_kernel<<<(unsigned)cdiv(E, 16), 256, 0, st>>>(partial, (int)prob_sum_rows(T, E, k), E, prob_sum);
+    prob_sum_kernel<<<(unsigned)cdiv(E, 16), 1024, 0, st>>>(partial, (int)prob_sum_rows(T, E, k), E, prob_sum);
   return launch_status();
 }
 
