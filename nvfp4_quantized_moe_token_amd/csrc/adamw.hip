@@ -60,6 +60,7 @@ struct Args {
   int32_t base;                    // ordinal of t[0] in the caller's list
   uint32_t seed;
   float lr, wd, b1, c1, b2, c2, eps;
+  float rate, inv_root;            // of `step` and `lr`, when neither comes from the device
   double beta1, beta2;
   int64_t step;
   const int64_t* step_dev;
@@ -68,6 +69,22 @@ struct Args {
   const int32_t* skip;
 };
 static_assert(sizeof(Args) <= 4096, "kernel arguments");
+
+// The bias corrections of step t: lr / (1 - b1^t) and 1 / sqrt(1 - b2^t), the
+// powers by repeated squaring in fp64.  The same operations on the host and on
+// the device, so a captured step gives the same bits.
+__host__ __device__ inline double power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1, b *= b)
+    if (t & 1) r *= b;
+  return r;
+}
+__host__ __device__ inline float corrected_rate(float lr, double beta1, int64_t t) {
+  return (float)((double)lr / (1.0 - power(beta1, t)));
+}
+__host__ __device__ inline float corrected_root(double beta2, int64_t t) {
+  return (float)(1.0 / sqrt(1.0 - power(beta2, t)));
+}
 
 // 32-bit mixer: multiply and xor-shift, constants from the fractional digits
 // of the golden ratio and the square root of 3.
@@ -184,8 +201,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(const Args a) {
   const int64_t step = a.step_dev ? *a.step_dev : a.step;
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  const double bc1 = 1.0 - pow(a.beta1, (double)step), bc2 = 1.0 - pow(a.beta2, (double)step);
-  const float rate = (float)((double)lr / bc1), inv_root = (float)(1.0 / sqrt(bc2));
+  float rate = a.rate, inv_root = a.inv_root;
+  if (a.step_dev || a.lr_dev) {
+    rate = corrected_rate(lr, a.beta1, step);
+    inv_root = corrected_root(a.beta2, step);
+  }
   const float keep = 1.0f - lr * a.wd;
   uint32_t key = 0;
   if (STATE8 || P_BF16) key = mix(mix(mix(a.seed) + (uint32_t)step) + (uint32_t)(a.base + ti));
@@ -371,6 +391,8 @@ extern "C" int adamw_step(const nvfp4moe_adamw_tensor* tensors, int count, int p
   a.beta1 = beta1;
   a.beta2 = beta2;
   a.step = step;
+  a.rate = step > 0 ? corrected_rate(a.lr, beta1, step) : 0.0f;
+  a.inv_root = step > 0 ? corrected_root(beta2, step) : 0.0f;
   a.step_dev = step_dev;
   a.lr_dev = lr_dev;
   a.grad_scale = grad_scale;
