@@ -27,7 +27,8 @@
 // lane (16-byte loads of fp32), so the scale of a block is one wave
 // reduction and nothing is shared between waves.  A workgroup takes kChunk
 // consecutive elements of one tensor; the tensors' pointers and first
-// workgroups travel in the kernel arguments, up to kMaxTensors per launch.
+// workgroups travel in the kernel arguments, 72 tensors per launch (56
+// with 8-bit moments).
 // The bound is HBM: 30 bytes per element with fp32 moments, a bf16 copy and
 // fp32 gradients, 18 with 8-bit moments.
 #include <math.h>
@@ -40,7 +41,6 @@ namespace {
 constexpr int kStateBlock = NVFP4MOE_ADAMW_BLOCK;  // elements per 8-bit scale: one wave, 4 per lane
 constexpr int kWaveBlocks = 4;                     // blocks per wave
 constexpr int kChunk = 4 * kWaveBlocks * kStateBlock;  // elements per workgroup (4 waves)
-constexpr int kMaxTensors = 48;                    // per launch: their records fit 4 KiB of arguments
 static_assert(kStateBlock == 256, "one wave holds a block");
 
 struct Tensor {
@@ -48,13 +48,19 @@ struct Tensor {
   const void* g;
   void* m;
   void* v;
-  float* ms;
-  float* vs;
   uint16_t* copy;
   int64_t n;
 };
+struct Scales {
+  float* m;
+  float* v;
+};
+template <bool STATE8>
 struct Args {
+  static constexpr bool kState8 = STATE8;
+  static constexpr int kMaxTensors = STATE8 ? 56 : 72;  // per launch: their records fit 4 KiB of arguments
   Tensor t[kMaxTensors];
+  Scales s[STATE8 ? kMaxTensors : 1];
   int32_t first[kMaxTensors + 1];  // first workgroup of each tensor
   int32_t n_tensors;
   int32_t base;                    // ordinal of t[0] in the caller's list
@@ -68,7 +74,17 @@ struct Args {
   const float* grad_scale;
   const int32_t* skip;
 };
-static_assert(sizeof(Args) <= 4096, "kernel arguments");
+static_assert(sizeof(Args<false>) <= 4096 && sizeof(Args<true>) <= 4096, "kernel arguments");
+
+// The tensor of this workgroup.
+template <bool STATE8>
+__device__ __forceinline__ int tensor_of_group(const Args<STATE8>& a) {
+  int ti = 0;
+#pragma unroll
+  for (int step = 64; step > 0; step >>= 1)
+    if (ti + step < a.n_tensors && a.first[ti + step] <= (int)blockIdx.x) ti += step;
+  return ti;
+}
 
 // The bias corrections of step t: lr / (1 - b1^t) and 1 / sqrt(1 - b2^t), the
 // powers by repeated squaring in fp64.  The same operations on the host and on
@@ -187,13 +203,11 @@ __device__ __forceinline__ void store4_u8(void* base, int64_t i, int64_t n, bool
 }
 
 template <bool P_BF16, bool G_BF16, bool STATE8>
-__global__ __launch_bounds__(256) void adamw_kernel(const Args a) {
+__global__ __launch_bounds__(256) void adamw_kernel(const Args<STATE8> a) {
   if (a.skip && *a.skip != 0) return;
-  // The workgroup's tensor.
-  int ti = 0;
-  for (int step = 32; step > 0; step >>= 1)
-    if (ti + step < a.n_tensors && a.first[ti + step] <= (int)blockIdx.x) ti += step;
+  const int ti = tensor_of_group(a);
   const Tensor& t = a.t[ti];
+  const Scales& sc = a.s[STATE8 ? ti : 0];
   const int64_t n = t.n;
   const int64_t chunk = (int64_t)((int)blockIdx.x - a.first[ti]) * kChunk;
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
@@ -224,7 +238,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const Args a) {
     load4<G_BF16>(t.g, i, n, whole, g);
     if constexpr (STATE8) {
       const uint32_t mc = load4_u8(t.m, i, n, whole), vc = load4_u8(t.v, i, n, whole);
-      const float sm = t.ms[i0 / kStateBlock], sv = t.vs[i0 / kStateBlock];
+      const float sm = sc.m[i0 / kStateBlock], sv = sc.v[i0 / kStateBlock];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         m[q] = e4m3_decode((mc >> (8 * q)) & 0xFF) * sm;
@@ -277,8 +291,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const Args a) {
       store4_u8(t.m, i, n, whole, mc);
       store4_u8(t.v, i, n, whole, vc);
       if (lane == 0) {
-        t.ms[i0 / kStateBlock] = sm;
-        t.vs[i0 / kStateBlock] = av;
+        sc.m[i0 / kStateBlock] = sm;
+        sc.v[i0 / kStateBlock] = av;
       }
     } else {
       store4_f32(t.m, i, n, whole, m);
@@ -288,11 +302,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(const Args a) {
 }
 
 // fp32 values of 8-bit moments.
-__global__ __launch_bounds__(256) void adamw_read_kernel(const Args a) {
-  int ti = 0;
-  for (int step = 32; step > 0; step >>= 1)
-    if (ti + step < a.n_tensors && a.first[ti + step] <= (int)blockIdx.x) ti += step;
+__global__ __launch_bounds__(256) void adamw_read_kernel(const Args<true> a) {
+  const int ti = tensor_of_group(a);
   const Tensor& t = a.t[ti];
+  const Scales& sc = a.s[ti];
   float* om = reinterpret_cast<float*>(t.p);
   float* ov = reinterpret_cast<float*>(t.copy);
   const int64_t n = t.n, chunk = (int64_t)((int)blockIdx.x - a.first[ti]) * kChunk;
@@ -305,7 +318,7 @@ __global__ __launch_bounds__(256) void adamw_read_kernel(const Args a) {
     const bool whole = vec && i0 + kStateBlock <= n;
     const int64_t i = i0 + lane * 4;
     const uint32_t mc = load4_u8(t.m, i, n, whole), vc = load4_u8(t.v, i, n, whole);
-    const float sm = t.ms[i0 / kStateBlock], sv = t.vs[i0 / kStateBlock];
+    const float sm = sc.m[i0 / kStateBlock], sv = sc.v[i0 / kStateBlock];
     float m[4], v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -319,14 +332,14 @@ __global__ __launch_bounds__(256) void adamw_read_kernel(const Args a) {
 
 // Fills launches of up to kMaxTensors tensors and calls go(args, workgroups)
 // for each; tensors without elements are left out.
-template <class F>
-int for_launches(const nvfp4moe_adamw_tensor* list, int count, Args& a, F go) {
+template <bool STATE8, class F>
+int for_launches(const nvfp4moe_adamw_tensor* list, int count, Args<STATE8>& a, F go) {
   a.n_tensors = 0;
   int64_t groups = 0;
   for (int i = 0; i <= count; ++i) {
     const int64_t n = i < count ? list[i].n : 0, need = cdiv(n, kChunk);
     // the ordinals of a launch's tensors are consecutive: an empty tensor keeps its place
-    if (i == count || a.n_tensors == kMaxTensors || groups + need > 0x7FFFFFFFLL) {
+    if (i == count || a.n_tensors == a.kMaxTensors || groups + need > 0x7FFFFFFFLL) {
       if (groups > 0) {
         a.first[a.n_tensors] = (int32_t)groups;
         const int rc = go(a, (unsigned)groups);
@@ -338,8 +351,8 @@ int for_launches(const nvfp4moe_adamw_tensor* list, int count, Args& a, F go) {
     }
     if (a.n_tensors == 0) a.base = i;
     const nvfp4moe_adamw_tensor& s = list[i];
-    a.t[a.n_tensors] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, s.avg_scale, s.avg_sq_scale,
-                              reinterpret_cast<uint16_t*>(s.param_bf16), n};
+    a.t[a.n_tensors] = Tensor{s.param, s.grad, s.exp_avg, s.exp_avg_sq, reinterpret_cast<uint16_t*>(s.param_bf16), n};
+    if (STATE8) a.s[a.n_tensors] = Scales{s.avg_scale, s.avg_sq_scale};
     a.first[a.n_tensors++] = (int32_t)groups;
     groups += need;
   }
@@ -379,39 +392,35 @@ extern "C" int adamw_step(const nvfp4moe_adamw_tensor* tensors, int count, int p
   const int arch = check_arch();
   if (arch != NVFP4MOE_OK) return arch;
   hipStream_t st = as_stream(stream);
-  Args a = {};
-  a.seed = seed;
-  a.lr = (float)lr;
-  a.wd = (float)weight_decay;
-  a.b1 = (float)beta1;
-  a.c1 = (float)(1.0 - beta1);
-  a.b2 = (float)beta2;
-  a.c2 = (float)(1.0 - beta2);
-  a.eps = (float)eps;
-  a.beta1 = beta1;
-  a.beta2 = beta2;
-  a.step = step;
-  a.rate = step > 0 ? corrected_rate(a.lr, beta1, step) : 0.0f;
-  a.inv_root = step > 0 ? corrected_root(beta2, step) : 0.0f;
-  a.step_dev = step_dev;
-  a.lr_dev = lr_dev;
-  a.grad_scale = grad_scale;
-  a.skip = skip;
-  const bool p16 = param_dtype == NVFP4MOE_BF16, g16 = grad_dtype == NVFP4MOE_BF16, s8 = state_bits == 8;
-  return for_launches(tensors, count, a, [&](const Args& args, unsigned grid) {
-#define NVA(P, G, S) \
-  if (p16 == P && g16 == G && s8 == S) adamw_kernel<P, G, S><<<grid, 256, 0, st>>>(args);
-    NVA(false, false, false)
-    NVA(false, false, true)
-    NVA(false, true, false)
-    NVA(false, true, true)
-    NVA(true, false, false)
-    NVA(true, false, true)
-    NVA(true, true, false)
-    NVA(true, true, true)
-#undef NVA
-    return launch_status();
-  });
+  const bool p16 = param_dtype == NVFP4MOE_BF16, g16 = grad_dtype == NVFP4MOE_BF16;
+  auto run = [&](auto a) {
+    constexpr bool S = decltype(a)::kState8;
+    a.seed = seed;
+    a.lr = (float)lr;
+    a.wd = (float)weight_decay;
+    a.b1 = (float)beta1;
+    a.c1 = (float)(1.0 - beta1);
+    a.b2 = (float)beta2;
+    a.c2 = (float)(1.0 - beta2);
+    a.eps = (float)eps;
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.step = step;
+    a.rate = step > 0 ? corrected_rate(a.lr, beta1, step) : 0.0f;
+    a.inv_root = step > 0 ? corrected_root(beta2, step) : 0.0f;
+    a.step_dev = step_dev;
+    a.lr_dev = lr_dev;
+    a.grad_scale = grad_scale;
+    a.skip = skip;
+    return for_launches(tensors, count, a, [&](const Args<S>& args, unsigned grid) {
+      if (p16 && g16) adamw_kernel<true, true, S><<<grid, 256, 0, st>>>(args);
+      else if (p16) adamw_kernel<true, false, S><<<grid, 256, 0, st>>>(args);
+      else if (g16) adamw_kernel<false, true, S><<<grid, 256, 0, st>>>(args);
+      else adamw_kernel<false, false, S><<<grid, 256, 0, st>>>(args);
+      return launch_status();
+    });
+  };
+  return state_bits == 8 ? run(Args<true>{}) : run(Args<false>{});
 }
 
 extern "C" int adamw_read_state(const nvfp4moe_adamw_tensor* tensors, int count, float* const* avg_out,
@@ -431,8 +440,8 @@ extern "C" int adamw_read_state(const nvfp4moe_adamw_tensor* tensors, int count,
   const int arch = check_arch();
   if (arch != NVFP4MOE_OK) return arch;
   hipStream_t st = as_stream(stream);
-  Args a = {};
-  return for_launches(tensors, count, a, [&](Args& args, unsigned grid) {
+  Args<true> a = {};
+  return for_launches(tensors, count, a, [&](Args<true>& args, unsigned grid) {
     for (int i = 0; i < args.n_tensors; ++i) {
       args.t[i].p = avg_out[args.base + i];
       args.t[i].copy = reinterpret_cast<uint16_t*>(avg_sq_out[args.base + i]);

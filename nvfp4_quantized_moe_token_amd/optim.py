@@ -1,5 +1,5 @@
 """AdamW for the learner's weights on the library's adamw_step: one launch for
-up to 48 tensors, moments in fp32 or in 8 bits.
+56 or 72 tensors, moments in fp32 or in 8 bits.
 
 The class owns the moments and the list of pointers that the C entry point
 takes; every step of the arithmetic runs in the HIP kernel.
