@@ -11,10 +11,9 @@
 // Data movement.  Codes and scales go HBM -> LDS by buffer loads that write
 // LDS directly; rows past an expert's end or past N read as zeros.  A stage
 // holds 256 reduction elements: 128 bytes of codes per row (one cache line),
-// 16-byte units XOR-swizzled by row, and the row's 8 scale bytes as two words
-// in two planes (elements 0..127 and 128..255), so that a lane's word serves
-// two MFMAs (the instruction selects the byte).  A ring of S stages keeps
-// S - 1 in flight; one wait and one workgroup barrier per stage.
+// 16-byte units XOR-swizzled by row.  Scales travel 16 bytes a row, for two
+// stages at once.  A ring of S stages runs S - 1 ahead of the computation,
+// across the ends of tiles; one wait and one workgroup barrier per stage.
 //
 // Scheduling is that of the other grouped GEMMs: a persistent grid, each
 // workgroup finds its tiles from the device offsets, tiles in contiguous
@@ -29,8 +28,6 @@
 
 namespace nvfp4moe {
 namespace {
-
-constexpr int kKS = 256;  // reduction elements per stage
 
 enum Epi { EPI_PLAIN = 0, EPI_SILU = 1, EPI_SILU_Q = 2 };
 
@@ -49,319 +46,542 @@ struct Params {
   int E, n_tiles;
 };
 
-// Code rows are 128 bytes; 16-byte unit u of row r lies at unit u ^ swz(r).  The
-// swizzle repeats every 32 rows, so a wave's fragments differ by constant
-// offsets, and unit 2c + h of chunk c is one XOR away from unit h.
-__device__ __forceinline__ int swz(int r) { return kswz(r & 31); }
+constexpr int kKS = 256;            // reduction elements per stage: 128 bytes of codes per row, one cache line
+constexpr int kRowB = kKS / 2;      // code bytes per row
+constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
+constexpr int kTiles = 64;          // tiles looked up at a time
+constexpr int kWaveOut = 1024;      // bytes of a wave's epilogue staging: 16 rows of 64 bytes
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
 typedef __attribute__((address_space(3))) const uint32_t lds_u32_t;
-// 32 codes at an LDS byte address; the operand's upper four registers are not
-// read for a 4-bit format.
+
+// A fragment: 16 bytes of codes (the instruction's operand has room for 32).
 __device__ __forceinline__ i32x8_t frag(uint32_t at) {
   const i32x4_t v = *(lds_i32x4_t*)(uintptr_t)at;
-  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+  return (i32x8_t){v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+}
+
+// 16-byte unit u of code row r lies at unit u ^ swz(r).  The swizzle repeats
+// every 32 rows, so a wave's fragments differ by constant offsets, and unit
+// 2c + h of chunk c is one XOR away from unit h.
+__device__ __forceinline__ int swz(int r) { return kswz(r & 31); }
+
+// Accumulators stay in the accumulation registers until an element is used:
+// left to itself the compiler moves whole blocks to vector registers at the
+// end of the k-loop and spills.  settle() waits out the MFMA -> read latency,
+// which the compiler does not see here; element() then reads one.
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
+__device__ __forceinline__ float element(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+// A buffer region of less than 2^31 bytes: reads past it are zeros, writes are
+// dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t region(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, kRawBufferWord3);
+}
+// Four consecutive elements as bf16.
+__device__ __forceinline__ uint2 bf16x4(const f32x16_t& a, int g) {
+  const float x = element(a[4 * g]), y = element(a[4 * g + 1]), z = element(a[4 * g + 2]), w = element(a[4 * g + 3]);
+  return make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
 }
 
 template <int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p) {
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
-  static_assert(FM >= 1 && FN >= 1 && WTM % 32 == 0 && WTN % 32 == 0, "wave tiling");
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && BN % 64 == 0, "whole loads per wave");
+  static_assert(FM >= 1 && FN >= 2 && WTM % 32 == 0 && WTN % 64 == 0, "wave tiling");
   constexpr bool SILU = EPI != EPI_PLAIN;
-  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  constexpr int SA = BM < 64 ? 64 : BM;          // scale rows of A (whole 64-lane loads)
-  constexpr int PLANE = (SA + BN) * 4;           // one scale word per row
-  constexpr int AT_A = 2 * PLANE, AT_B = AT_A + A_BYTES, STAGE = AT_B + B_BYTES;  // scales, A, B
-  static_assert(STAGE % 128 == 0 && AT_A % 128 == 0, "the chunk XOR stays inside a row");
-  constexpr int A_INSTR = BM / (8 * NW), B_INSTR = BN / (8 * NW);
-  constexpr int SC_BLK = (SA + BN) / 64, SC_LOADS = 2 * SC_BLK;  // loads of 64 words per stage
-  constexpr int SC_INSTR = (SC_LOADS + NW - 1) / NW;             // per wave; the excess lands in a pad
-  constexpr int NDMA = A_INSTR + B_INSTR + SC_INSTR;
-  static_assert(S >= 2 && NDMA * (S - 2) <= 63, "pipeline depth");
+  constexpr int SA = BM < 64 ? 64 : BM;                    // scale rows of A (whole loads)
+  constexpr int AT_B = BM * kRowB, STAGE = AT_B + BN * kRowB;  // codes of A, then B
+  constexpr int SBUF = (SA + BN) * 16;                     // scales of two stages
+  // 1 KiB loads of 8 code rows, and of 64 rows of scales, dealt to the waves in
+  // turn; every wave issues NDMA per stage, whatever is left over landing in a
+  // pad, so that its waits are constants.
+  constexpr int A_LOADS = BM / 8, B_LOADS = BN / 8, SC_LOADS = (SA + BN) / 64;
+  constexpr int A_INSTR = A_LOADS / NW, B_INSTR = B_LOADS / NW, SC_INSTR = (SC_LOADS + NW - 1) / NW;
+  constexpr int NDMA = A_INSTR + B_INSTR + SC_INSTR, HALF = (NDMA + 1) / 2;
+  static_assert(A_LOADS % NW == 0 && B_LOADS % NW == 0 && NW % 4 == 0, "the rows of a wave's loads agree modulo 32");
+  constexpr int AHEAD = (S - 2) * NDMA;  // loads of this wave that are younger than the stage waited for
+  static_assert(S >= 2 && AHEAD <= 31, "pipeline depth");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + 256];
-  __shared__ int64_t s_tile[5];  // expert, first row, end row, row-block count, n-tile
-  constexpr int kOffLds = 1025;
-  __shared__ int32_t s_off[kOffLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * (STAGE + SBUF) + NW * kWaveOut + 1024];
+  __shared__ __attribute__((aligned(16))) int4 s_tile[2 * kTiles];  // this workgroup's tiles: expert, n-tile, first and end row
+  __shared__ int32_t s_off[kOffsetsInLds + 1];                      // row offsets
+  __shared__ int32_t s_blk[kOffsetsInLds + 1];                      // row blocks before each expert
+  __shared__ int s_blocks;
+  static_assert(sizeof(smem) + sizeof(s_tile) + sizeof(s_off) + sizeof(s_blk) + 64 <= 160 * 1024, "LDS");
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wid / WN, wn = wid % WN;
-  const uint32_t smem_lds = (uint32_t)(uintptr_t)(const lds_void_t*)smem;
-  const bool off_in_lds = p.E < kOffLds;
+  const uint32_t smem_lds = (uint32_t)(uintptr_t)(const lds_void_t*)smem, scales = smem_lds + S * STAGE,
+                 out = S * (STAGE + SBUF) + wid * kWaveOut, pad = smem_lds + S * (STAGE + SBUF) + NW * kWaveOut;
+  const bool off_in_lds = p.E <= kOffsetsInLds;
   lds_i32_t* off_lds = (lds_i32_t*)s_off;
   if (off_in_lds)
     for (int i = threadIdx.x; i <= p.E; i += NW * 64) s_off[i] = p.offsets[i];
+  __syncthreads();
   if (wid == 0) {
-    const int blocks = count_row_blocks<BM>(p.offsets, p.E, p.M);
-    if (lane == 0) s_tile[3] = blocks;
+    if (off_in_lds) {
+      int base = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 64) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < p.E) expert_range(off_lds, e, p.M, lo, hi);
+        int incl = (hi - lo + BM - 1) / BM;
+        const int cnt = incl;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int v = __shfl_up(incl, o, 64);
+          if (lane >= o) incl += v;
+        }
+        if (e < p.E) s_blk[e] = base + incl - cnt;
+        base += __shfl(incl, 63, 64);
+      }
+      if (lane == 0) {
+        s_blk[p.E] = base;
+        s_blocks = base;
+      }
+    } else {
+      const int blocks = count_row_blocks<BM>(p.offsets, p.E, p.M);
+      if (lane == 0) s_blocks = blocks;
+    }
   }
   __syncthreads();
-  const int64_t total = s_tile[3] * p.n_tiles;
+  const int64_t total = (int64_t)__builtin_amdgcn_readfirstlane(s_blocks) * p.n_tiles;
   const int xcd = blockIdx.x & 7;
-  const int64_t t_end = total * (xcd + 1) / 8, t_step = gridDim.x >> 3;
+  const int64_t t_step = gridDim.x >> 3, t_first = total * xcd / 8 + (blockIdx.x >> 3), t_end = total * (xcd + 1) / 8;
+  const int my_tiles = t_first < t_end ? (int)((t_end - t_first + t_step - 1) / t_step) : 0;
 
-  // A lane's byte offsets in the regions of a tile: the same for every tile;
-  // a stage adds a fixed number of bytes per row.
-  const int64_t rowb = p.K / 2, srow = p.K / 32, gate_f = SILU ? p.N / 2 : 0;
-  uint32_t oa[A_INSTR], ob[B_INSTR], os[SC_INSTR];
-  // every load of a wave has the same rows modulo 32, so its lane takes the
-  // same 16-byte unit of each row
-  static_assert((8 * NW) % 32 == 0, "rows of a wave's loads, modulo 32");
-  const uint32_t unit16 = ((lane & 7) ^ swz(wid * 8 + lane / 8)) << 4;
-#pragma unroll
-  for (int i = 0; i < A_INSTR; ++i) {
-    const int row = (wid + NW * i) * 8 + lane / 8;
-    oa[i] = (uint32_t)(row * rowb) + unit16;
-  }
-#pragma unroll
-  for (int i = 0; i < B_INSTR; ++i) {
-    const int row = (wid + NW * i) * 8 + lane / 8;
-    const int64_t grow = SILU ? gate_up_row(row, gate_f, 0) : row;
-    ob[i] = (uint32_t)(grow * rowb) + unit16;
-  }
-#pragma unroll
-  for (int i = 0; i < SC_INSTR; ++i) {
-    const int idx = wid + NW * i, blk = idx % SC_BLK, plane = idx / SC_BLK;
-    const bool is_a = blk * 64 < SA;
-    const int row = (is_a ? blk * 64 : blk * 64 - SA) + lane;
-    const bool real = idx < SC_LOADS && (!is_a || row < BM);
-    const int64_t grow = SILU && !is_a ? gate_up_row(row, gate_f, 0) : row;
-    os[i] = real ? (uint32_t)(grow * srow + plane * 4) : kOOB;
-  }
-
-  // This lane's fragment addresses in slot 0: row lane % 32 of the wave's
-  // first row block, unit lane / 32; and its scale words in plane 0.
-  const uint32_t unit0 = (lane & 31) * 128 + (((lane >> 5) ^ swz(lane)) << 4);
-  const uint32_t fa0 = smem_lds + AT_A + wm * WTM * 128 + unit0, fb0 = smem_lds + AT_B + wn * WTN * 128 + unit0;
-  const uint32_t sa0 = smem_lds + (wm * WTM + (lane & 31)) * 4, sb0 = smem_lds + (SA + wn * WTN + (lane & 31)) * 4;
-
-  float tile_amax = 0.0f;
-  for (int64_t L = total * xcd / 8 + (blockIdx.x >> 3); L < t_end; L += t_step) {
-    lds_barrier();  // every wave is done with the previous tile's LDS and s_tile
-    if (wid == 0) {
-      int e = -1, nt = 0;
-      int64_t r0 = 0, r1 = 0;
-      const bool ok = off_in_lds ? find_tile<BM, true>(off_lds, p.E, p.M, L, p.n_tiles, e, r0, r1, nt)
-                                 : find_tile<BM, true>(p.offsets, p.E, p.M, L, p.n_tiles, e, r0, r1, nt);
-      if (lane == 0) {
-        s_tile[0] = ok ? e : -1;
-        s_tile[1] = r0;
-        s_tile[2] = r1;
-        s_tile[4] = nt;
+  // Looks up this workgroup's tiles i0 .. i0 + 63, one per lane, into half
+  // (i0 / 64) % 2 of s_tile.  Every wave does so for itself and writes the same
+  // values.  The tiles of an expert are numbered n-tile-major (its row blocks
+  // that share a weight panel are neighbours and run side by side on one XCD).
+  auto look_up = [&](int i0) {
+    int4 t = make_int4(-1, 0, 0, 0);
+    if (off_in_lds) {
+      if (i0 + lane < my_tiles) {
+        const uint32_t nt = (uint32_t)p.n_tiles, L = (uint32_t)(t_first + (i0 + lane) * t_step), slot = L / nt;
+        int e = 0, hi_e = p.E;  // the last expert with no more than `slot` blocks before it
+        while (hi_e - e > 1) {
+          const int mid = (e + hi_e) >> 1;
+          if ((uint32_t)s_blk[mid] <= slot) e = mid;
+          else hi_e = mid;
+        }
+        int lo, hi;
+        expert_range(off_lds, e, p.M, lo, hi);
+        const uint32_t in = L - (uint32_t)s_blk[e] * nt, cnt = (uint32_t)(s_blk[e + 1] - s_blk[e]);
+        t.x = e;
+        t.y = (int)(in / cnt);
+        t.z = lo + (int)(in % cnt) * BM;
+        t.w = hi - t.z < BM ? hi : t.z + BM;
+      }
+    } else {
+      for (int i = 0; i < kTiles && i0 + i < my_tiles; ++i) {
+        int e = -1, n = 0;
+        int64_t r0 = 0, r1 = 0;
+        const bool ok = find_tile<BM, true>(p.offsets, p.E, p.M, t_first + (i0 + i) * t_step, p.n_tiles, e, r0, r1, n);
+        if (lane == i && ok) t = make_int4(e, n, (int)r0, (int)r1);
       }
     }
-    lds_barrier();
-    const int expert = __builtin_amdgcn_readfirstlane((int)s_tile[0]);
-    if (expert < 0) break;  // uniform: only when offsets changed under the kernel
-    const int64_t m0 = uniform64(s_tile[1]), m_end = uniform64(s_tile[2]), n0 = uniform64(s_tile[4]) * BN;
+    s_tile[(i0 & kTiles) + lane] = t;
+  };
+  // Tile i of this workgroup, in scalar registers (expert -1: none).
+  auto tile = [&](int i) {
+    int4 t = make_int4(-1, 0, 0, 0);
+    if (i < my_tiles) {
+      t = s_tile[i & (2 * kTiles - 1)];
+      t.x = __builtin_amdgcn_readfirstlane(t.x);
+      t.y = __builtin_amdgcn_readfirstlane(t.y);
+      t.z = __builtin_amdgcn_readfirstlane(t.z);
+      t.w = __builtin_amdgcn_readfirstlane(t.w);
+    }
+    return t;
+  };
 
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + m0 * rowb, (m_end - m0) * rowb);
-    const __amdgpu_buffer_rsrc_t rsa = make_rsrc(p.as + m0 * srow, (m_end - m0) * srow);
-    const int64_t brow = (int64_t)expert * p.N + (SILU ? n0 / 2 : n0);
-    const int64_t nv = SILU ? p.N - n0 / 2 : p.N - n0 < BN ? p.N - n0 : BN;
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.b + brow * rowb, nv * rowb);
-    const __amdgpu_buffer_rsrc_t rsb = make_rsrc(p.bs + brow * srow, nv * srow);
-
-    auto load_stage = [&](int64_t kt, int slot) {
-      const uint32_t st = smem_lds + slot * STAGE;
-      const uint32_t k0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(kt * kKS));
-      // K % 256 == 128: the second half of the last stage reads as zeros
-      const uint32_t left = (uint32_t)p.K - k0;
-      const bool in_k = unit16 * 2 < left;
+  // Loads.  A lane's byte offsets of its first loads of a tile; load i adds
+  // 8 NW i rows (gate and up granules of 32 rows alternate, and 8 NW is a
+  // multiple of 32).  Scales are read 16 bytes a row, for two stages at once:
+  // every row is a cache line of its own, and a load of 64 lines takes the
+  // address unit 64 to 110 cycles however short they are (measured; a 1 KiB
+  // load of whole lines takes 16).
+  const int64_t F = p.N / 2;
+  const uint32_t rowb = (uint32_t)(p.K / 2), srow = (uint32_t)(p.K / 32);
+  const int lrow = wid * 8 + lane / 8, lunit = (lane & 7) ^ swz(lrow);
+  const uint32_t la0 = (uint32_t)lrow * rowb + lunit * 16;
+  const uint32_t lb0 = (uint32_t)(SILU ? gate_up_row(lrow, F, 0) : lrow) * rowb + lunit * 16;
+  uint32_t ls0[SC_INSTR];
 #pragma unroll
-      for (int i = 0; i < A_INSTR; ++i) dma16(ra, st + AT_A + (wid + NW * i) * 1024, in_k ? oa[i] + k0 / 2 : kOOB);
+  for (int x = 0; x < SC_INSTR; ++x) {
+    const int idx = wid + NW * x;
+    const bool is_a = idx * 64 < SA;
+    const int row = (is_a ? idx * 64 : idx * 64 - SA) + lane;
+    const bool real = idx < SC_LOADS && (!is_a || row < BM);
+    ls0[x] = real ? (uint32_t)(SILU && !is_a ? gate_up_row(row, F, 0) : row) * srow : kOOB;
+  }
+  const int nk = p.K > 0 ? (int)((p.K + kKS - 1) / kKS) : 1;  // (K == 0: one stage of zeros)
+  // The last stage may hold 128 elements only: its upper units are not read
+  // (zeros), and the scales of its upper chunks, which would be the next
+  // row's, are taken as 0.
+  const uint32_t beyond = p.K % kKS != 0 && lunit >= 4 ? kOOB : 0u;
+  // The load cursor: stage ld_kt of tile ld_i, always S - 1 stages ahead of the
+  // computation.  Behind the last tile its regions are empty and its loads go
+  // to the pad.
+  int ld_i = 0, ld_kt = 0;
+  uint32_t ld_slot = 0, ld_sbuf = 0, la = 0, lb = 0;
+  bool ld_on = true;
+  __amdgpu_buffer_rsrc_t ra, rb, rsc[SC_INSTR];
+  auto regions = [&]() {
+    const int4 t = tile(ld_i);
+    ld_on = t.x >= 0;
+    const int64_t n0 = (int64_t)t.y * BN, brow = ld_on ? (int64_t)t.x * p.N + (SILU ? n0 / 2 : n0) : 0;
+    const uint32_t left = (uint32_t)p.N - (uint32_t)n0 / (SILU ? 2 : 1);
+    const uint32_t nv = !ld_on ? 0u : SILU || left < BN ? left : BN, mv = (uint32_t)(t.w - t.z);
+    ra = region(p.a + t.z * (int64_t)rowb, mv * rowb);
+    rb = region(p.b + brow * (int64_t)rowb, nv * rowb);
 #pragma unroll
-      for (int i = 0; i < B_INSTR; ++i) dma16(rb, st + AT_B + (wid + NW * i) * 1024, in_k ? ob[i] + k0 / 2 : kOOB);
-#pragma unroll
-      for (int i = 0; i < SC_INSTR; ++i) {
-        const int idx = wid + NW * i, blk = idx % SC_BLK, plane = idx / SC_BLK;
-        const uint32_t at = idx < SC_LOADS ? st + plane * PLANE + blk * 256
-                                           : smem_lds + S * STAGE;
-        dma4(blk * 64 < SA ? rsa : rsb, at, (uint32_t)plane * 128 < left ? os[i] + k0 / 32 : kOOB);
+    for (int x = 0; x < SC_INSTR; ++x) {
+      const bool is_a = (wid + NW * x) * 64 < SA;
+      rsc[x] = is_a ? region(p.as + t.z * (int64_t)srow, mv * srow) : region(p.bs + brow * (int64_t)srow, nv * srow);
+    }
+  };
+  auto offsets = [&]() {
+    const bool last = ld_kt + 1 == nk;
+    la = (la0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
+    lb = (lb0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
+  };
+  auto dma = [&](int x) __attribute__((always_inline)) {  // load x of NDMA of the cursor's stage
+    if (x < A_INSTR) {
+      dma16(ra, ld_on ? smem_lds + ld_slot + (wid + NW * x) * 1024 : pad, la + (uint32_t)(8 * NW * x) * rowb);
+    } else if (x < A_INSTR + B_INSTR) {
+      const int i = x - A_INSTR;
+      const uint32_t row = (uint32_t)(SILU ? gate_up_row(8 * NW * i, F, 0) : 8 * NW * i);
+      dma16(rb, ld_on ? smem_lds + ld_slot + AT_B + (wid + NW * i) * 1024 : pad, lb + row * rowb);
+    } else {
+      const int i = x - A_INSTR - B_INSTR;
+      const bool real = (SC_LOADS % NW == 0 || wid + NW * i < SC_LOADS) && ld_on && (ld_kt & 1) == 0;
+      if (S == 2) {  // (no wait counts loads)
+        if (real) dma16(rsc[i], scales + ld_sbuf + (wid + NW * i) * 1024, ls0[i] + (uint32_t)ld_kt * 8);
+      } else {
+        dma16(rsc[i], real ? scales + ld_sbuf + (wid + NW * i) * 1024 : pad, real ? ls0[i] + (uint32_t)ld_kt * 8 : kOOB);
       }
-    };
+    }
+  };
+  auto advance = [&]() {
+    ld_slot = ld_slot + STAGE == S * STAGE ? 0 : ld_slot + STAGE;
+    if ((ld_kt & 1) || ld_kt + 1 == nk) ld_sbuf = ld_sbuf + SBUF == S * SBUF ? 0 : ld_sbuf + SBUF;
+    if (++ld_kt == nk) {
+      ld_kt = 0;
+      ++ld_i;
+      if ((ld_i & (kTiles - 1)) == 0) look_up(ld_i);
+      regions();
+    }
+    offsets();
+  };
 
-    f32x16_t acc[FM][FN];
+  // This lane's fragment addresses in slot 0: row lane % 32 of the wave's
+  // first row block, unit lane / 32; and its first scale words.
+  const uint32_t unit0 = (lane & 31) * kRowB + (((lane >> 5) ^ swz(lane & 31)) << 4);
+  const uint32_t fa0 = smem_lds + wm * WTM * kRowB + unit0, fb0 = smem_lds + AT_B + wn * WTN * kRowB + unit0;
+  const uint32_t sa0 = scales + (wm * WTM + (lane & 31)) * 16, sb0 = scales + (SA + wn * WTN + (lane & 31)) * 16;
+  const int sh = 8 * (lane >> 5);
+
+  i32x8_t fa[2][FM], fb[2][FN];
+  int wa[FM], wb[FN], sa[FM], sb[FN];  // scale words as read, and of the chunks in work
+  auto read = [&](uint32_t slot, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag(((fb0 + slot) ^ (32 * c)) + j * 32 * kRowB);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag(((fa0 + slot) ^ (32 * c)) + i * 32 * kRowB);
+  };
+  auto read_scales = [&](uint32_t at) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) wb[j] = (int)*(lds_u32_t*)(uintptr_t)(sb0 + at + j * 512);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) wa[i] = (int)*(lds_u32_t*)(uintptr_t)(sa0 + at + i * 512);
+  };
+  // Bytes h and h + 2 of the words (h = lane / 32) to bytes 0 and 2; none of
+  // them when bits is 0.
+  auto take_scales = [&](uint32_t bits) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = (int)__builtin_amdgcn_ubfe((uint32_t)wa[i], sh, bits);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sb[j] = (int)__builtin_amdgcn_ubfe((uint32_t)wb[j], sh, bits);
+  };
+  f32x16_t acc[FM][FN];
+  auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    const int64_t nk = (p.K + kKS - 1) / kKS;
-    // A wave whose rows all lie past the expert's end skips its MFMAs (it
-    // still loads and takes part in the barriers).
-    const bool active = m_end - m0 > wm * WTM;
+  };
+  // MFMA x of FM * FN of chunk c: byte 0 or 2 of the scale words.  B first:
+  // the result is the transposed tile.
+  auto mfma = [&](int c, int x) __attribute__((always_inline)) {
+    const int i = x / FN, j = x % FN;
+    if (c & 1)
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[1][j], fa[1][i], acc[i][j], 4, 4, 2, sb[j], 2, sa[i]);
+    else
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[0][j], fa[0][i], acc[i][j], 4, 4, 0, sb[j], 0, sa[i]);
+  };
+  // Keeps MFMAs x and x + 1 where they are written (they would be sunk behind
+  // the branches that follow).
+  auto pin = [&](int x) __attribute__((always_inline)) {
+    asm volatile("" : "+a"(acc[x / FN][x % FN]), "+a"(acc[(x + 1) / FN][(x + 1) % FN]));
+  };
+  // Chunk c's MFMAs with loads x0 .. x1 - 1 spread among them (all waves'
+  // loads at once would keep the address unit busy longer than the chunk).
+  auto chunk = [&](int c, int x0, int x1, bool issue) __attribute__((always_inline)) {
+    constexpr int G = FM * FN / 2;  // pairs of MFMAs
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s)
-      if (s < nk) load_stage(s, s);
-
-    for (int64_t kt = 0; kt < nk; ++kt) {
-      const int64_t ahead = nk - 1 - kt < S - 2 ? nk - 1 - kt : S - 2;
-      wait_steps_ahead<S - 2, NDMA>((int)ahead);
-      lds_barrier();
-      if (kt + S - 1 < nk) load_stage(kt + S - 1, (int)((kt + S - 1) % S));
-      const uint32_t slot = (uint32_t)__builtin_amdgcn_readfirstlane((int)(kt % S)) * STAGE;
-
-      if (active) {
-        i32x8_t fa[2][FM], fb[2][FN];
-        int sa[2][FM], sb[2][FN];  // by half of the stage
-        auto read = [&](int c) {
+    for (int g = 0; g < G; ++g) {
+      mfma(c, 2 * g);
+      mfma(c, 2 * g + 1);
+      pin(2 * g);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag(((fa0 + slot) ^ (32 * c)) + i * 4096);
-#pragma unroll
-          for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag(((fb0 + slot) ^ (32 * c)) + j * 4096);
-          if ((c & 1) == 0) {
-            // this half's scale words: byte 2 (c % 2) + h belongs to chunk c
-            const int sh = 8 * (lane >> 5);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-              sa[c >> 1][i] = (int)(*(lds_u32_t*)(uintptr_t)(sa0 + slot + (c >> 1) * PLANE + i * 128) >> sh);
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-              sb[c >> 1][j] = (int)(*(lds_u32_t*)(uintptr_t)(sb0 + slot + (c >> 1) * PLANE + j * 128) >> sh);
-          }
-        };
-        read(0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2 * (FM + FN), 0);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // of the waves sharing a SIMD the one behind in the stage issues first
-          if (c == 0) __builtin_amdgcn_s_setprio(1);
-          else if (c == 2) __builtin_amdgcn_s_setprio(0);
-          if (c + 1 < 4) read(c + 1);
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-              // B first: the result is the transposed tile (see the epilogue)
-              if (c & 1)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[1][j], fa[1][i], acc[i][j], 4, 4, 2,
-                                                                            sb[c >> 1][j], 2, sa[c >> 1][i]);
-              else
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[0][j], fa[0][i], acc[i][j], 4, 4, 0,
-                                                                            sb[c >> 1][j], 0, sa[c >> 1][i]);
-            }
-          if (c + 1 < 4)
-            interleave_mfma_ds<FM * FN, (FM + FN) * 2>();
-          else
-            interleave_mfma_ds<FM * FN, 0>();
-        }
-      }
+      for (int x = x0; x < x1; ++x)
+        if ((x - x0) * G / (x1 - x0) == g && issue) dma(x);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+
+  float tile_amax = 0.0f;
+  if (my_tiles > 0) {
+    look_up(0);
+    regions();
+    offsets();
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) {
+#pragma unroll
+      for (int x = 0; x < NDMA; ++x) dma(x);
+      advance();
+    }
+#pragma unroll
+    for (int x = 0; x < HALF; ++x) dma(x);
+    wait_vmcnt<AHEAD + HALF>();
+    lds_barrier();
+    read(0, 0);
+    read_scales(0);
+  }
+  uint32_t slot = 0, so = 0;  // ring slot and scale buffer (plus 8 for the second of two stages) of the stage in work
+  int fresh = 0, nst = 0;     // stages whose wait must allow for the last epilogue's nst stores
+  bool rest = true;           // the cursor's stage has loads left to issue
+#pragma unroll 1
+  for (int it = 0; it < my_tiles; ++it) {
+    const int4 cur = tile(it);
+    const int64_t m0 = cur.z, m_end = cur.w, n0 = (int64_t)cur.y * BN;
+    clear();
+#pragma unroll 1
+    for (int kt = 0; kt < nk; ++kt) {
+      const bool last = kt + 1 == nk;
+      // Each chunk's fragments are read under the MFMAs of the one before.
+      take_scales(24);
+      read(slot, 1);
+      chunk(0, HALF, NDMA, rest);
+      if (rest) advance();
+      rest = true;
+      read(slot, 2);
+      read_scales(so + 4);
+      chunk(1, 0, 0, false);
+      take_scales(last && p.K % kKS != 0 ? 0 : 24);
+      read(slot, 3);
+      chunk(2, 0, 0, false);
+      // The last chunk's fragments are in registers, so the slot is free once
+      // every wave is here; the next stage has landed.  Stores of an epilogue
+      // are younger than the loads of the S stages after it and need not have
+      // finished.
+      if (fresh == 0) {
+        wait_vmcnt<AHEAD>();
+      } else {
+        --fresh;
+        if (nst >= 32) wait_vmcnt<AHEAD + 32>();
+        else if (nst >= 16) wait_vmcnt<AHEAD + 16>();
+        else wait_vmcnt<AHEAD>();
+      }
+      lds_barrier();
+      slot = slot + STAGE == S * STAGE ? 0 : slot + STAGE;
+      if ((kt & 1) || last) {
+        so = (so & ~15u) + SBUF;
+        if (so == S * SBUF) so = 0;
+      } else {
+        so += 8;
+      }
+      read(slot, 0);
+      read_scales(so);
+      chunk(3, 0, HALF, true);
+    }
+    // The rest of the cursor's stage goes before the epilogue's stores.
+#pragma unroll
+    for (int x = HALF; x < NDMA; ++x) dma(x);
+    advance();
+    rest = false;
+    fresh = S - 1;
+    nst = 0;
 
     // Epilogue.  The B fragment is the MFMA's first operand, so lane l holds
     // output row l % 32 and, for g = 0..3, the four consecutive columns
-    // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Each wave passes its
-    // 32-row blocks through a private LDS region (the ring is free).
-    lds_barrier();
-    const int q = lane & 31, hh = lane >> 5;
+    // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Pieces of 16 rows and 64
+    // bytes pass through a staging area of the wave's own, so that a store
+    // writes 64 consecutive bytes of each row (which cost a CU what whole lines
+    // do, 20 cycles a KiB; 32-byte pieces cost 32); the next tile's stages land
+    // meanwhile.  LDS serves a wave in order: nothing is waited for between a
+    // piece's writes and reads but the data, and a block is stored while the
+    // next one passes.  Rows past the expert's end are past the store's region.
+    settle();
+    const int rq = lane & 15, hh = lane >> 5, half = (lane >> 4) & 1;  // this lane's row in its half
+    uint8_t* reg = smem + out;
+    const int pr = lane >> 2, pu = lane & 3;  // row and 16-byte unit of a piece on its way out
+    uint8_t* put_at = reg + rq * 64 + 8 * hh;
+    const uint8_t* get_at = reg + pr * 64 + ((pu ^ (pr >> 2)) << 4);
+    auto put = [&](const uint2 (&w)[4], int part) __attribute__((always_inline)) {
+      if (half == part) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) *reinterpret_cast<uint2*>(put_at + ((g ^ (rq >> 2)) << 4)) = w[g];
+      }
+    };
+    auto get = [&]() __attribute__((always_inline)) {
+      asm volatile("" ::: "memory");  // other lanes' writes
+      const i32x4_t v = *reinterpret_cast<const i32x4_t*>(get_at);
+      asm volatile("" ::: "memory");
+      return v;
+    };
+    const uint32_t tile_rows = (uint32_t)(cur.w - cur.z);
     if constexpr (SILU) {
-      constexpr int FW = WTN / 2;      // features per wave
-      constexpr int CH = FW / 8;       // 16-byte chunks per row and part
-      constexpr int PART = 32 * FW * 2;
-      static_assert(WTN % 64 == 0 && (CH & (CH - 1)) == 0 && NW * 2 * PART <= S * STAGE, "SiLU staging");
-      uint16_t* Yp = reinterpret_cast<uint16_t*>(p.c);
-      uint16_t* Hp = reinterpret_cast<uint16_t*>(p.h);
-      const int64_t F = p.N / 2, f0 = n0 / 2 + wn * FW;
-      uint8_t* reg = smem + wid * 2 * PART;
+      const uint32_t yb = (uint32_t)p.N * 2, hb = (uint32_t)F * 2, qb = (uint32_t)F / 2, eb = (uint32_t)F / 32;
+      uint16_t *Yp = reinterpret_cast<uint16_t*>(p.c), *Hp = reinterpret_cast<uint16_t*>(p.h);
+      const __amdgpu_buffer_rsrc_t ry = region(Yp + m0 * p.N, tile_rows * yb), rh = region(Hp + m0 * F, tile_rows * hb);
+      const __amdgpu_buffer_rsrc_t rq_ = region(p.hq + m0 * qb, tile_rows * qb), re = region(p.hs + m0 * eb, tile_rows * eb);
+      const uint32_t vy = pr * yb + pu * 16, vh = pr * hb + pu * 16, vq = pr * qb + pu * 4, ve = pu == 0 ? pr * eb : kOOB;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int64_t row0 = m0 + wm * WTM + i * 32;
-        if (row0 >= m_end) break;
 #pragma unroll
-        for (int jj = 0; jj < FN / 2; ++jj)
+        for (int j = 0; j < FN; j += 2) {
+          // Y1 is rounded to bf16 first: H is the gate of the stored values.
+          uint2 gv[4], uv[4];
+          i32x4_t o[2][3];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const f32x16_t& ga = acc[i][2 * jj];
-            const f32x16_t& ua = acc[i][2 * jj + 1];
-            const int off = q * (FW * 2) + (((jj * 4 + g) ^ (q & (CH - 1))) << 4) + 8 * hh;
-            *reinterpret_cast<uint2*>(reg + off) =
-                make_uint2(pack_bf16x2(ga[4 * g], ga[4 * g + 1]), pack_bf16x2(ga[4 * g + 2], ga[4 * g + 3]));
-            *reinterpret_cast<uint2*>(reg + PART + off) =
-                make_uint2(pack_bf16x2(ua[4 * g], ua[4 * g + 1]), pack_bf16x2(ua[4 * g + 2], ua[4 * g + 3]));
+            gv[g] = bf16x4(acc[i][j], g);
+            uv[g] = bf16x4(acc[i][j + 1], g);
+          }
+          if (Yp) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              put(gv, part);
+              o[part][0] = get();
+              put(uv, part);
+              o[part][1] = get();
+            }
           }
 #pragma unroll
-        for (int t = 0; t < 32 * CH / 64; ++t) {
-          const int r = t * (64 / CH) + lane / CH, ch = lane % CH;
-          const int off = r * (FW * 2) + ((ch ^ (r & (CH - 1))) << 4);
-          const int64_t row = row0 + r, f = f0 + ch * 8;
-          const uint4 vg = *reinterpret_cast<const uint4*>(reg + off);
-          const uint4 vu = *reinterpret_cast<const uint4*>(reg + PART + off);
-          const uint32_t gw[4] = {vg.x, vg.y, vg.z, vg.w}, uw[4] = {vu.x, vu.y, vu.z, vu.w};
-          float hv[8];
-          uint32_t hw[4];
+          for (int g = 0; g < 4; ++g)
+            gv[g] = make_uint2(pack_bf16x2(silu_gate(bf16_lo(gv[g].x), bf16_lo(uv[g].x)),
+                                           silu_gate(bf16_hi(gv[g].x), bf16_hi(uv[g].x))),
+                               pack_bf16x2(silu_gate(bf16_lo(gv[g].y), bf16_lo(uv[g].y)),
+                                           silu_gate(bf16_hi(gv[g].y), bf16_hi(uv[g].y))));
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            hw[w] = pack_bf16x2(silu_gate(bf16_lo(gw[w]), bf16_lo(uw[w])), silu_gate(bf16_hi(gw[w]), bf16_hi(uw[w])));
-            hv[2 * w] = bf16_lo(hw[w]);
-            hv[2 * w + 1] = bf16_hi(hw[w]);
+          for (int part = 0; part < 2; ++part) {
+            put(gv, part);
+            o[part][2] = get();
           }
-          const bool valid = row < m_end;
-          float am = 0.0f;
 #pragma unroll
-          for (int w = 0; w < 8; ++w) am = fmaxf(am, fabsf(hv[w]));
-          if (valid) {
-            tile_amax = fmaxf(tile_amax, am);
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t row = wm * WTM + i * 32 + part * 16, f = (uint32_t)n0 / 2 + wn * (WTN / 2) + j * 16;
             if (Yp) {
-              *reinterpret_cast<uint4*>(Yp + row * p.N + f) = vg;
-              *reinterpret_cast<uint4*>(Yp + row * p.N + F + f) = vu;
+              __builtin_amdgcn_raw_buffer_store_b128(o[part][0], ry, vy, row * yb + f * 2, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(o[part][1], ry, vy, row * yb + hb + f * 2, 0);
             }
-            if (Hp) *reinterpret_cast<uint4*>(Hp + row * F + f) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          }
-          if constexpr (EPI == EPI_SILU_Q) {
-            // lanes ch .. ch ^ 3 hold the 32 features of one block of one row
-            am = fmaxf(am, __shfl_xor(am, 1, 64));
-            am = fmaxf(am, __shfl_xor(am, 2, 64));
-            const int se = shared_exp<2>(am);
-            const uint32_t codes = encode8_e2m1(hv, se);
-            if (valid) {
-              *reinterpret_cast<uint32_t*>(p.hq + row * (F / 2) + f / 2) = codes;
-              if ((ch & 3) == 0) p.hs[row * (F / 32) + f / 32] = (uint8_t)(se + 127);
+            const i32x4_t h = o[part][2];
+            if (Hp) __builtin_amdgcn_raw_buffer_store_b128(h, rh, vh, row * hb + f * 2, 0);
+            if (EPI == EPI_SILU_Q || p.amax) {
+              // (rows past the end hold 0 or NaN, which the maximum passes over)
+              float hf[8], am = 0.0f;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                hf[2 * w] = bf16_lo((uint32_t)h[w]);
+                hf[2 * w + 1] = bf16_hi((uint32_t)h[w]);
+                am = fmaxf(am, fmaxf(fabsf(hf[2 * w]), fabsf(hf[2 * w + 1])));
+              }
+              tile_amax = fmaxf(tile_amax, am);
+              if constexpr (EPI == EPI_SILU_Q) {
+                // four lanes hold the 32 features of one block of one row
+                am = fmaxf(am, __shfl_xor(am, 1, 64));
+                am = fmaxf(am, __shfl_xor(am, 2, 64));
+                const int se = shared_exp<2>(am);
+                __builtin_amdgcn_raw_buffer_store_b32(encode8_e2m1(hf, se), rq_, vq, row * qb + f / 2, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32, 0);
+              }
             }
           }
+          nst += 2 * ((Yp ? 2 : 0) + (Hp ? 1 : 0) + (EPI == EPI_SILU_Q ? 2 : 0));
+          __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
         }
       }
     } else {
-      constexpr int EB = OUT32 ? 4 : 2;        // bytes per element
-      constexpr int CH = WTN * EB / 16;        // 16-byte chunks per row
-      constexpr int REGION = 32 * WTN * EB;
-      static_assert(NW * REGION <= S * STAGE && (CH & (CH - 1)) == 0, "epilogue staging");
-      uint8_t* reg = smem + wid * REGION;
-      const int64_t col0 = n0 + wn * WTN;
+      constexpr uint32_t EB = OUT32 ? 4 : 2;  // bytes per element
+      const uint32_t cb = (uint32_t)p.N * EB;
+      const __amdgpu_buffer_rsrc_t rc = region(reinterpret_cast<uint8_t*>(p.c) + m0 * cb, tile_rows * cb);
+      const uint32_t vc = pr * cb + pu * 16;
+      i32x4_t v[2][OUT32 ? 2 : 1], before[2][OUT32 ? 2 : 1];
+      auto store = [&](int x, const i32x4_t (&w)[2][OUT32 ? 2 : 1]) __attribute__((always_inline)) {  // block x
+        const uint32_t row = wm * WTM + (x / FN) * 32, col = (uint32_t)n0 + wn * WTN + (x % FN) * 32;
+        if (col < (uint32_t)p.N) {  // (N % 32 == 0)
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int64_t row0 = m0 + wm * WTM + i * 32;
-        if (row0 >= m_end) break;
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+            for (uint32_t q = 0; q < EB / 2; ++q)
+              __builtin_amdgcn_raw_buffer_store_b128(w[part][q], rc, vc, (row + part * 16) * cb + col * EB + q * 64, 0);
+          nst += EB;
+        }
+      };
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x16_t& a = acc[i][j];
-            if constexpr (OUT32) {
-              const int ch = j * 8 + 2 * g + hh;
-              *reinterpret_cast<float4*>(reg + q * (WTN * 4) + ((ch ^ (q & (CH - 1))) << 4)) =
-                  make_float4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]);
-            } else {
-              const int ch = j * 4 + g;
-              *reinterpret_cast<uint2*>(reg + q * (WTN * 2) + ((ch ^ (q & (CH - 1))) << 4) + 8 * hh) =
-                  make_uint2(pack_bf16x2(a[4 * g], a[4 * g + 1]), pack_bf16x2(a[4 * g + 2], a[4 * g + 3]));
+      for (int x = 0; x < FM * FN; ++x) {
+        const f32x16_t& a = acc[x / FN][x % FN];
+        if constexpr (OUT32) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // 16 columns at a time
+            float4 w[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int b = 8 * q + 4 * g;
+              w[g] = make_float4(element(a[b]), element(a[b + 1]), element(a[b + 2]), element(a[b + 3]));
+            }
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (half == part) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                  *reinterpret_cast<float4*>(reg + rq * 64 + (((2 * g + hh) ^ (rq >> 2)) << 4)) = w[g];
+              }
+              v[part][q] = get();
             }
           }
-#pragma unroll 4
-        for (int t = 0; t < 32 * CH / 64; ++t) {
-          const int r = t * (64 / CH) + lane / CH, ch = lane % CH;
-          const uint4 v = *reinterpret_cast<const uint4*>(reg + r * (WTN * EB) + ((ch ^ (r & (CH - 1))) << 4));
-          const int64_t row = row0 + r, col = col0 + ch * (16 / EB);
-          if (row < m_end && col < p.N)
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.c) + (row * p.N + col) * EB) = v;
+        } else {
+          uint2 w[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) w[g] = bf16x4(a, g);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            put(w, part);
+            v[part][0] = get();
+          }
         }
+        if (x > 0) store(x - 1, before);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (uint32_t q = 0; q < EB / 2; ++q) before[part][q] = v[part][q];
+        __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
       }
+      store(FM * FN - 1, before);
     }
   }
 
+  wait_vmcnt<0>();  // no load may land after the workgroup's LDS is given away
   if constexpr (SILU) {
     if (p.amax) {
       __shared__ float red[NW];
@@ -410,7 +630,7 @@ int launch_tiles(const Params& p0, hipStream_t st) {
 // ring deep; with many it is the MFMAs and the LDS reads that feed them.
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
-  if (p.M <= 32 * (int64_t)p.E) return launch_tiles<32, 256, 1, 4, 4, EPI, OUT32>(p, st);
+  if (p.M <= 32 * (int64_t)p.E) return launch_tiles<32, 256, 1, 4, 3, EPI, OUT32>(p, st);
   if (p.M <= 96 * (int64_t)p.E) return launch_tiles<64, 256, 1, 4, 3, EPI, OUT32>(p, st);
   return launch_tiles<256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
@@ -423,7 +643,7 @@ int check_operands(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, c
   if (M_total > 0 && N > 0 && K > 0 && (!a_q || !a_s || !b_q || !b_s)) return NVFP4MOE_EINVAL;
   if (K % 128 != 0 || N % 32 != 0) return NVFP4MOE_ESHAPE;
   // a tile's operand region is read through 32-bit offsets
-  if (M_total > 0x7FFFFFFFLL || N > 0x7FFFFFFFLL || K > (1 << 22)) return NVFP4MOE_ESHAPE;
+  if (M_total > 0x7FFFFFFFLL || N > (1 << 20) || K > (1 << 22)) return NVFP4MOE_ESHAPE;
   if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(expert_offsets, 4))
     return NVFP4MOE_ESHAPE;
   p = Params{};
