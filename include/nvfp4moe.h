@@ -623,7 +623,7 @@ int grouped_gemm_w4a8_silu_gate_mx(const uint8_t* a_q, const uint8_t* a_s, const
  *   b_q [E][N][K/2],    b_s [E][N][K/32]     (mx_quantize E2M1)
  *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).
  * K % 128 == 0, N % 32 == 0; a_q, b_q, c 16-byte aligned, a_s, b_s 4-byte
- * aligned; M_total, N < 2^31, K <= 2^22.  K == 0 gives zeros.  Errors: EINVAL
+ * aligned; M_total < 2^31, N <= 2^20, K <= 2^22.  K == 0 gives zeros.  Errors: EINVAL
  * (NULL, negative, bad dtype), ESHAPE (shape and alignment rules).
  */
 int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,
@@ -639,7 +639,7 @@ int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_
  *   y1 [M_total][2F] bf16 or NULL, h [M_total][F] bf16 or NULL, amax_out fp32
  *   [1] or NULL (max |H|); q_h [M_total][F/2] (4-byte aligned) and s_h
  *   [M_total][F/32], both or neither; h or q_h is required.
- * F % 128 == 0, K % 128 == 0, F * K < 2^31.  Other rules and errors as
+ * F % 128 == 0, F <= 2^19, K % 128 == 0, F * K < 2^31.  Other rules and errors as
  * grouped_gemm_mxfp4.
  */
 int grouped_gemm_mxfp4_silu_gate(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,

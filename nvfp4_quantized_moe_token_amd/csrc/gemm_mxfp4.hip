@@ -16,13 +16,28 @@
 // across the ends of tiles; one wait and one workgroup barrier per stage.
 //
 // Scheduling is that of the other grouped GEMMs: a persistent grid, each
-// workgroup finds its tiles from the device offsets, tiles in contiguous
-// ranges per XCD with the row blocks of an expert next to each other.
+// workgroup finds its tiles from the device offsets (up to 64 of them at a
+// time), tiles in contiguous ranges per XCD with the row blocks of an expert
+// next to each other.
 //
-// Epilogues.  Plain: the tile leaves through LDS, so that every store writes
-// whole lines.  SiLU gate: tiles hold matching gate and up columns; Y1 is
-// rounded to bf16 and H = silu(G) * U is taken from the rounded values, as the
-// standalone kernel does; optionally H is quantized to MXFP4 on the way out.
+// Epilogues.  The tile leaves through LDS in pieces of 64 bytes per row.  SiLU
+// gate: tiles hold matching gate and up columns; Y1 is rounded to bf16 and
+// H = silu(G) * U is taken from the rounded values, as the standalone kernel
+// does; optionally H is quantized to MXFP4 on the way out.
+//
+// Bounds and measurements (us of the kernel; 128 experts, top-8).  A 256x256
+// tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS per MFMA (half of the
+// LDS's rate at the MFMAs' peak); 64x64 waves (128x256 and 256x128 tiles, or
+// two workgroups per CU) read a third more and lose more than finer tiles save:
+// gate+up of 8192 tokens 209 against 216 to 244.  Stages of 128 elements and a
+// ring of four are no faster either (155 against 138 for a dense 4096 x 8192 x
+// 8192 product, 4.0 PFLOP/s): lines are then read in halves.
+//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      210
+//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         243
+//   gate+up, 512 tokens    51 (4.2 TB/s)     down, 512 tokens       30
+// Without their stores the first two take 170 and 161, without any epilogue 129
+// and 117: a workgroup's stores and SiLU are not hidden behind its products,
+// since its accumulators fill the registers and its stages the LDS.
 #include "gemm_tiles.hpp"
 #include "mx_codec.hpp"
 
@@ -53,7 +68,8 @@ constexpr int kTiles = 64;          // tiles looked up at a time
 constexpr int kWaveOut = 1024;      // bytes of a wave's epilogue staging: 16 rows of 64 bytes
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
-typedef __attribute__((address_space(3))) const uint32_t lds_u32_t;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) const u32x2_t lds_u32x2_t;
 
 // A fragment: 16 bytes of codes (the instruction's operand has room for 32).
 __device__ __forceinline__ i32x8_t frag(uint32_t at) {
@@ -104,7 +120,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p
   constexpr int NDMA = A_INSTR + B_INSTR + SC_INSTR, HALF = (NDMA + 1) / 2;
   static_assert(A_LOADS % NW == 0 && B_LOADS % NW == 0 && NW % 4 == 0, "the rows of a wave's loads agree modulo 32");
   constexpr int AHEAD = (S - 2) * NDMA;  // loads of this wave that are younger than the stage waited for
-  static_assert(S >= 2 && AHEAD <= 31, "pipeline depth");
+  static_assert(S >= 2 && AHEAD + 32 <= 63, "pipeline depth");
 
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * (STAGE + SBUF) + NW * kWaveOut + 1024];
   __shared__ __attribute__((aligned(16))) int4 s_tile[2 * kTiles];  // this workgroup's tiles: expert, n-tile, first and end row
@@ -287,7 +303,8 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p
   const int sh = 8 * (lane >> 5);
 
   i32x8_t fa[2][FM], fb[2][FN];
-  int wa[FM], wb[FN], sa[FM], sb[FN];  // scale words as read, and of the chunks in work
+  u32x2_t wa[FM], wb[FN];  // scale words of the next stage as read
+  int sa[FM], sb[FN];      // of the chunks in work
   auto read = [&](uint32_t slot, int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag(((fb0 + slot) ^ (32 * c)) + j * 32 * kRowB);
@@ -296,17 +313,17 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p
   };
   auto read_scales = [&](uint32_t at) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) wb[j] = (int)*(lds_u32_t*)(uintptr_t)(sb0 + at + j * 512);
+    for (int j = 0; j < FN; ++j) wb[j] = *(lds_u32x2_t*)(uintptr_t)(sb0 + at + j * 512);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) wa[i] = (int)*(lds_u32_t*)(uintptr_t)(sa0 + at + i * 512);
+    for (int i = 0; i < FM; ++i) wa[i] = *(lds_u32x2_t*)(uintptr_t)(sa0 + at + i * 512);
   };
-  // Bytes h and h + 2 of the words (h = lane / 32) to bytes 0 and 2; none of
-  // them when bits is 0.
-  auto take_scales = [&](uint32_t bits) __attribute__((always_inline)) {
+  // Bytes h and h + 2 of word w of a stage's two (h = lane / 32) to bytes 0 and
+  // 2; none of them when bits is 0.
+  auto take_scales = [&](int w, uint32_t bits) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sa[i] = (int)__builtin_amdgcn_ubfe((uint32_t)wa[i], sh, bits);
+    for (int i = 0; i < FM; ++i) sa[i] = (int)__builtin_amdgcn_ubfe(wa[i][w], sh, bits);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) sb[j] = (int)__builtin_amdgcn_ubfe((uint32_t)wb[j], sh, bits);
+    for (int j = 0; j < FN; ++j) sb[j] = (int)__builtin_amdgcn_ubfe(wb[j][w], sh, bits);
   };
   f32x16_t acc[FM][FN];
   auto clear = [&]() {
@@ -379,15 +396,14 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p
     for (int kt = 0; kt < nk; ++kt) {
       const bool last = kt + 1 == nk;
       // Each chunk's fragments are read under the MFMAs of the one before.
-      take_scales(24);
+      take_scales(0, 24);
       read(slot, 1);
       chunk(0, HALF, NDMA, rest);
       if (rest) advance();
       rest = true;
       read(slot, 2);
-      read_scales(so + 4);
       chunk(1, 0, 0, false);
-      take_scales(last && p.K % kKS != 0 ? 0 : 24);
+      take_scales(1, last && p.K % kKS != 0 ? 0 : 24);
       read(slot, 3);
       chunk(2, 0, 0, false);
       // The last chunk's fragments are in registers, so the slot is free once

@@ -247,6 +247,32 @@ def test_full_size_sampled():
     _check(to_np(y1[torch.from_numpy(rows).cuda()]), ref, ab, d["D"], False)
 
 
+@pytest.mark.parametrize("E,N", [(260, 16384), (600, 8192)])
+def test_more_tiles_than_a_workgroup_looks_up_at_once(E, N):
+    """16640 and 19200 tiles of 32 x 256, over 64 per workgroup of a 256-CU
+    grid, with the offsets in LDS and in global memory; sampled experts."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    g = torch.Generator(device="cuda").manual_seed(E)
+    K = 128
+    counts = torch.randint(1, 4, (E,), generator=g, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = counts.cumsum(0)
+    M = int(off[-1])
+
+    def u8(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.uint8)
+
+    aq, as_, bq, bs = u8(0, 256, M, K // 2), u8(120, 135, M, K // 32), u8(0, 256, E, N, K // 2), u8(120, 135, E, N, K // 32)
+    got = to_np(ops.grouped_gemm_mxfp4(aq, as_, bq, bs, off))
+    offs = to_np(off)
+    for e in [0, 1, E // 3, E // 2, E - 2, E - 1]:
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        a = mx.dequantize(to_np(aq[lo:hi]), to_np(as_[lo:hi]), "e2m1").astype(np.float64)
+        b = mx.dequantize(to_np(bq[e]), to_np(bs[e]), "e2m1").astype(np.float64)
+        _check(got[lo:hi], a @ b.T, np.abs(a) @ np.abs(b).T, K, False)
+
+
 def test_two_streams_and_captured_replays():
     require_gpu()
     from nvfp4_quantized_moe_token_amd import moe_layer

@@ -140,7 +140,7 @@ def _bad(fn, args, cases):
 
 def test_router_refusals(lib):
     ws = lib.moe_router_workspace_size(100, 128, 8)
-    assert ws == 7 * 128 * 4 and lib.moe_router_workspace_size(-1, 128, 8) == 0   # 16 tokens per workgroup
+    assert ws == 2 * 128 * 4 and lib.moe_router_workspace_size(-1, 128, 8) == 0   # 64 tokens per workgroup
     assert lib.moe_router_workspace_size(1 << 20, 128, 8) == 512 * 128 * 4
     args = [FAKE, 0, 100, 128, 8, None, 0, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, ws, None]
     _bad(lib.moe_router, args, [
@@ -178,6 +178,15 @@ def test_mxfp4_refusals(lib):
     _bad(lib.grouped_gemm_mxfp4_silu_gate, args, [
         ({7: -1}, -1), ({13: None}, -1), ({12: None}, -1), ({10: None, 12: None, 13: None}, -1), ({7: 64}, -2),
         ({8: 64}, -2), ({7: 1 << 13, 8: 1 << 18}, -2), ({9: FAKE + 8}, -2), ({12: FAKE + 2}, -2)])
+
+
+def test_mxfp4_width_limit(lib):
+    # a tile's output region is addressed in 32 bits
+    _bad(lib.grouped_gemm_mxfp4, [FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 256, FAKE, 0, None],
+         [({7: (1 << 20) + 32}, -2)])
+    _bad(lib.grouped_gemm_mxfp4_silu_gate,
+         [FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 128, 256, FAKE, FAKE, FAKE, FAKE, FAKE, None],
+         [({7: (1 << 19) + 128, 8: 128}, -2)])
 
 
 def test_adamw_refusals(lib):
