@@ -141,7 +141,7 @@ def _bad(fn, args, cases):
 def test_router_refusals(lib):
     ws = lib.moe_router_workspace_size(100, 128, 8)
     assert ws == 2 * 128 * 4 and lib.moe_router_workspace_size(-1, 128, 8) == 0   # 64 tokens per workgroup
-    assert lib.moe_router_workspace_size(1 << 20, 128, 8) == 512 * 128 * 4
+    assert lib.moe_router_workspace_size(1 << 20, 128, 8) == 256 * 128 * 4
     args = [FAKE, 0, 100, 128, 8, None, 0, 1.0, FAKE, FAKE, FAKE, FAKE, FAKE, ws, None]
     _bad(lib.moe_router, args, [
         ({2: -1}, -1), ({3: 0}, -1), ({4: 0}, -1), ({1: 2}, -1), ({6: 2}, -1), ({0: None}, -1), ({8: None}, -1),
