@@ -879,9 +879,14 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const uint8_t* __restr
 template <int IN, int Y, int OUT, bool DY, bool DW>
 void launch_combine_bwd(const void* dout, const void* y, const int32_t* dest, const float* w, const int32_t* offsets,
                         int E, int64_t T, int k, int64_t D, void* dy, float* dw, float* amax_out, hipStream_t st) {
-  // Four waves per token while one wave each would leave compute units idle
-  // (fewer than 8 waves per CU).
-  const bool split = T < (int64_t)device_cu_count() * 8;
+  // Four waves per token where each has elements to take, one wave otherwise:
+  // a rule on D alone, so that a token's sums do not depend on the batch.
+  // Kernel us with one wave | four, bf16, k = 8:
+  //   D  512: T 1024  7.5 | 11.6, 8192  33 |  83
+  //   D 1024: T 1024 11.6 | 13.6, 8192  60 | 102
+  //   D 2048: T   16  9.9 |  5.2, 512 17.3 | 9.6, 4096 78 | 65, 8192 138 | 132 (4.3 TB/s)
+  //   D 4096: T 8192  279 |  244
+  const bool split = D > 3 * 512;
   int64_t grid = split ? T : cdiv(T, 4);
   const int64_t cap = amax_out ? kAmaxGrid : kMaxStreamGrid;
   if (grid > cap) grid = cap;
