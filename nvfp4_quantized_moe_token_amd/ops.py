@@ -145,18 +145,18 @@ def moe_router(logits, k, bias=None, score=ROUTER_TOPK_SOFTMAX, scale=1.0, want_
     _need(lse, "lse", torch.float32, T)
     _need(prob_sum, "prob_sum", torch.float32, E)
     with _on_device(logits, bias, topk_ids, topk_w, lse, prob_sum, workspace):
-        dev, f32 = logits.device, torch.float32
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None else topk_ids
-        topk_w = torch.empty((T, k), dtype=f32, device=dev) if topk_w is None else topk_w
+        new, f32 = logits.new_empty, torch.float32
+        topk_ids = new((T, k), dtype=torch.int32) if topk_ids is None else topk_ids
+        topk_w = new((T, k), dtype=f32) if topk_w is None else topk_w
         if lse is None and want_lse:
-            lse = torch.empty((T,), dtype=f32, device=dev)
+            lse = new((T,), dtype=f32)
         if prob_sum is None and want_prob_sum:
-            prob_sum = torch.empty((E,), dtype=f32, device=dev)
+            prob_sum = new((E,), dtype=f32)
         lib = _lib.load()
         ws_bytes = 0
         if prob_sum is not None:
             if workspace is None:
-                workspace = torch.empty((lib.moe_router_workspace_size(T, E, k),), dtype=torch.uint8, device=dev)
+                workspace = new((lib.moe_router_workspace_size(T, E, k),), dtype=torch.uint8)
             ws_bytes = workspace.numel() * workspace.element_size()
         rc = lib.moe_router(_ptr(logits), _DT[logits.dtype], T, E, k, _ptr(bias), score, scale, _ptr(topk_ids),
                             _ptr(topk_w), _ptr(lse), _ptr(prob_sum), _ptr(workspace), ws_bytes, _stream())
@@ -180,7 +180,7 @@ def moe_router_bwd(logits, topk_ids, d_topk_w, score=ROUTER_TOPK_SOFTMAX, scale=
     _need(out, "out", _FLOATS, T, E)
     with _on_device(logits, topk_ids, d_topk_w, lse, d_lse, d_prob_sum, out):
         if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype if out_dtype is None else out_dtype, device=logits.device)
+            out = logits.new_empty((T, E), dtype=out_dtype)
         rc = _lib.load().moe_router_bwd(_ptr(logits), _DT[logits.dtype], T, E, k, _ptr(topk_ids), score, scale,
                                         _ptr(d_topk_w), _ptr(lse), _ptr(d_lse), _ptr(d_prob_sum), _ptr(out),
                                         _DT[out.dtype], _stream())
@@ -405,9 +405,9 @@ def moe_unpermute_bwd(dout, y_perm, dest, offsets, k, topk_w=None, dy_perm=None,
     _need(amax_out, "amax_out", torch.float32, 1)
     with _on_device(dout, y_perm, dest, offsets, topk_w, dy_perm, d_topk_w, amax_out):
         if dy_perm is None and want_dy:
-            dy_perm = torch.empty((R, D), dtype=dout.dtype if dy_dtype is None else dy_dtype, device=dout.device)
+            dy_perm = dout.new_empty((R, D), dtype=dy_dtype)
         if d_topk_w is None and want_dw:
-            d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+            d_topk_w = dout.new_empty((T, k), dtype=torch.float32)
         rc = _lib.load().moe_unpermute_bwd(
             _ptr(dout), _DT[dout.dtype], _ptr(y_perm), _DT[y_perm.dtype] if y_perm is not None else BF16, _ptr(dest),
             _ptr(topk_w), _ptr(offsets), offsets.numel() - 1, T, k, D, _ptr(dy_perm),
@@ -634,7 +634,7 @@ def grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets, out=None, out_dtype=torch.fl
     M, K, E, N = _mxfp4_operands(a_q, a_s, b_q, b_s, offsets)
     _need(out, "out", _FLOATS, M, N)
     with _on_device(a_q, a_s, b_q, b_s, offsets, out):
-        out = torch.empty((M, N), dtype=out_dtype, device=a_q.device) if out is None else out
+        out = a_q.new_empty((M, N), dtype=out_dtype) if out is None else out
         rc = _lib.load().grouped_gemm_mxfp4(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M, N, K,
                                             _ptr(out), _DT[out.dtype], _stream())
     _check("grouped_gemm_mxfp4", rc)
@@ -659,12 +659,12 @@ def grouped_gemm_mxfp4_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=T
     _need(s_h, "s_h", u8, M, F // 32)
     want_q = want_q or q_h is not None or s_h is not None
     with _on_device(a_q, a_s, b_q, b_s, offsets, y1, h, amax_out, q_h, s_h):
-        dev = a_q.device
-        y1 = torch.empty((M, N), dtype=bf, device=dev) if y1 is None and want_y1 else y1
-        h = torch.empty((M, F), dtype=bf, device=dev) if h is None and want_h else h
+        new = a_q.new_empty
+        y1 = new((M, N), dtype=bf) if y1 is None and want_y1 else y1
+        h = new((M, F), dtype=bf) if h is None and want_h else h
         if want_q:
-            q_h = torch.empty((M, F // 2), dtype=u8, device=dev) if q_h is None else q_h
-            s_h = torch.empty((M, F // 32), dtype=u8, device=dev) if s_h is None else s_h
+            q_h = new((M, F // 2), dtype=u8) if q_h is None else q_h
+            s_h = new((M, F // 32), dtype=u8) if s_h is None else s_h
         rc = _lib.load().grouped_gemm_mxfp4_silu_gate(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M,
                                                       F, K, _ptr(y1), _ptr(h), _ptr(amax_out), _ptr(q_h), _ptr(s_h),
                                                       _stream())

@@ -96,19 +96,27 @@ class AdamW:
         still counts)."""
         grads = list(grads)
         gdt = grads[0].dtype if grads and grads[0] is not None else None
-        if gdt not in _FLOATS or len(grads) != len(self._numel) or any(
-                g is None or g.dtype is not gdt or g.numel() != n for g, n in zip(grads, self._numel)):
+        dev = self.params[0].get_device()
+        ok = gdt in _FLOATS and len(grads) == len(self._numel)
+        if ok:
+            for d, g, n in zip(self._entries, grads, self._numel):
+                if (g is None or g.dtype is not gdt or g.numel() != n or g.get_device() != dev
+                        or not g.is_contiguous()):
+                    ok = False
+                    break
+                d.grad = g.data_ptr()
+        if not ok:  # say which
             self._same_sizes("grads", grads, _FLOATS, required=True)
-            raise ValueError("grads: one dtype for all")
+            if any(g.dtype != gdt for g in grads):
+                raise ValueError("grads: one dtype for all")
+            _on_device(self.params[0], *grads)
         for name, t, dt in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
             if t is not None and (t.dtype != dt or t.numel() != 1):
                 raise ValueError("%s: one %s on the GPU" % (name, dt))
-        with _on_device(self.params[0], grad_scale, skip, *grads):
+        with _on_device(self.params[0], grad_scale, skip):
             self.steps += 1
             if self.step_dev is not None:
                 self.step_dev.add_(1)
-            for d, g in zip(self._entries, grads):
-                d.grad = g.data_ptr()
             rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[gdt],
                                         self.state_bits, self.lr, self.betas[0], self.betas[1], self.eps,
                                         self.weight_decay, self.steps, _ptr(self.step_dev), _ptr(self.lr_dev),
