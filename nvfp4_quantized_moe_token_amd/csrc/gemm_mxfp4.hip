@@ -644,16 +644,24 @@ int launch_tiles(const Params& p0, hipStream_t st) {
 // Tiles by the mean rows per expert (the host does not know more): with few
 // rows the work is reading the weights, so the row block is small and the ring
 // three stages deep; with many it is the MFMAs, the LDS reads that feed them
-// and the stores.  Measured kernel times in us, 128 experts, gate+up
-// (768 features, K = 2048) | down (N = 2048, K = 768), row blocks of 32, 64
-// and 256, by rows per expert:
-//   16: 45.4 48.8 67.5               96: 96.9 75.7 76.6 | 54.2 45.2 44.7
-//   32: 56.1 51.0 68.8 | 30.3 30.2 41.0    128: 119.7 91.6 80.9 | 67.8 53.2 46.8
-//   64: 74.6 65.2 72.6 | 41.5 36.2 42.8
+// and the stores.  The row block is one that most experts' rows fit in, up to
+// 256, where blocks of 192 need two.  Measured kernel times in us, 128 experts,
+// gate+up (768 features, K = 2048) and down (N = 2048, K = 768):
+//   rows      gate+up, blocks of           down, blocks of
+//             32     64    192    256      32     64    192    256
+//    16     45.4   48.8          67.5
+//    32     56.1   51.0          68.8    30.3   30.2          41.0
+//    64     74.6   64.9   67.2   71.9    41.5   35.6   38.4   42.0
+//    80            72.5   69.2   73.9           43.3   39.9   43.4
+//    96     96.9   75.2   72.1   76.6    54.2   44.1   40.6   44.5
+//   128    119.7   91.6   75.8   79.5    67.8   53.2   43.2   46.3
+//   160                   79.9   85.5                  47.3   49.3
+//   208                  118.7   96.1                  67.9   55.6
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   if (p.M <= 24 * (int64_t)p.E) return launch_tiles<32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 96 * (int64_t)p.E) return launch_tiles<64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<192, 256, 2, 4, 2, EPI, OUT32>(p, st);
   return launch_tiles<256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 

@@ -49,10 +49,13 @@ def _check(got, ref, ab, K, bf16):
 
 
 COUNTS = [
-    ([0, 1, 300, 0, 37, 256, 511], 96, 256),      # 256-row tiles: empty, one-row, tails; N not a tile multiple
+    ([0, 1, 300, 0, 37, 256, 511], 96, 256),      # 192-row tiles: empty, one-row, tails; N not a tile multiple
+    ([0, 1, 600, 0, 37, 512, 511], 96, 256),      # 256-row tiles: the same
+    ([300, 0, 400], 288, 128),                    # and a single half stage
     ([700], 512, 384),                            # one expert (dense), K % 256 == 128
     ([300, 0, 129], 288, 128),                    # a single half stage
     ([64, 65, 0, 1, 33, 90], 256, 640),           # 64-row tiles
+    ([100, 192, 0, 193, 31, 160], 544, 384),
     ([3] * 40 + [257, 0], 1056, 512),             # small tiles: many small experts and one large
     ([1], 32, 2048),                              # one row
     ([0, 2, 0, 0, 5, 32, 31, 1], 544, 768),
@@ -115,7 +118,9 @@ def test_gemm_empty_and_zero_width():
 
 
 @pytest.mark.parametrize("counts,F,K", [([0, 5, 260, 1, 513, 64], 256, 384), ([700, 33], 384, 512),
-                                        ([1, 0, 2, 30, 7], 128, 256), ([70, 0, 95, 60], 128, 640), ([4], 768, 2048)])
+                                        ([1, 0, 2, 30, 7], 128, 256), ([70, 0, 95, 60], 128, 640),
+                                        ([150, 193, 40], 256, 384), ([0, 5, 560, 1, 813, 64], 256, 384),
+                                        ([4], 768, 2048)])
 def test_silu_epilogue_equals_the_separate_steps(counts, F, K):
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
