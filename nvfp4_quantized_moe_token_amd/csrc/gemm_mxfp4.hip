@@ -35,6 +35,7 @@
 //   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      210
 //   down, 16384 tokens, skewed routing (N = 2048, K = 768)         243
 //   gate+up, 512 tokens    51 (4.2 TB/s)     down, 512 tokens       30
+//   gate+up weights, 16 tokens (214 MB)                       28 (7.5 TB/s)
 // Without their stores the first two take 170 and 161, without any epilogue 129
 // and 117: a workgroup's stores and SiLU are not hidden behind its products,
 // since its accumulators fill the registers and its stages the LDS.

@@ -28,9 +28,9 @@
 // instructions for the four tokens of a wave: 3 maxima over 8 registers (three
 // at a time), 4 across the lanes, 16 to find the winner's expert, 4 across, 16
 // to take it out.  16 tokens 3.9 us (a launch and one trip to memory); 16384
-// tokens with lse and sums 11.0 us (0.86 TB/s), the last sum 3.8 us, where 512
-// smaller workgroups and floating-point keys took 11.6 and 10.6.  The gradient
-// of 8192 tokens 5.8 us (1.5 TB/s).
+// tokens with lse and sums 10 to 11 us (0.9 TB/s), the last sum 2 to 4 us,
+// where 512 smaller workgroups and floating-point keys took 11.6 and 10.6.  The
+// gradient of 8192 tokens 5.6 us (1.6 TB/s).
 #include <type_traits>
 
 #include "common.hpp"

@@ -237,3 +237,26 @@ def test_refusals():
     with pytest.raises(ValueError):
         optim.AdamW([torch.zeros(100, 2, device="cuda").t()])
     assert opt.steps == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_refused_step_changes_nothing(bits):
+    """Gradients on the host, missing, strided or of the wrong number are
+    refused; the step count and the weights stay, and the next step counts on."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import optim
+    shapes = [(0,), (), (300,)]
+    params = [torch.ones(s, device="cuda") for s in shapes]
+    good = [torch.ones(s, device="cuda") for s in shapes]
+    opt = optim.AdamW(params, state_bits=bits, lr=0.1, weight_decay=0.0)
+    bad = [[good[0], torch.ones(()), good[2]], good[:2], [good[0], None, good[2]],
+           [good[0], good[1], torch.ones(600, device="cuda")[::2]], [good[0], good[1].bfloat16(), good[2]]]
+    for grads in bad:
+        with pytest.raises(ValueError):
+            opt.step(grads)
+    torch.cuda.synchronize()
+    assert opt.steps == 0 and all((p == 1).all() for p in params)
+    opt.step(good)
+    torch.cuda.synchronize()
+    # m / sqrt(v) of a first step is 1: the weights move by the rate, to a few roundings
+    assert opt.steps == 1 and all((p - 0.9).abs().max() < 1e-6 for p in params if p.numel())

@@ -232,6 +232,20 @@ def test_forward_stage_by_stage(T, k, E, D, F, drop):
     assert (np.abs(to_np(buf.out) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * bound + 1e-30).all()
 
 
+def test_forward_without_tokens():
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import moe_layer
+    k, E, D, F = 2, 8, 256, 128
+    dev = torch.device("cuda")
+    gu = moe_layer.quantize_expert_weights_mx(torch.ones(E, 2 * F, D, dtype=torch.bfloat16, device=dev))
+    dn = moe_layer.quantize_expert_weights_mx(torch.ones(E, D, F, dtype=torch.bfloat16, device=dev))
+    buf = moe_layer.BuffersMXFP4(0, k, E, D, F, dev)
+    moe_layer.forward_mxfp4(torch.zeros(0, D, dtype=torch.bfloat16, device=dev),
+                            torch.zeros(0, k, dtype=torch.int32, device=dev), torch.zeros(0, k, device=dev), gu, dn, buf)
+    torch.cuda.synchronize()
+    assert buf.out.shape == (0, D)
+
+
 def test_full_size_sampled():
     """The 8192-token gate+up product (65536 rows, 128 experts, 2F = 1536, K =
     2048), rows of four experts against the oracle."""
