@@ -623,7 +623,7 @@ int grouped_gemm_w4a8_silu_gate_mx(const uint8_t* a_q, const uint8_t* a_s, const
  *   b_q [E][N][K/2],    b_s [E][N][K/32]     (mx_quantize E2M1)
  *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).
  * K % 128 == 0, N % 32 == 0; a_q, b_q, c 16-byte aligned, a_s, b_s 4-byte
- * aligned; M_total < 2^31, N <= 2^20, K <= 2^22.  K == 0 gives zeros.  Errors: EINVAL
+ * aligned; M_total < 2^31 - 256, N <= 2^20, K <= 2^22.  K == 0 gives zeros.  Errors: EINVAL
  * (NULL, negative, bad dtype), ESHAPE (shape and alignment rules).
  */
 int grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,

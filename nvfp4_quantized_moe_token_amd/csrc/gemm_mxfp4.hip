@@ -188,10 +188,12 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void mxfp4_kernel(Params p
         int lo, hi;
         expert_range(off_lds, e, p.M, lo, hi);
         const uint32_t in = L - (uint32_t)s_blk[e] * nt, cnt = (uint32_t)(s_blk[e + 1] - s_blk[e]);
-        t.x = e;
-        t.y = (int)(in / cnt);
-        t.z = lo + (int)(in % cnt) * BM;
-        t.w = hi - t.z < BM ? hi : t.z + BM;
+        if (in < cnt * nt) {  // (always, with ascending offsets)
+          t.x = e;
+          t.y = (int)(in / cnt);
+          t.z = lo + (int)(in % cnt) * BM;
+          t.w = hi - t.z < BM ? hi : t.z + BM;
+        }
       }
     } else {
       for (int i = 0; i < kTiles && i0 + i < my_tiles; ++i) {
@@ -674,7 +676,7 @@ int check_operands(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, c
   if (M_total > 0 && N > 0 && K > 0 && (!a_q || !a_s || !b_q || !b_s)) return NVFP4MOE_EINVAL;
   if (K % 128 != 0 || N % 32 != 0) return NVFP4MOE_ESHAPE;
   // a tile's operand region is read through 32-bit offsets
-  if (M_total > 0x7FFFFFFFLL || N > (1 << 20) || K > (1 << 22)) return NVFP4MOE_ESHAPE;
+  if (M_total >= 0x7FFFFF00LL || N > (1 << 20) || K > (1 << 22)) return NVFP4MOE_ESHAPE;
   if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(expert_offsets, 4))
     return NVFP4MOE_ESHAPE;
   p = Params{};

@@ -183,7 +183,7 @@ def test_mxfp4_refusals(lib):
 def test_mxfp4_width_limit(lib):
     # a tile's output region is addressed in 32 bits
     _bad(lib.grouped_gemm_mxfp4, [FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 64, 256, FAKE, 0, None],
-         [({7: (1 << 20) + 32}, -2)])
+         [({7: (1 << 20) + 32}, -2), ({6: (1 << 31) - 256}, -2)])
     _bad(lib.grouped_gemm_mxfp4_silu_gate,
          [FAKE, FAKE, FAKE, FAKE, FAKE, 4, 64, 128, 256, FAKE, FAKE, FAKE, FAKE, FAKE, None],
          [({7: (1 << 19) + 128, 8: 128}, -2)])
