@@ -6,6 +6,7 @@ takes; every step of the arithmetic runs in the HIP kernel.
 """
 
 import ctypes
+import types
 
 import torch
 
@@ -13,6 +14,11 @@ from . import _lib
 from .ops import _DT, _FLOATS, _check, _on_device, _ptr, _stream
 
 BLOCK = _lib.ADAMW_BLOCK
+_WORDS = ctypes.sizeof(_lib.AdamWTensor) // 8  # 8-byte fields of the C record
+
+# Methods called over whole lists: half the time of a loop of bound calls.
+_PTR, _NUMEL, _DEVICE, _CONTIGUOUS = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device,
+                                      torch.Tensor.is_contiguous)
 
 
 class AdamW:
@@ -32,7 +38,7 @@ class AdamW:
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params_bf16=None,
                  state_bits=32, seed=0, step=0, state=None, capturable=False):
-        self.params = list(params)
+        self._params = tuple(params)
         if not self.params:
             raise ValueError("AdamW needs at least one parameter")
         if state_bits not in (8, 32):
@@ -40,33 +46,72 @@ class AdamW:
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits, self.seed, self.steps = state_bits, seed & 0xFFFFFFFF, step
         n = len(self.params)
-        dt = self.params[0].dtype
-        if dt not in (torch.float32, torch.bfloat16) or any(p.dtype != dt for p in self.params):
-            raise ValueError("AdamW takes parameters of one dtype, fp32 or bf16")
-        self.params_bf16 = [None] * n if params_bf16 is None else list(params_bf16)
-        self._same_sizes("params_bf16", self.params_bf16, torch.bfloat16)
-        if dt != torch.float32 and any(c is not None for c in self.params_bf16):
-            raise ValueError("params_bf16 goes with fp32 parameters")
+        self._params_bf16 = (None,) * n if params_bf16 is None else tuple(params_bf16)
+        self._state = {}
+        self._validate()
+        names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
         if state is None:
             state = self._new_state()
-        names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
-        self.state = {k: list(state[k]) for k in names}
-        for k in names[:2]:
-            self._same_sizes(k, self.state[k], torch.uint8 if state_bits == 8 else torch.float32, required=True)
-        for k in names[2:]:
-            self._same_sizes(k, self.state[k], torch.float32, required=True, blocks=True)
-        tensors = self.params + self.params_bf16 + [t for k in names for t in self.state[k]]
-        _on_device(*tensors)
+        self._state = {k: tuple(state[k]) for k in names}
+        self._list = (_lib.AdamWTensor * n)()
+        self._words = (ctypes.c_void_p * (_WORDS * n)).from_buffer(self._list)  # its fields, _WORDS per tensor
+        self._held = [t for t in (*self.params, *self.params_bf16, *(t for k in names for t in self._state[k]))
+                      if t is not None]
+        self._take()
         dev = self.params[0].device
         self.step_dev = torch.full((1,), step, dtype=torch.int64, device=dev) if capturable else None
         self.lr_dev = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
-        self._list = (_lib.AdamWTensor * n)()
-        self._entries = list(self._list)  # views of it, made once
-        for i, (d, p, c) in enumerate(zip(self._entries, self.params, self.params_bf16)):
-            d.param, d.param_bf16, d.n = _ptr(p), _ptr(c), p.numel()
-            for k in names:
-                setattr(d, k, _ptr(self.state[k][i]))
-        self._numel = [p.numel() for p in self.params]
+
+    # The tensors are fixed for good (their storage is not): another set is
+    # another optimizer.
+    @property
+    def params(self):
+        return self._params
+
+    @property
+    def params_bf16(self):
+        return self._params_bf16
+
+    @property
+    def state(self):
+        return types.MappingProxyType(self._state)
+
+    def _validate(self):
+        """Refuses tensors of the wrong dtype, size, device or layout."""
+        dt = self.params[0].dtype
+        if dt not in (torch.float32, torch.bfloat16) or any(p.dtype != dt for p in self.params):
+            raise ValueError("AdamW takes parameters of one dtype, fp32 or bf16")
+        self._same_sizes("params_bf16", self.params_bf16, torch.bfloat16)
+        if dt != torch.float32 and any(c is not None for c in self.params_bf16):
+            raise ValueError("params_bf16 goes with fp32 parameters")
+        moments = torch.uint8 if self.state_bits == 8 else torch.float32
+        for k, ts in self._state.items():
+            scales = k.endswith("_scale")
+            self._same_sizes(k, ts, torch.float32 if scales else moments, required=True, blocks=scales)
+        _on_device(*self.params, *self.params_bf16, *(t for ts in self._state.values() for t in ts))
+
+    def _take(self):
+        """Checks the tensors and lists their addresses for the library."""
+        self._known = None
+        self._validate()
+        self._numel = list(map(_NUMEL, self.params))
+        lists = dict(self._state, param=self.params, param_bf16=self.params_bf16)
+        for i, d in enumerate(self._list):
+            d.n = self._numel[i]
+            for k, ts in lists.items():
+                setattr(d, k, _ptr(ts[i]))
+        self._known = self._addresses()
+
+    def _addresses(self):
+        # With the parameters' extents: weights moved to the host and back in
+        # another type can land where they were.
+        return list(map(_PTR, self._held)) + [p.nbytes for p in self.params]
+
+    def _refresh(self):
+        """A tensor's storage may be another since the last call (``p.data =``,
+        weights moved away and back): then the new one is checked and taken."""
+        if self._addresses() != self._known:
+            self._take()
 
     def _same_sizes(self, name, ts, dtype, required=False, blocks=False):
         if len(ts) != len(self.params):
@@ -95,21 +140,20 @@ class AdamW:
         skip (int32 [1], device): nothing changes when it is not 0 (the step
         still counts)."""
         grads = list(grads)
-        gdt = grads[0].dtype if grads and grads[0] is not None else None
-        dev = self.params[0].get_device()
-        ok = gdt in _FLOATS and len(grads) == len(self._numel)
-        if ok:
-            for d, g, n in zip(self._entries, grads, self._numel):
-                if (g is None or g.dtype is not gdt or g.numel() != n or g.get_device() != dev
-                        or not g.is_contiguous()):
-                    ok = False
-                    break
-                d.grad = g.data_ptr()
+        self._refresh()
+        try:
+            dts = {g.dtype for g in grads}
+            gdt = dts.pop() if len(dts) == 1 else None
+            ok = (gdt in _FLOATS and list(map(_NUMEL, grads)) == self._numel and all(map(_CONTIGUOUS, grads))
+                  and set(map(_DEVICE, grads)) == {self.params[0].get_device()})
+        except (AttributeError, TypeError):  # not a tensor
+            ok = False
         if not ok:  # say which
             self._same_sizes("grads", grads, _FLOATS, required=True)
-            if any(g.dtype != gdt for g in grads):
+            if any(g.dtype != grads[0].dtype for g in grads):
                 raise ValueError("grads: one dtype for all")
             _on_device(self.params[0], *grads)
+        self._words[1::_WORDS] = list(map(_PTR, grads))
         for name, t, dt in (("grad_scale", grad_scale, torch.float32), ("skip", skip, torch.int32)):
             if t is not None and (t.dtype != dt or t.numel() != 1):
                 raise ValueError("%s: one %s on the GPU" % (name, dt))
@@ -130,13 +174,14 @@ class AdamW:
         if self.state_bits == 32:
             m, v = self.state["exp_avg"], self.state["exp_avg_sq"]
             if out is None:
-                return m, v
+                return list(m), list(v)
             for d, s in zip((*out[0], *out[1]), (*m, *v)):
                 d.copy_(s)
             return out
         if out is None:
             out = tuple([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
                         for _ in range(2))
+        self._refresh()
         for t in out:
             self._same_sizes("out", t, torch.float32, required=True)
         with _on_device(self.params[0], *out[0], *out[1]):

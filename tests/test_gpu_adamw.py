@@ -260,3 +260,34 @@ def test_a_refused_step_changes_nothing(bits):
     torch.cuda.synchronize()
     # m / sqrt(v) of a first step is 1: the weights move by the rate, to a few roundings
     assert opt.steps == 1 and all((p - 0.9).abs().max() < 1e-6 for p in params if p.numel())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_weights_moved_away_and_back(bits):
+    """Parameters, copies and moments whose storage was replaced between steps:
+    the next step works on the new one, and the old one stays as it was."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import optim
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+    sizes = [300, 4097]
+    ps, gs = ([torch.randn(n, generator=gen, device="cuda") for n in sizes] for _ in range(2))
+    a, b = (optim.AdamW([p.clone() for p in ps], params_bf16=[p.to(BF16) for p in ps], state_bits=bits, seed=2, **HYPER)
+            for _ in range(2))
+    a.step(gs)
+    b.step(gs)
+    held = [*a.params, *a.params_bf16, *(t for ts in a.state.values() for t in ts)]
+    old = [t.data for t in held]
+    was = [t.clone() for t in old]
+    for t in held:
+        t.data = t.data.clone()
+    a.step(gs)
+    b.step(gs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(old, was))
+    for x, y in zip(held, [*b.params, *b.params_bf16, *(t for ts in b.state.values() for t in ts)]):
+        assert torch.equal(x, y)
+    a.params[0].data = a.params[0].data.cpu()
+    with pytest.raises(ValueError):
+        a.step(gs)
+    assert a.steps == 2

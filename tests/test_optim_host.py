@@ -1,0 +1,114 @@
+"""The optimizer's host side, without a GPU: the library's call is recorded
+instead of made, on tensors in host memory."""
+
+import contextlib
+
+import pytest
+import torch
+
+from nvfp4_quantized_moe_token_amd import _lib, optim
+
+FIELDS = [n for n, _ in _lib.AdamWTensor._fields_]
+
+
+class Library:
+    """Records the calls; answers with `rc`."""
+
+    def __init__(self):
+        self.rc, self.calls = _lib.OK, []
+
+    def _record(self, name, args):
+        self.calls.append((name, [{f: getattr(d, f) for f in FIELDS} for d in args[0]], args))
+        return self.rc
+
+    def adamw_step(self, *args):
+        return self._record("step", args)
+
+    def adamw_read_state(self, *args):
+        return self._record("read", args)
+
+    def nvfp4moe_status_string(self, rc):
+        return b"refused"
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+
+    def on_device(*ts):
+        if any(t is not None and not t.is_contiguous() for t in ts):
+            raise ValueError("contiguous tensors")
+        return contextlib.nullcontext()
+
+    monkeypatch.setattr(_lib, "load", lambda *a: lib)
+    monkeypatch.setattr(optim, "_on_device", on_device)
+    monkeypatch.setattr(optim, "_stream", lambda: None)
+    return lib
+
+
+def _held(opt, i):
+    """Name in the library's record -> tensor, of parameter i."""
+    return dict({k: t[i] for k, t in opt.state.items()}, param=opt.params[i], param_bf16=opt.params_bf16[i])
+
+
+def _check_record(record, opt):
+    for i, d in enumerate(record):
+        assert d["n"] == opt.params[i].numel()
+        for name, t in _held(opt, i).items():
+            assert d[name] == (None if t is None else t.data_ptr()), (i, name)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_replaced_storage_is_noticed(library, bits):
+    """`.data =` on a parameter, a copy or a moment: the next call takes the
+    new address (the old storage may be anyone's by then)."""
+    params = [torch.zeros(n) for n in (5, 600, 1)]
+    copies = [torch.zeros(5, dtype=torch.bfloat16), None, torch.zeros(1, dtype=torch.bfloat16)]
+    opt = optim.AdamW(params, params_bf16=copies, state_bits=bits)
+    grads = [torch.zeros(p.shape) for p in params]
+    opt.step(grads)
+    _check_record(library.calls[-1][1], opt)
+    assert [d["grad"] for d in library.calls[-1][1]] == [g.data_ptr() for g in grads]
+    for name in _held(opt, 0):
+        for i in (2, 0):
+            t = _held(opt, i)[name]
+            t.data = t.data.clone()
+            opt.step(grads)
+            _check_record(library.calls[-1][1], opt)
+    if bits == 8:
+        opt.state["avg_scale"][1].data = torch.zeros(3)
+        opt.state_values()
+        assert library.calls[-1][0] == "read"
+        _check_record(library.calls[-1][1], opt)
+
+
+def test_replaced_storage_is_checked(library):
+    def fresh():
+        return optim.AdamW([torch.zeros(64), torch.zeros(8)])
+
+    for change in (lambda o: setattr(o.params[0], "data", torch.zeros(65)),
+                   lambda o: setattr(o.params[1], "data", torch.zeros(8, dtype=torch.bfloat16)),
+                   lambda o: setattr(o.params[0], "data", torch.zeros(64, 2)[:, 0]),
+                   lambda o: setattr(o.state["exp_avg"][0], "data", torch.zeros(32)),
+                   lambda o: setattr(o.state["exp_avg_sq"][1], "data", torch.zeros(8, dtype=torch.float16))):
+        opt = fresh()
+        change(opt)
+        before = len(library.calls)
+        for _ in range(2):                     # refused again, not forgotten
+            with pytest.raises(ValueError):
+                opt.step([torch.zeros(p.shape) for p in opt.params])
+        assert len(library.calls) == before and opt.steps == 0
+
+
+def test_tensors_cannot_be_assigned(library):
+    """The library works on the tensors the optimizer was made with; an
+    assignment that it would not see is refused."""
+    opt = optim.AdamW([torch.zeros(4)], state_bits=8)
+    for name in ("params", "params_bf16", "state"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, [torch.zeros(4)])
+    for seq in (opt.params, opt.params_bf16, *opt.state.values()):
+        with pytest.raises(TypeError):
+            seq[0] = torch.zeros(4)
+    with pytest.raises(TypeError):
+        opt.state["exp_avg"] = (torch.zeros(4),)
