@@ -339,8 +339,11 @@ class Learner:
         self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
 
     def forward(self, x):
-        """The layer's output [T, D] (bf16) for x [T, D] bf16; the router's
-        lse and prob_sum stay in ``lse`` and ``prob_sum`` for its losses."""
+        """The layer's output [T, D] (bf16, the layer's own buffer) for x [T, D]
+        bf16; the router's lse and prob_sum stay in ``lse`` and ``prob_sum`` for
+        its losses.  x is kept, not copied: ``backward`` reads it again."""
+        ops._need(x, "x", torch.bfloat16, self.logits.shape[0], self.w_r.shape[1])
+        ops._on_device(x, self.w_r)
         self.x = x
         ops.grouped_gemm_bf16(ops.NT, x, self.w_r.unsqueeze(0), self.one_group, out=self.logits)
         ops.moe_router(self.logits, self.k, bias=self.router_bias, score=self.score, topk_ids=self.topk_ids,

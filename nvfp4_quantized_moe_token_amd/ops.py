@@ -674,20 +674,24 @@ def grouped_gemm_mxfp4_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=T
 
 def grouped_gemm_bf16(layout, a, b, offsets, num_experts=None, out=None, out_dtype=torch.float32, accumulate=False):
     """Grouped BF16 GEMM; layout NT / NN / TN as in the C header."""
-    _dev(a, b, offsets, out)
-    M = a.shape[0]
+    _need(a, "a", torch.bfloat16, None, None)
+    M, K = a.shape
     E = offsets.numel() - 1 if num_experts is None else num_experts
     if layout == NT:
-        K, N = a.shape[1], b.shape[1]
+        _need(b, "b", torch.bfloat16, None, None, K)
+        N = b.shape[1]
         shape = (M, N)
     elif layout == NN:
-        K, N = a.shape[1], b.shape[2]
+        _need(b, "b", torch.bfloat16, None, K, None)
+        N = b.shape[2]
         shape = (M, N)
     elif layout == TN:
-        K, N = a.shape[1], b.shape[1]
+        _need(b, "b", torch.bfloat16, M, None)
+        N = b.shape[1]
         shape = (E, K, N)
     else:
         raise ValueError("layout must be NT, NN or TN")
+    _dev(a, b, offsets, out)
     out = torch.empty(shape, dtype=out_dtype, device=a.device) if out is None else out
     rc = _lib.load().grouped_gemm_bf16(layout, _ptr(a), _ptr(b), _ptr(offsets), E, M, N, K, _ptr(out),
                                        _DT[out.dtype], int(bool(accumulate)), None, 0, _stream())
@@ -698,6 +702,8 @@ def grouped_gemm_bf16(layout, a, b, offsets, num_experts=None, out=None, out_dty
 def grouped_gemm_bf16_tn_gather(a, b, src, k, offsets, num_experts=None, out=None, out_dtype=torch.float32,
                                 accumulate=False):
     """TN weight gradient with B rows gathered: C_e = sum_{r in e} a[r]^T b[src[r] // k]."""
+    _need(a, "a", torch.bfloat16, None, None)
+    _need(b, "b", torch.bfloat16, None, None)
     _dev(a, b, src, offsets, out)
     M, K = a.shape
     N = b.shape[1]
