@@ -43,6 +43,8 @@ class AdamW:
             raise ValueError("AdamW needs at least one parameter")
         if state_bits not in (8, 32):
             raise ValueError("state_bits: 8 or 32, got %r" % (state_bits,))
+        if not (all(0.0 <= b < 1.0 for b in betas) and len(betas) == 2 and eps >= 0.0 and step >= 0):
+            raise ValueError("AdamW: two betas in [0, 1), eps and step not negative; got %r, %r, %r" % (betas, eps, step))
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits, self.seed, self.steps = state_bits, seed & 0xFFFFFFFF, step
         n = len(self.params)
@@ -158,14 +160,15 @@ class AdamW:
             if t is not None and (t.dtype != dt or t.numel() != 1):
                 raise ValueError("%s: one %s on the GPU" % (name, dt))
         with _on_device(self.params[0], grad_scale, skip):
-            self.steps += 1
-            if self.step_dev is not None:
-                self.step_dev.add_(1)
+            t_dev = None if self.step_dev is None else self.step_dev + 1
             rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[gdt],
                                         self.state_bits, self.lr, self.betas[0], self.betas[1], self.eps,
-                                        self.weight_decay, self.steps, _ptr(self.step_dev), _ptr(self.lr_dev),
+                                        self.weight_decay, self.steps + 1, _ptr(t_dev), _ptr(self.lr_dev),
                                         _ptr(grad_scale), _ptr(skip), self.seed, _stream())
-        _check("adamw_step", rc)
+            _check("adamw_step", rc)
+            self.steps += 1  # (a step that was refused does not count)
+            if self.step_dev is not None:
+                self.step_dev.add_(1)
 
     def state_values(self, out=None):
         """The moments as fp32 tensors, two lists (exp_avg, exp_avg_sq):

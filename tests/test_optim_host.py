@@ -112,3 +112,27 @@ def test_tensors_cannot_be_assigned(library):
             seq[0] = torch.zeros(4)
     with pytest.raises(TypeError):
         opt.state["exp_avg"] = (torch.zeros(4),)
+
+
+@pytest.mark.parametrize("kw", [dict(betas=(0.9, 1.0)), dict(betas=(-0.1, 0.9)), dict(betas=(0.9,)),
+                                dict(betas=(float("nan"), 0.9)), dict(eps=-1e-8), dict(eps=float("nan")),
+                                dict(step=-1)])
+def test_hyperparameters_are_checked_at_once(library, kw):
+    with pytest.raises(ValueError):
+        optim.AdamW([torch.zeros(4)], **kw)
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_step_that_the_library_refuses_does_not_count(library, capturable):
+    opt = optim.AdamW([torch.zeros(4)], step=5, capturable=capturable)
+    grads = [torch.zeros(4)]
+    opt.step(grads)
+    library.rc = _lib.EINVAL
+    for _ in range(3):
+        with pytest.raises(RuntimeError):
+            opt.step(grads)
+    assert opt.steps == 6 and (not capturable or opt.step_dev.item() == 6)
+    library.rc = _lib.OK
+    opt.step(grads)
+    assert opt.steps == 7 and (not capturable or opt.step_dev.item() == 7)
+    assert library.calls[-1][2][10] == 7
