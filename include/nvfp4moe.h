@@ -735,7 +735,8 @@ int silu_gate_bwd(const void* y1, const void* dh, int64_t R, int64_t F, void* dy
  *                to 0.  The update uses the moments before rounding.  Zero
  *                bytes and scales are zero moments.
  *   step, step_dev  t >= 1 on the host, or a device int64 [1] (then step is
- *                not read): a captured graph counts its own steps.
+ *                not read): a captured graph counts its own steps.  t numbers
+ *                the updates: after a skipped call it is the same again.
  *   lr, lr_dev   likewise (fp32 [1] on the device, NULL: lr).
  *   grad_scale   fp32 [1] device or NULL (1): a clipping or unscaling factor.
  *   skip         int32 [1] device or NULL: when not 0 nothing is changed.

@@ -28,7 +28,7 @@ class AdamW:
     params_bf16: for each fp32 parameter a bf16 tensor that every step
     overwrites with its rounded value (or None, for all or for one).
     state_bits: 32, or 8 (codes with one fp32 scale per 256 elements, rounded
-    stochastically).  seed: of that rounding.  step: steps already taken.
+    stochastically).  seed: of that rounding.  step: updates already made.
     state: moments to go on with, a dict of lists: exp_avg, exp_avg_sq, and
     for 8 bits avg_scale, avg_sq_scale (kept, not copied); zeros otherwise.
     capturable: the step count and the learning rate live on the device
@@ -63,6 +63,10 @@ class AdamW:
         dev = self.params[0].device
         self.step_dev = torch.full((1,), step, dtype=torch.int64, device=dev) if capturable else None
         self.lr_dev = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
+        # 1 less the steps skipped: added to the steps taken it is the number
+        # of the next update.  Only the GPU knows it once a flag was given.
+        self._next = torch.ones((1,), dtype=torch.int64, device=dev)
+        self._skips = capturable  # (a captured step goes on after an eager one was skipped)
 
     # The tensors are fixed for good (their storage is not): another set is
     # another optimizer.
@@ -139,8 +143,9 @@ class AdamW:
     def step(self, grads, grad_scale=None, skip=None):
         """One step with one gradient per parameter (fp32 or bf16, all the
         same).  grad_scale (fp32 [1], device): a factor on every gradient.
-        skip (int32 [1], device): nothing changes when it is not 0 (the step
-        still counts)."""
+        skip (int32 [1], device): nothing changes when it is not 0.  The step
+        counts in ``steps`` and ``step_dev``, but the bias corrections (and
+        the rounding's bits) go by the updates made: see ``updates``."""
         grads = list(grads)
         self._refresh()
         try:
@@ -160,7 +165,8 @@ class AdamW:
             if t is not None and (t.dtype != dt or t.numel() != 1):
                 raise ValueError("%s: one %s on the GPU" % (name, dt))
         with _on_device(self.params[0], grad_scale, skip):
-            t_dev = None if self.step_dev is None else self.step_dev + 1
+            self._skips = self._skips or skip is not None
+            t_dev = self._next + (self.steps if self.step_dev is None else self.step_dev) if self._skips else None
             rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[gdt],
                                         self.state_bits, self.lr, self.betas[0], self.betas[1], self.eps,
                                         self.weight_decay, self.steps + 1, _ptr(t_dev), _ptr(self.lr_dev),
@@ -169,6 +175,14 @@ class AdamW:
             self.steps += 1  # (a step that was refused does not count)
             if self.step_dev is not None:
                 self.step_dev.add_(1)
+            if skip is not None:
+                self._next.add_(skip.view(1).ne(0), alpha=-1)
+
+    def updates(self):
+        """The steps that were not skipped (those of ``step=`` included): what
+        ``step=`` of an optimizer that goes on with these moments takes.
+        Waits for the GPU."""
+        return (self.steps if self.step_dev is None else self.step_dev.item()) + self._next.item() - 1
 
     def state_values(self, out=None):
         """The moments as fp32 tensors, two lists (exp_avg, exp_avg_sq):

@@ -291,3 +291,45 @@ def test_weights_moved_away_and_back(bits):
     with pytest.raises(ValueError):
         a.step(gs)
     assert a.steps == 2
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capturable", [False, True])
+def test_skipped_steps_leave_no_trace(bits, capturable):
+    """Steps with and without the skip flag set, eager and replayed: the same
+    bits as an optimizer that was never asked for the skipped ones."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import optim
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12)
+    p0 = torch.randn(3000, generator=gen, device="cuda")
+    gs = [torch.randn(3000, generator=gen, device="cuda") for _ in range(6)]
+    a, b = (optim.AdamW([p0.clone()], state_bits=bits, seed=4, capturable=c, **HYPER) for c in (capturable, False))
+    skip = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def same():
+        torch.cuda.synchronize()
+        assert torch.equal(a.params[0], b.params[0]) and a.updates() == b.steps
+        for s in a.state:
+            assert torch.equal(a.state[s][0], b.state[s][0])
+
+    for g, flag in zip(gs, (1, 1, 0, 1, None, 0)):
+        skip.fill_(flag or 0)
+        a.step([g], skip=None if flag is None else skip)
+        if not flag:
+            b.step([g])
+        same()
+    if not capturable:
+        return
+    x = gs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step([x], skip=skip)
+    a.steps -= 1                            # (captured, not run)
+    for g, flag in zip(gs, (0, 1, 0, 1, 1, 0)):
+        skip.fill_(flag)
+        x.copy_(g)
+        graph.replay()
+        if not flag:
+            b.step([g])
+        same()

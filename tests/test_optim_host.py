@@ -2,6 +2,7 @@
 instead of made, on tensors in host memory."""
 
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -136,3 +137,25 @@ def test_a_step_that_the_library_refuses_does_not_count(library, capturable):
     opt.step(grads)
     assert opt.steps == 7 and (not capturable or opt.step_dev.item() == 7)
     assert library.calls[-1][2][10] == 7
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_bias_corrections_go_by_the_updates_made(library, monkeypatch, capturable):
+    """A skipped step leaves the moments, so t, the number of updates in them,
+    stays too; the steps taken count on."""
+    numbers = []
+
+    def record(*args):
+        numbers.append(args[10] if args[11] is None else ctypes.c_int64.from_address(args[11]).value)
+        return _lib.OK
+
+    monkeypatch.setattr(Library, "adamw_step", lambda self, *args: record(*args))
+    opt = optim.AdamW([torch.zeros(4)], step=10, capturable=capturable)
+    grads, updates = [torch.zeros(4)], 10
+    for flag in (None, 0, 1, None, 5, -1, 0, None):
+        opt.step(grads, skip=None if flag is None else torch.tensor([flag], dtype=torch.int32))
+        if not flag:
+            updates += 1
+            assert numbers[-1] == updates
+        assert opt.updates() == updates
+    assert opt.steps == 18 and (not capturable or opt.step_dev.item() == 18)
