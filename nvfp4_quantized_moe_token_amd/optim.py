@@ -19,6 +19,7 @@ _WORDS = ctypes.sizeof(_lib.AdamWTensor) // 8  # 8-byte fields of the C record
 # Methods called over whole lists: half the time of a loop of bound calls.
 _PTR, _NUMEL, _DEVICE, _CONTIGUOUS = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device,
                                       torch.Tensor.is_contiguous)
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 class AdamW:
@@ -165,6 +166,9 @@ class AdamW:
             if t is not None and (t.dtype != dt or t.numel() != 1):
                 raise ValueError("%s: one %s on the GPU" % (name, dt))
         with _on_device(self.params[0], grad_scale, skip):
+            if self.step_dev is None and _capturing():
+                raise RuntimeError("AdamW: a step that is captured needs capturable=True (replays would all be step %d)"
+                                   % (self.steps + 1))
             self._skips = self._skips or skip is not None
             t_dev = self._next + (self.steps if self.step_dev is None else self.step_dev) if self._skips else None
             rc = _lib.load().adamw_step(self._list, len(grads), _DT[self.params[0].dtype], _DT[gdt],

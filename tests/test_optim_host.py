@@ -44,6 +44,7 @@ def library(monkeypatch):
     monkeypatch.setattr(_lib, "load", lambda *a: lib)
     monkeypatch.setattr(optim, "_on_device", on_device)
     monkeypatch.setattr(optim, "_stream", lambda: None)
+    monkeypatch.setattr(optim, "_capturing", lambda: False, raising=False)
     return lib
 
 
@@ -159,3 +160,15 @@ def test_bias_corrections_go_by_the_updates_made(library, monkeypatch, capturabl
             assert numbers[-1] == updates
         assert opt.updates() == updates
     assert opt.steps == 18 and (not capturable or opt.step_dev.item() == 18)
+
+
+def test_a_captured_step_counts_or_is_refused(library, monkeypatch):
+    """Replays of a step whose number was taken on the host would all have the
+    same bias corrections and the same random bits."""
+    opts = [optim.AdamW([torch.zeros(4)], capturable=c) for c in (False, True)]
+    monkeypatch.setattr(optim, "_capturing", lambda: True, raising=False)
+    with pytest.raises(RuntimeError):
+        opts[0].step([torch.zeros(4)])
+    assert library.calls == [] and opts[0].steps == 0
+    opts[1].step([torch.zeros(4)])
+    assert library.calls[-1][2][11] is not None
