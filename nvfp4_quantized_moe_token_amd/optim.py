@@ -95,7 +95,14 @@ class AdamW:
         for k, ts in self._state.items():
             scales = k.endswith("_scale")
             self._same_sizes(k, ts, torch.float32 if scales else moments, required=True, blocks=scales)
-        _on_device(*self.params, *self.params_bf16, *(t for ts in self._state.values() for t in ts))
+        held = [t for t in (*self.params, *self.params_bf16, *(t for ts in self._state.values() for t in ts))
+                if t is not None]
+        _on_device(*held)
+        # A tensor given twice (shared weights) would be updated by two
+        # workgroups at once.
+        ends = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in held if t.numel())
+        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+            raise ValueError("AdamW: two of the tensors overlap in memory (shared parameters go in once)")
 
     def _take(self):
         """Checks the tensors and lists their addresses for the library."""

@@ -172,3 +172,22 @@ def test_a_captured_step_counts_or_is_refused(library, monkeypatch):
     assert library.calls == [] and opts[0].steps == 0
     opts[1].step([torch.zeros(4)])
     assert library.calls[-1][2][11] is not None
+
+
+def test_overlapping_tensors_are_refused(library):
+    """Two workgroups would update the same elements at the same time."""
+    p, q = torch.zeros(1000), torch.zeros(1000)
+    zeros = [torch.zeros(1000), torch.zeros(1000)]
+    for bad in (lambda: optim.AdamW([p, q, p]),
+                lambda: optim.AdamW([p[:600], p[599:]]),
+                lambda: optim.AdamW([p, q], state=dict(exp_avg=zeros, exp_avg_sq=[zeros[1], torch.zeros(1000)])),
+                lambda: optim.AdamW([p, q], state=dict(exp_avg=[zeros[0], p], exp_avg_sq=[zeros[1], torch.zeros(1000)]))):
+        with pytest.raises(ValueError):
+            bad()
+    opt = optim.AdamW([p[:600], p[600:], p[:0], q])     # neighbours, and an empty view of one
+    opt.step([torch.zeros(t.shape) for t in opt.params])
+    opt = optim.AdamW([p, torch.zeros(700)])
+    opt.params[1].data = p.data[300:]
+    with pytest.raises(ValueError):
+        opt.step([torch.zeros(t.shape) for t in opt.params])
+    assert len(library.calls) == 1
