@@ -132,9 +132,8 @@ __device__ __forceinline__ uint32_t encode_m(float x, float s, uint32_t r) {
 }
 __device__ __forceinline__ uint32_t encode_v(float x, float s, uint32_t r) {
   if (!finite(x)) return 255u;
-  if (!(s > 0.0f)) return 0u;
-  const float y = x / s;
-  if (!(y > 0.0f)) return 0u;
+  if (!(x > 0.0f)) return 0u;  // (then s, the block's maximum, is positive too)
+  const float y = x / s;       // 0 when x is below 2^-149 of s: the lowest code all the same
   const int c = (int)((__float_as_uint(y) + (r << 4)) >> 20) - 762;
   return (uint32_t)(c < 1 ? 1 : c > 254 ? 254 : c);
 }

@@ -86,7 +86,7 @@ def encode(m, v, r):
         y = (v / s).astype(f)
         rv = (r & np.uint32(0xFFFF)).astype(np.int64)
         vc = np.clip(((y.view(np.uint32).astype(np.int64) + (rv << 4)) >> 20) - 762, 1, 254)
-        vc = np.where((s > 0) & (y > 0), vc, 0)
+        vc = np.where(v > 0, vc, 0)    # (a quotient that underflows takes the lowest code)
         vc = np.where(np.isfinite(v), vc, 255)
     return mc.astype(np.uint8), ms, vc.astype(np.uint8), vs
 

@@ -333,3 +333,20 @@ def test_skipped_steps_leave_no_trace(bits, capturable):
         if not flag:
             b.step([g])
         same()
+
+
+def test_a_positive_second_moment_never_becomes_zero():
+    """Gradients whose squares lie so far apart that fp32 has no quotient."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import optim
+    g = torch.zeros(512, device="cuda")
+    g[:5] = torch.tensor([2.0 ** 50, 2.0 ** 30, 2.0 ** -24, 2.0 ** -30, -2.0 ** -60])
+    opt = optim.AdamW([torch.ones(512, device="cuda")], state_bits=8, seed=6, **HYPER)
+    opt.step([g])
+    torch.cuda.synchronize()
+    m32, v32 = adamw.moments_f32(_np32(g), np.zeros(512, np.float32), np.zeros(512, np.float32), HYPER["betas"])
+    _, _, vc, vs = adamw.encode(m32, v32, adamw.random_bits(6, 1, 0, 512))
+    got = to_np(opt.state["exp_avg_sq"][0])
+    np.testing.assert_array_equal(got, vc)
+    np.testing.assert_array_equal(to_np(opt.state["avg_sq_scale"][0]), vs)
+    assert (got[:5] > 0).all() and (got[5:] == 0).all()

@@ -250,3 +250,13 @@ def test_python_refusals_need_no_gpu():
                      exp_avg=[z(300, dtype=u8)], exp_avg_sq=[z(300, dtype=u8)], avg_scale=[z(1)], avg_sq_scale=[z(2)]))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_positive_second_moment_never_becomes_zero():
+    # quotients from the lowest code's value down to ones that fp32 holds as 0
+    v = np.zeros(256, np.float32)
+    v[:5] = [2.0 ** 100, 2.0 ** 69, 2.0 ** -48, 2.0 ** -50, 2.0 ** -140]
+    for r in (0, 0xFFFFFFFF):
+        _, _, vc, vs = adamw.encode(np.zeros(256, np.float32), v, np.full(256, r, np.uint32))
+        assert vs[0] == v[0]
+        np.testing.assert_array_equal(vc[:6], [254, 6, 1, 1, 1, 0])
