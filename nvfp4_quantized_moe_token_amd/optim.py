@@ -199,19 +199,20 @@ class AdamW:
         """The moments as fp32 tensors, two lists (exp_avg, exp_avg_sq):
         written to ``out`` (two lists of fp32 tensors) when given.  With fp32
         moments and no ``out`` these are the moments themselves."""
-        if self.state_bits == 32:
-            m, v = self.state["exp_avg"], self.state["exp_avg_sq"]
-            if out is None:
-                return list(m), list(v)
-            for d, s in zip((*out[0], *out[1]), (*m, *v)):
-                d.copy_(s)
-            return out
+        self._refresh()
         if out is None:
+            if self.state_bits == 32:
+                return list(self.state["exp_avg"]), list(self.state["exp_avg_sq"])
             out = tuple([torch.empty(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
                         for _ in range(2))
-        self._refresh()
+        if len(out) != 2:
+            raise ValueError("out: two lists, got %d" % len(out))
         for t in out:
             self._same_sizes("out", t, torch.float32, required=True)
+        if self.state_bits == 32:
+            for d, s in zip((*out[0], *out[1]), (*self.state["exp_avg"], *self.state["exp_avg_sq"])):
+                d.copy_(s.view(d.shape))
+            return out
         with _on_device(self.params[0], *out[0], *out[1]):
             ptrs = [(ctypes.c_void_p * len(t))(*[x.data_ptr() for x in t]) for t in out]
             rc = _lib.load().adamw_read_state(self._list, len(self.params), ptrs[0], ptrs[1], _stream())

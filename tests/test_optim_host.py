@@ -191,3 +191,17 @@ def test_overlapping_tensors_are_refused(library):
     with pytest.raises(ValueError):
         opt.step([torch.zeros(t.shape) for t in opt.params])
     assert len(library.calls) == 1
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_are_read_into_tensors_that_fit(library, bits):
+    """Lists too short, or tensors that the moments would be spread over."""
+    opt = optim.AdamW([torch.zeros(4), torch.zeros(3)], state_bits=bits)
+    z = torch.zeros
+    for out in (([z(4)], [z(4)]), ([z(4), z(3)],), ([z(4), z(5, 3)], [z(4), z(3)]), ([z(4), z(3)], [z(4), None]),
+                ([z(4), z(3)], [z(4), z(3, dtype=torch.bfloat16)])):
+        with pytest.raises(ValueError):
+            opt.state_values(out=out)
+    assert library.calls == []
+    out = [z(2, 2), z(3)], [z(4), z(3, 1)]
+    assert opt.state_values(out=out) is out
