@@ -193,7 +193,9 @@ int moe_router(const void* logits, int logits_dtype, int64_t T, int E, int k, co
  *   logits, topk_ids, score, scale: as in the forward call (ids outside
  *             [0, E) contribute nothing; a repeated id adds up).
  *   d_topk_w  [T][k] fp32 or NULL (zeros); d_lse [T] or NULL; d_prob_sum [E]
- *             or NULL.
+ *             or NULL.  An expert of probability 0 (masked; all of a row of
+ *             -inf) neither gives nor takes a gradient of theirs, so what they
+ *             hold there does not matter: d_lse of such a row may be -inf or NaN.
  *   lse       [T] fp32 of the forward, or NULL (then it is computed again).
  *   d_logits  [T][E] of d_dtype (F32 or BF16) out, every element written; fp32
  *             arithmetic.  Must not overlap the logits.

@@ -14,7 +14,9 @@
 // Backward (u_j = scale * dw_j):
 //   TOPK_SOFTMAX: dl[id_j] += q_j (u_j - sum_i q_i u_i), q = softmax of the chosen;
 //   SOFTMAX:      dl[id_j] += p_j u_j, and dl_e -= p_e sum_j p_j u_j;
-//   dl_e += p_e (dlse + dS_e - sum_e' p_e' dS_e').
+//   dl_e += p_e (dlse + dS_e - sum_e' p_e' dS_e'), terms with p = 0 left out:
+//           the lse of a row without experts is -inf, and so is the gradient of
+//           its square.
 // All arithmetic is fp32.
 //
 // Layout.  A group of L lanes serves one token, each lane holding V logits in
@@ -389,12 +391,12 @@ __global__ __launch_bounds__(kRouterThreads) void router_bwd_kernel(
       for (int v = 0; v < V; ++v) {
         const int e = expert_of<L, W>(v, i);
         s[v] = e < E ? dsum[e] : 0.0f;
-        mean += p[v] * s[v];
+        mean += p[v] == 0.0f ? 0.0f : p[v] * s[v];
       }
       base -= group_sum<L>(mean);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = p[v] * (dsum ? base + s[v] : base);
+    for (int v = 0; v < V; ++v) d[v] = p[v] == 0.0f ? 0.0f : p[v] * (dsum ? base + s[v] : base);
   }
   for (int j = 0; j < k; ++j) {
     const int src = (threadIdx.x & 63) / L * L + j;  // lane j of this token's group

@@ -48,6 +48,11 @@ def prob_sum(logits):
     return _softmax(logits).sum(axis=0)
 
 
+def _times(p, x):
+    """p x, 0 where p is 0 (a masked expert), whatever x is there."""
+    return np.where(p == 0, 0.0, p * np.where(p == 0, 0.0, x))
+
+
 def backward(logits, ids, score, scale, dw, dlse=None, dsum=None):
     """d logits (fp64) of sum(w dw) + sum(lse dlse) + sum(prob_sum dsum)."""
     l = np.asarray(logits, np.float64)
@@ -66,8 +71,8 @@ def backward(logits, ids, score, scale, dw, dlse=None, dsum=None):
             np.add.at(d[t], e, p[t, e] * u[t, on])
             d[t] -= p[t] * (p[t, e] * u[t, on]).sum()
     if dlse is not None:
-        d += p * np.asarray(dlse, np.float64)[:, None]
+        d += _times(p, np.asarray(dlse, np.float64)[:, None])
     if dsum is not None:
         s = np.asarray(dsum, np.float64)
-        d += p * (s[None, :] - (p * s).sum(axis=1, keepdims=True))
+        d += _times(p, s[None, :] - _times(p, s).sum(axis=1, keepdims=True))
     return d

@@ -224,3 +224,30 @@ def test_captured_router_replays():
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(out[n], want[n]), n
+
+
+@pytest.mark.parametrize("E,k", [(60, 4), (128, 8), (130, 3), (300, 12), (600, 2), (2000, 20)])
+@pytest.mark.parametrize("score", ["topk", "all"])
+def test_gradients_that_are_not_finite_at_masked_places(E, k, score):
+    """A z-loss over padded rows hands in -inf or NaN for them, a loss of the
+    logarithm of prob_sum an infinity for an expert that is masked everywhere."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    rng = np.random.default_rng(E + k)
+    T = 40
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[::4] = -np.inf
+    l[:, 3::7] = -np.inf
+    g = to_gpu(l, torch.float32)
+    r = ops.moe_router(g, k, score=SCORES[score], want_lse=True)
+    ids = router.select(l, None, k)
+    dw, dl, ds = (rng.standard_normal(n).astype(np.float32) for n in ((T, k), (T,), (E,)))
+    dl[::4], dl[4] = -np.inf, np.nan
+    ds[3::7] = np.inf
+    for lse in (r["lse"], None):
+        d = ops.moe_router_bwd(g, r["topk_ids"], to_gpu(dw, torch.float32), score=SCORES[score], lse=lse,
+                               d_lse=to_gpu(dl, torch.float32), d_prob_sum=to_gpu(ds, torch.float32))
+        torch.cuda.synchronize()
+        got, want = to_np(d), router.backward(l, ids, score, 1.0, dw, dl, ds)
+        assert (got[::4] == 0).all() and (got[:, 3::7] == 0).all()
+        assert np.abs(got - want).max() <= _exp_rel(l, 64) * 40

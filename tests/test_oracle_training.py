@@ -260,3 +260,14 @@ def test_a_positive_second_moment_never_becomes_zero():
         _, _, vc, vs = adamw.encode(np.zeros(256, np.float32), v, np.full(256, r, np.uint32))
         assert vs[0] == v[0]
         np.testing.assert_array_equal(vc[:6], [254, 6, 1, 1, 1, 0])
+
+
+def test_router_gradient_of_masked_rows_by_hand():
+    """z-loss lse^2 of a row of -inf: its d_lse is -inf, its gradient zero; and
+    a masked expert's d_prob_sum reaches nobody."""
+    l = np.array([[-INF, -INF, -INF], [0, 0, -INF]], np.float32)
+    ids = np.array([[-1], [0]], np.int32)
+    dsum = np.array([1, 3, np.inf])
+    for dlse in ([-INF, 2], [np.nan, 2]):
+        got = router.backward(l, ids, "topk", 1.0, [[np.nan], [5.0]], dlse, dsum)
+        np.testing.assert_allclose(got, [[0, 0, 0], [1 + 0.5 * (1 - 2), 1 + 0.5 * (3 - 2), 0]])
