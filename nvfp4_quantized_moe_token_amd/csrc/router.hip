@@ -515,16 +515,25 @@ extern "C" int moe_router_bwd(const void* logits, int logits_dtype, int64_t T, i
   const bool bf = logits_dtype == NVFP4MOE_BF16, obf = d_dtype == NVFP4MOE_BF16;
   with_layout(E, k, E % 4 == 0 && aligned(logits, 4 * lb) && aligned(d_logits, 4 * db), [&](auto Lc, auto Vc, auto Wc) {
     constexpr int L = decltype(Lc)::value, V = decltype(Vc)::value, W = decltype(Wc)::value;
-    const int64_t grid = cdiv(T, kRouterThreads / L);
-#define NVR_GO(B, O)                                                                                       \
-  router_bwd_kernel<L, V, W, B, O><<<(unsigned)grid, kRouterThreads, 0, st>>>(logits, T, E, k, topk_ids, score, scale, \
-                                                                              d_topk_w, lse, d_lse, d_prob_sum, d_logits)
-    if (bf) {
-      if (obf) NVR_GO(true, true);
-      else NVR_GO(true, false);
-    } else {
-      if (obf) NVR_GO(false, true);
-      else NVR_GO(false, false);
+    // A dispatch has fewer than 2^32 work-items: tokens beyond that go in
+    // launches of their own.
+    constexpr int64_t kSlice = kMaxStreamGrid * (kRouterThreads / L);
+    for (int64_t t0 = 0; t0 < T; t0 += kSlice) {
+      const int64_t n = T - t0 < kSlice ? T - t0 : kSlice, grid = cdiv(n, kRouterThreads / L);
+      const void* x = reinterpret_cast<const uint8_t*>(logits) + t0 * E * lb;
+      void* d = reinterpret_cast<uint8_t*>(d_logits) + t0 * E * db;
+      const float *dw = d_topk_w ? d_topk_w + t0 * k : nullptr, *ls = lse ? lse + t0 : nullptr,
+                  *dl = d_lse ? d_lse + t0 : nullptr;
+#define NVR_GO(B, O)                                                                                            \
+  router_bwd_kernel<L, V, W, B, O><<<(unsigned)grid, kRouterThreads, 0, st>>>(x, n, E, k, topk_ids + t0 * k, score, \
+                                                                              scale, dw, ls, dl, d_prob_sum, d)
+      if (bf) {
+        if (obf) NVR_GO(true, true);
+        else NVR_GO(true, false);
+      } else {
+        if (obf) NVR_GO(false, true);
+        else NVR_GO(false, false);
+      }
     }
 #undef NVR_GO
   });

@@ -251,3 +251,27 @@ def test_gradients_that_are_not_finite_at_masked_places(E, k, score):
         got, want = to_np(d), router.backward(l, ids, score, 1.0, dw, dl, ds)
         assert (got[::4] == 0).all() and (got[:, 3::7] == 0).all()
         assert np.abs(got - want).max() <= _exp_rel(l, 64) * 40
+
+
+def test_gradient_of_more_tokens_than_one_dispatch_holds():
+    """2^28 + 21 tokens of two experts, 16 per workgroup: over 2^32 work-items.
+    Tokens at the start, across both ends of a launch and at the end against
+    calls of their own."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    T, E = (1 << 28) + 21, 2
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-256, 256, (T, E), generator=gen, device="cuda", dtype=torch.int16)
+    x = x.to(torch.bfloat16).mul_(2.0 ** -6)
+    dw = torch.ones((T, 1), device="cuda")
+    ids = torch.arange(T, device="cuda", dtype=torch.int32).remainder_(2).view(T, 1)
+    d = torch.full((T, E), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops.moe_router_bwd(x, ids, dw, score=SCORES["all"], out=d)
+    torch.cuda.synchronize()
+    per = (1 << 20) * 16
+    for lo in (0, per - 50, 5 * per - 3, (1 << 28) - 40, T - 100):
+        s = slice(lo, min(lo + 100, T))
+        want = ops.moe_router_bwd(x[s].clone(), ids[s].clone(), dw[s].clone(), score=SCORES["all"])
+        torch.cuda.synchronize()
+        assert torch.equal(d[s], want), lo
+    assert not (d == 7.0).any()
