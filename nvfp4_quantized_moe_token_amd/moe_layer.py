@@ -302,12 +302,13 @@ def forward_mxfp4(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep=False):
     inside the gate+up epilogue.  ``keep``: bf16 Y1 and H are stored too
     (buf.y1, buf.h), for ``backward``, which then gathers its activation rows
     from x."""
-    meta = ops.moe_permute_mxfp4(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
-    ops.grouped_gemm_mxfp4_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"],
-                                     y1=buf.y1 if keep else None, want_y1=keep, h=buf.h if keep else None,
-                                     want_h=keep, q_h=buf.a2_q, s_h=buf.a2_s)
-    ops.grouped_gemm_mxfp4(buf.a2_q, buf.a2_s, wq_dn["q"], wq_dn["s"], meta["offsets"], out=buf.y2)
-    ops.moe_unpermute(buf.y2, meta["dest"], buf.T, buf.k, topk_w=topk_w, out=buf.out)
+    with ops._on_device(x, topk_ids, topk_w, buf.out):
+        meta = ops.moe_permute_mxfp4(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
+        ops.grouped_gemm_mxfp4_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"],
+                                         y1=buf.y1 if keep else None, want_y1=keep, h=buf.h if keep else None,
+                                         want_h=keep, q_h=buf.a2_q, s_h=buf.a2_s)
+        ops.grouped_gemm_mxfp4(buf.a2_q, buf.a2_s, wq_dn["q"], wq_dn["s"], meta["offsets"], out=buf.y2)
+        ops.moe_unpermute(buf.y2, meta["dest"], buf.T, buf.k, topk_w=topk_w, out=buf.out)
     return meta
 
 
@@ -336,19 +337,20 @@ class Learner:
         self.dw_r = e(1, E, D)
         self.one_group = torch.tensor([0, T], dtype=torch.int32, device=dev)
         self.opt = optim.AdamW(self.master, params_bf16=self.copies, **adamw)
-        self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
+        with ops._on_device(self.w_r):
+            self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
 
     def forward(self, x):
         """The layer's output [T, D] (bf16, the layer's own buffer) for x [T, D]
         bf16; the router's lse and prob_sum stay in ``lse`` and ``prob_sum`` for
         its losses.  x is kept, not copied: ``backward`` reads it again."""
         ops._need(x, "x", torch.bfloat16, self.logits.shape[0], self.w_r.shape[1])
-        ops._on_device(x, self.w_r)
-        self.x = x
-        ops.grouped_gemm_bf16(ops.NT, x, self.w_r.unsqueeze(0), self.one_group, out=self.logits)
-        ops.moe_router(self.logits, self.k, bias=self.router_bias, score=self.score, topk_ids=self.topk_ids,
-                       topk_w=self.topk_w, lse=self.lse, prob_sum=self.prob_sum, workspace=self.router_ws)
-        self.meta = forward_mxfp4(x, self.topk_ids, self.topk_w, self.wq_gu, self.wq_dn, self.buf, keep=True)
+        with ops._on_device(x, self.w_r):
+            self.x = x
+            ops.grouped_gemm_bf16(ops.NT, x, self.w_r.unsqueeze(0), self.one_group, out=self.logits)
+            ops.moe_router(self.logits, self.k, bias=self.router_bias, score=self.score, topk_ids=self.topk_ids,
+                           topk_w=self.topk_w, lse=self.lse, prob_sum=self.prob_sum, workspace=self.router_ws)
+            self.meta = forward_mxfp4(x, self.topk_ids, self.topk_w, self.wq_gu, self.wq_dn, self.buf, keep=True)
         return self.buf.out
 
     def backward(self, dy, d_lse=None, d_prob_sum=None):
@@ -356,11 +358,13 @@ class Learner:
         gradients of the router's losses; the weights' gradients stay in
         ``grads()``."""
         b = self.buf
-        backward(dy, self.topk_w, self.w_gu, self.w_dn, self.meta, b, x=self.x, d_topk_w=self.d_topk_w)
-        ops.moe_router_bwd(self.logits, self.topk_ids, self.d_topk_w, score=self.score, lse=self.lse, d_lse=d_lse,
-                           d_prob_sum=d_prob_sum, out=self.d_logits)
-        ops.grouped_gemm_bf16(ops.TN, self.d_logits, self.x, self.one_group, out=self.dw_r)
-        ops.grouped_gemm_bf16(ops.NN, self.d_logits, self.w_r.unsqueeze(0), self.one_group, out=b.dx, accumulate=True)
+        with ops._on_device(dy, self.w_r):
+            backward(dy, self.topk_w, self.w_gu, self.w_dn, self.meta, b, x=self.x, d_topk_w=self.d_topk_w)
+            ops.moe_router_bwd(self.logits, self.topk_ids, self.d_topk_w, score=self.score, lse=self.lse, d_lse=d_lse,
+                               d_prob_sum=d_prob_sum, out=self.d_logits)
+            ops.grouped_gemm_bf16(ops.TN, self.d_logits, self.x, self.one_group, out=self.dw_r)
+            ops.grouped_gemm_bf16(ops.NN, self.d_logits, self.w_r.unsqueeze(0), self.one_group, out=b.dx,
+                                  accumulate=True)
         return b.dx
 
     def grads(self):
@@ -368,6 +372,7 @@ class Learner:
 
     def update(self, grad_scale=None, skip=None):
         """One optimizer step; the bf16 and MXFP4 weights follow."""
-        self.opt.step(self.grads(), grad_scale=grad_scale, skip=skip)
-        quantize_expert_weights_mx(self.w_gu, out=self.wq_gu)
-        quantize_expert_weights_mx(self.w_dn, out=self.wq_dn)
+        with ops._on_device(self.w_r):
+            self.opt.step(self.grads(), grad_scale=grad_scale, skip=skip)
+            quantize_expert_weights_mx(self.w_gu, out=self.wq_gu)
+            quantize_expert_weights_mx(self.w_dn, out=self.wq_dn)

@@ -1,10 +1,12 @@
 """Calls that the learner's layer and its BF16 products refuse, without a GPU:
 each raises before anything is launched."""
 
+import contextlib
+
 import pytest
 import torch
 
-from nvfp4_quantized_moe_token_amd import moe_layer, ops
+from nvfp4_quantized_moe_token_amd import moe_layer, ops, optim
 
 BF16 = torch.bfloat16
 
@@ -67,3 +69,56 @@ def test_learner_refuses_other_inputs(launched, x):
     with pytest.raises(ValueError):
         _learner().forward(x)
     assert launched == []
+
+
+T, E, D, F, K = 4, 32, 128, 128, 2
+
+
+@pytest.fixture
+def inside(launched, monkeypatch):
+    """`launched`, on tensors in host memory; inside["names"] are the calls made
+    while the tensors' GPU was the current one."""
+    depth, seen = [0], dict(names=[])
+
+    @contextlib.contextmanager
+    def on_device(*ts):
+        depth[0] += 1
+        yield
+        depth[0] -= 1
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: (launched.append(name), seen["names"].append(name) if depth[0] else None) and 0
+
+    monkeypatch.setattr(ops._lib, "load", lambda *a: Library())
+    for m in (ops, optim):
+        monkeypatch.setattr(m, "_on_device", on_device)
+    monkeypatch.setattr(optim, "_stream", lambda: None)
+    monkeypatch.setattr(optim, "_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: None)
+    return seen
+
+
+def _f32(*shape):
+    return z(*shape, dtype=torch.float32)
+
+
+def test_every_launch_of_the_learner_is_on_the_weights_gpu(inside, launched):
+    """Also when another GPU is the current one."""
+    ln = moe_layer.Learner(_f32(E, D), _f32(E, 2 * F, D), _f32(E, D, F), T, K)
+    ln.forward(z(T, D))
+    ln.backward(z(T, D))
+    ln.update()
+    queries = {"moe_permute_workspace_size", "moe_router_workspace_size"}
+    assert [n for n in launched if n not in queries] == [n for n in inside["names"] if n not in queries]
+    assert len(launched) > 15
+
+
+def test_mxfp4_forward_is_on_the_inputs_gpu(inside, launched):
+    buf = moe_layer.BuffersMXFP4(T, K, E, D, F, torch.device("cpu"))
+    u8 = dict(dtype=torch.uint8)
+    gu, dn = (dict(q=z(E, n, k // 2, **u8), s=z(E, n, k // 32, **u8)) for n, k in ((2 * F, D), (D, F)))
+    ids = z(T, K, dtype=torch.int32)
+    launched.clear()
+    moe_layer.forward_mxfp4(z(T, D), ids, _f32(T, K), gu, dn, buf)
+    assert launched == inside["names"][-len(launched):] and "moe_unpermute" in launched
