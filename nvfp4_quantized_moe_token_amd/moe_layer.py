@@ -302,6 +302,7 @@ def forward_mxfp4(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep=False):
     inside the gate+up epilogue.  ``keep``: bf16 Y1 and H are stored too
     (buf.y1, buf.h), for ``backward``, which then gathers its activation rows
     from x."""
+    ops._need(topk_w, "topk_w", torch.float32, buf.T, buf.k)
     with ops._on_device(x, topk_ids, topk_w, buf.out):
         meta = ops.moe_permute_mxfp4(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
         ops.grouped_gemm_mxfp4_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"],

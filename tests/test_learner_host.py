@@ -122,3 +122,15 @@ def test_mxfp4_forward_is_on_the_inputs_gpu(inside, launched):
     launched.clear()
     moe_layer.forward_mxfp4(z(T, D), ids, _f32(T, K), gu, dn, buf)
     assert launched == inside["names"][-len(launched):] and "moe_unpermute" in launched
+
+
+def test_mxfp4_forward_takes_fp32_weights_of_its_tokens(launched):
+    """Others would be read as fp32, past their end."""
+    buf = moe_layer.BuffersMXFP4(T, K, E, D, F, torch.device("cpu"))
+    u8 = dict(dtype=torch.uint8)
+    gu, dn = (dict(q=z(E, n, k // 2, **u8), s=z(E, n, k // 32, **u8)) for n, k in ((2 * F, D), (D, F)))
+    launched.clear()
+    for tw in (z(T, K), z(T, K + 1, dtype=torch.float32), z(T * K, dtype=torch.float32)):
+        with pytest.raises(ValueError, match="topk_w"):
+            moe_layer.forward_mxfp4(z(T, D), z(T, K, dtype=torch.int32), tw, gu, dn, buf)
+    assert launched == []
