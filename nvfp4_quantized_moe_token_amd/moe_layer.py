@@ -337,6 +337,8 @@ class Learner:
         self.router_ws = e(max(ops._lib.load().moe_router_workspace_size(T, E, k), 1), dt=torch.uint8)
         self.dw_r = e(1, E, D)
         self.one_group = torch.tensor([0, T], dtype=torch.int32, device=dev)
+        self.x = self.meta = None        # of the last forward
+        self.has_grads = False           # the gradients' buffers hold some
         self.opt = optim.AdamW(self.master, params_bf16=self.copies, **adamw)
         with ops._on_device(self.w_r):
             self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
@@ -358,6 +360,8 @@ class Learner:
         """Gradient of the input (fp32 [T, D]) for dy [T, D] bf16 and the
         gradients of the router's losses; the weights' gradients stay in
         ``grads()``."""
+        if self.meta is None:
+            raise RuntimeError("Learner.backward before a forward")
         b = self.buf
         with ops._on_device(dy, self.w_r):
             backward(dy, self.topk_w, self.w_gu, self.w_dn, self.meta, b, x=self.x, d_topk_w=self.d_topk_w)
@@ -366,13 +370,17 @@ class Learner:
             ops.grouped_gemm_bf16(ops.TN, self.d_logits, self.x, self.one_group, out=self.dw_r)
             ops.grouped_gemm_bf16(ops.NN, self.d_logits, self.w_r.unsqueeze(0), self.one_group, out=b.dx,
                                   accumulate=True)
+        self.has_grads = True
         return b.dx
 
     def grads(self):
         return [self.dw_r[0], self.buf.dw_gu, self.buf.dw_dn]
 
     def update(self, grad_scale=None, skip=None):
-        """One optimizer step; the bf16 and MXFP4 weights follow."""
+        """One optimizer step with the last backward's gradients; the bf16 and
+        MXFP4 weights follow."""
+        if not self.has_grads:
+            raise RuntimeError("Learner.update before a backward: there are no gradients")
         with ops._on_device(self.w_r):
             self.opt.step(self.grads(), grad_scale=grad_scale, skip=skip)
             quantize_expert_weights_mx(self.w_gu, out=self.wq_gu)

@@ -160,3 +160,23 @@ def test_an_example_trains():
             assert torch.isfinite(g).all() and torch.isfinite(w).all()
             # Adam's step is at most (1 - b1) / sqrt(1 - b2) rates (3.2), plus the decay
             assert (w - w0).abs().max() <= 1e-3 * (3.3 + 0.1 * w0.abs().max())
+
+
+def test_a_step_without_tokens():
+    """No tokens, no gradients: the update is the weight decay alone."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import moe_layer
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = [torch.randn(s, generator=g, device="cuda") * 0.05 for s in ((E, D), (E, 2 * F, D), (E, D, F))]
+    before = [x.clone() for x in w]
+    ln = moe_layer.Learner(*w, 0, K, lr=1e-3, weight_decay=0.5)
+    for t in ln.grads():
+        t.fill_(9)
+    x = torch.zeros(0, D, dtype=torch.bfloat16, device="cuda")
+    assert ln.forward(x).shape == (0, D)
+    assert ln.backward(x).shape == (0, D)
+    ln.update()
+    torch.cuda.synchronize()
+    for t, u, v in zip(ln.grads(), ln.master, before):
+        assert (t == 0).all()
+        assert (u - v * (1 - 1e-3 * 0.5)).abs().max() <= 2.0 ** -22 * v.abs().max()

@@ -134,3 +134,20 @@ def test_mxfp4_forward_takes_fp32_weights_of_its_tokens(launched):
         with pytest.raises(ValueError, match="topk_w"):
             moe_layer.forward_mxfp4(z(T, D), z(T, K, dtype=torch.int32), tw, gu, dn, buf)
     assert launched == []
+
+
+def test_the_learner_needs_its_steps_in_order(inside, launched):
+    """An update before any backward would take whatever its buffers hold."""
+    ln = moe_layer.Learner(_f32(E, D), _f32(E, 2 * F, D), _f32(E, D, F), T, K)
+    launched.clear()
+    with pytest.raises(RuntimeError):
+        ln.update()
+    with pytest.raises(RuntimeError):
+        ln.backward(z(T, D))
+    assert launched == [] and ln.opt.steps == 0
+    ln.forward(z(T, D))
+    with pytest.raises(RuntimeError):
+        ln.update()
+    ln.backward(z(T, D))
+    ln.update()
+    assert ln.opt.steps == 1
