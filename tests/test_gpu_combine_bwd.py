@@ -147,3 +147,10 @@ def test_captured_replays():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(amax, a)
+
+
+@pytest.mark.parametrize("T,k,E,D,drop", [(2500, 8, 16, 2048, 5), (9000, 2, 8, 64, 3), (2050, 10, 24, 1544, 4)])
+def test_workgroups_with_several_tokens(T, k, E, D, drop):
+    """With the maximum wanted 2048 workgroups walk the tokens, four waves of
+    one token (D > 1536) sharing their sums through LDS again and again."""
+    test_unpermute_bwd_parity(T, k, E, D, drop, (BF16, BF16, BF16))

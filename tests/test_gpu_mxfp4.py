@@ -18,6 +18,7 @@ pytestmark = gpu
 
 E2M1 = 1
 U = 2.0 ** -24
+BF16 = torch.bfloat16
 
 
 def _operands(rng, M, N, K, E, spread=1.0):
@@ -329,3 +330,53 @@ def test_two_streams_and_captured_replays():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(buf.out, want)
+
+
+@pytest.mark.parametrize("K", [256, 384, 640])                # one, two and three stages per tile
+@pytest.mark.parametrize("mean", [16, 48, 128, 300])          # each row block of the tile rule
+def test_workgroups_with_several_tiles(mean, K):
+    """768 to 2500 tiles on 256 CUs: the loads of a next tile run under an
+    epilogue and the waits behind it allow for its stores, whichever outputs it
+    has.  Every row of every form against products of one expert at a time
+    (a tile per workgroup at most) and the separate steps, bit for bit."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    E, F = 96, 1024
+    N = 2 * F
+    g = torch.Generator(device="cuda").manual_seed(mean * 1000 + K)
+    counts = torch.randint(0, 2 * mean, (E,), generator=g, device="cuda")
+    counts[3], counts[40] = 0, 1
+    offs = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offs[1:] = counts.cumsum(0)
+    ends = offs.tolist()
+    R = ends[-1]
+    M = R + 7
+    assert (24 < R / E) == (mean > 16) and (72 < R / E) == (mean > 48) and (176 < R / E) == (mean > 128)
+
+    def u8(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=g, device="cuda", dtype=torch.uint8)
+
+    aq, as_, bq, bs = u8(0, 256, M, K // 2), u8(120, 128, M, K // 32), u8(0, 256, E, N, K // 2), u8(120, 128, E, N, K // 32)
+    want = torch.full((M, N), 7.0, device="cuda")
+    for e in range(E):
+        lo, hi = ends[e], ends[e + 1]
+        if hi > lo:
+            one = torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda")
+            want[lo:hi] = ops.grouped_gemm_mxfp4(aq[lo:hi].clone(), as_[lo:hi].clone(), bq[e:e + 1], bs[e:e + 1], one)
+    y1 = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+    y1[:R] = want[:R].to(BF16)
+    h = torch.full((M, F), 7.0, dtype=BF16, device="cuda")
+    h[:R] = ops.silu_gate_fwd(y1[:R].contiguous())[0]
+    q, s = (torch.full((M, n), 77, dtype=torch.uint8, device="cuda") for n in (F // 2, F // 32))
+    q[:R], s[:R] = ops.mx_quantize(h[:R].contiguous(), E2M1)
+    for _ in range(2):
+        for dt, ref in ((torch.float32, want), (BF16, y1)):
+            c = torch.full((M, N), 7.0, dtype=dt, device="cuda")
+            ops.grouped_gemm_mxfp4(aq, as_, bq, bs, offs, out=c)
+            assert torch.equal(c, ref), dt
+        for keep_y1, keep_h, quant in ((1, 1, 0), (0, 1, 0), (0, 0, 1), (1, 1, 1), (1, 0, 1)):
+            out = dict(y1=torch.full_like(y1, 7.0) if keep_y1 else None, h=torch.full_like(h, 7.0) if keep_h else None,
+                       q_h=torch.full_like(q, 77) if quant else None, s_h=torch.full_like(s, 77) if quant else None)
+            ops.grouped_gemm_mxfp4_silu_gate(aq, as_, bq, bs, offs, want_y1=bool(keep_y1), want_h=bool(keep_h), **out)
+            for name, ref in (("y1", y1), ("h", h), ("q_h", q), ("s_h", s)):
+                assert out[name] is None or torch.equal(out[name], ref), (name, keep_y1, keep_h, quant)

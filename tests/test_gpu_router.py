@@ -275,3 +275,28 @@ def test_gradient_of_more_tokens_than_one_dispatch_holds():
         torch.cuda.synchronize()
         assert torch.equal(d[s], want), lo
     assert not (d == 7.0).any()
+
+
+@pytest.mark.parametrize("E,k,T", [(128, 8, 16385), (128, 8, 40000), (512, 4, 5000), (300, 20, 9001), (2048, 3, 1100)])
+def test_probability_sums_over_several_rounds_of_tokens(E, k, T):
+    """More tokens than the workgroups hold at once: each adds up several."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    rng = np.random.default_rng(E + T)
+    g, l = _logits(rng, T, E, torch.float32)
+    r = ops.moe_router(g, k, want_lse=True, want_prob_sum=True)
+    torch.cuda.synchronize()
+    ids = router.select(l, None, k)
+    np.testing.assert_array_equal(to_np(r["topk_ids"]), ids)
+    rel = _exp_rel(l, 64)
+    w, lse, s = router.weights(l, ids, "topk", 1.0), router.lse(l), router.prob_sum(l)
+    assert (np.abs(to_np(r["topk_w"]) - w) <= rel * w).all()
+    assert (np.abs(to_np(r["lse"]) - lse) <= rel + 4 * U * np.abs(lse)).all()
+    # a lane's chain of at most 5 tokens, 2 exchanges, 16 waves; 4 rows, 2 exchanges, 16 waves
+    assert (np.abs(to_np(r["prob_sum"]) - s) <= (rel + 45 * U) * s).all()
+    # probabilities of exactly 1: the sums are counts, whatever the order
+    e = rng.integers(0, E, T)
+    l = np.full((T, E), -np.inf, np.float32)
+    l[np.arange(T), e] = rng.standard_normal(T)
+    r = ops.moe_router(to_gpu(l, torch.float32), k, want_prob_sum=True)
+    np.testing.assert_array_equal(to_np(r["prob_sum"]), np.bincount(e, minlength=E))
