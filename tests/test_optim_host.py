@@ -88,7 +88,13 @@ def test_replaced_storage_is_checked(library):
     def fresh():
         return optim.AdamW([torch.zeros(64), torch.zeros(8)])
 
-    for change in (lambda o: setattr(o.params[0], "data", torch.zeros(65)),
+    def shrink(o):                             # where it was, but less of it
+        o.params[0].data = o.params[0].data[:60]
+
+    def other_type(o):                         # and as another type
+        o.params[0].data = o.params[0].data.view(torch.int32)
+
+    for change in (shrink, other_type, lambda o: setattr(o.params[0], "data", torch.zeros(65)),
                    lambda o: setattr(o.params[1], "data", torch.zeros(8, dtype=torch.bfloat16)),
                    lambda o: setattr(o.params[0], "data", torch.zeros(64, 2)[:, 0]),
                    lambda o: setattr(o.state["exp_avg"][0], "data", torch.zeros(32)),
