@@ -328,7 +328,8 @@ class Learner:
         dev = w_r.device
         self.k, self.score, self.router_bias = k, score, router_bias
         self.master = [w_r, w_gu, w_dn]
-        self.w_r, self.w_gu, self.w_dn = self.copies = [w.to(torch.bfloat16) for w in self.master]
+        # (detached: a copy of a leaf would keep the leaf's node of the autograd graph)
+        self.w_r, self.w_gu, self.w_dn = self.copies = [w.detach().to(torch.bfloat16) for w in self.master]
         self.buf = BuffersMXFP4(T, k, E, D, F, dev, backward=True, dx_dtype=torch.float32)
         e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         self.logits, self.d_logits = e(T, E), e(T, E, dt=torch.bfloat16)

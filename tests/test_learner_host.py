@@ -151,3 +151,12 @@ def test_the_learner_needs_its_steps_in_order(inside, launched):
     ln.backward(z(T, D))
     ln.update()
     assert ln.opt.steps == 1
+
+
+def test_the_copies_of_parameters_are_outside_the_autograd_graph(inside):
+    """A live graph of the leaves would meet a backward pass that the caller
+    captures over the same parameters."""
+    w = [torch.nn.Parameter(_f32(*s)) for s in ((E, D), (E, 2 * F, D), (E, D, F))]
+    ln = moe_layer.Learner(*w, T, K)
+    for t in (*ln.copies, ln.forward(z(T, D)), ln.backward(z(T, D)), *ln.grads()):
+        assert not t.requires_grad and t.grad_fn is None
