@@ -259,6 +259,8 @@ def moe_permute_mxfp4(topk_ids, num_experts, x, q=None, scales=None, status=None
     D, R = x.shape[1], T * k
     _need(q, "q", torch.uint8, R, D // 2)
     _need(scales, "scales", torch.uint8, R, D // 32)
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: one int32 on the GPU")
     with _on_device(topk_ids, x, q, scales, status, workspace):
         dev, i32, u8 = x.device, torch.int32, torch.uint8
         lib = _lib.load()

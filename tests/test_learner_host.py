@@ -160,3 +160,11 @@ def test_the_copies_of_parameters_are_outside_the_autograd_graph(inside):
     ln = moe_layer.Learner(*w, T, K)
     for t in (*ln.copies, ln.forward(z(T, D)), ln.backward(z(T, D)), *ln.grads()):
         assert not t.requires_grad and t.grad_fn is None
+
+
+def test_mxfp4_permutation_takes_an_int32_status(launched):
+    """The library writes four bytes there."""
+    for status in (z(1, dtype=torch.uint8), z(1, dtype=torch.int64), z(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="status"):
+            ops.moe_permute_mxfp4(z(T, K, dtype=torch.int32), E, z(T, D), status=status)
+    assert launched == []
