@@ -26,19 +26,27 @@
 // does; optionally H is quantized to MXFP4 on the way out.
 //
 // Bounds and measurements (us of the kernel; 128 experts, top-8).  A 256x256
-// tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS per MFMA (half of the
-// LDS's rate at the MFMAs' peak); 64x64 waves (128x256 and 256x128 tiles, or
-// two workgroups per CU) read a third more and lose more than finer tiles save:
-// gate+up of 8192 tokens 209 against 216 to 244.  Stages of 128 elements and a
+// tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS per MFMA; by the counters
+// the LDS is then busy 81% as long as the MFMAs (gate+up of 8192 tokens; 107% in
+// the skewed product, its epilogue included), writes of the loads not counted.
+// 64x64 waves (128x256 and 256x128 tiles, or two workgroups per CU) read a third
+// more and lose more than finer tiles save: gate+up of 8192 tokens 209 against
+// 216 to 244.  Stages of 128 elements and a
 // ring of four are no faster either (155 against 138 for a dense 4096 x 8192 x
 // 8192 product, 4.0 PFLOP/s): lines are then read in halves.
 //   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      210
 //   down, 16384 tokens, skewed routing (N = 2048, K = 768)         243
+//   gate+up, 8192 tokens, H quantized and nothing else stored      181
+//   the same with Y1 and H stored too (the learner's form)         235
+//   the skewed product with fp32 output (266 of bytes)             328
 //   gate+up, 512 tokens    51 (4.2 TB/s)     down, 512 tokens       30
-//   gate+up weights, 16 tokens (214 MB)                       28 (7.5 TB/s)
-// Without their stores the first two take 170 and 161, without any epilogue 129
-// and 117: a workgroup's stores and SiLU are not hidden behind its products,
-// since its accumulators fill the registers and its stages the LDS.
+//   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts (140 MB)
+//                                                     28 to 33 (4.3 to 4.9 TB/s)
+// In copies without their stores the first two take 170 and 161, without any
+// epilogue 129 and 117, where the MFMAs alone need 52 and 47: a workgroup's
+// stores and SiLU are not hidden behind its products, since its accumulators
+// fill the registers and its stages the LDS; the loop itself is held up by its
+// LDS reads and by row padding (a fifth of gate+up's MFMAs).
 #include "gemm_tiles.hpp"
 #include "mx_codec.hpp"
 

@@ -26,13 +26,19 @@
 // allow it.  Lane i holds experts e(v) = (v / W) * W * L + i * W + v % W, so a
 // lower v is a lower expert and ties resolve in order.
 //
-// Bounds, measured (E = 128, k = 8, fp32): the vector ALU.  A round is some 46
+// Exponentials and logarithms are the hardware's (__expf, __logf): their errors
+// are those of fp32 roundings (weights are off by 6e-8 relative, as with exact
+// functions), and gates are not worth more instructions.
+//
+// Bounds, measured (E = 128, k = 8, fp32): the rounds.  One is some 46
 // instructions for the four tokens of a wave: 3 maxima over 8 registers (three
 // at a time), 4 across the lanes, 16 to find the winner's expert, 4 across, 16
-// to take it out.  16 tokens 3.9 us (a launch and one trip to memory); 16384
+// to take it out.  With lse and sums the vector ALU issues 59% of the time and
+// waves wait 57% of theirs: the reductions of a round depend on one another.  16 tokens 3.9 us (a launch and one trip to memory); 16384
 // tokens with lse and sums 10 to 11 us (0.9 TB/s), the last sum 2 to 4 us,
 // where 512 smaller workgroups and floating-point keys took 11.6 and 10.6.  The
-// gradient of 8192 tokens 5.6 us (1.6 TB/s).
+// gradient of 8192 tokens 6.0 us (1.5 TB/s; 5.6 without the test for
+// probabilities of 0).
 #include <type_traits>
 
 #include "common.hpp"

@@ -319,7 +319,9 @@ class Learner:
     the router's weights) and ``update`` (one AdamW step, copies renewed).
 
     w_r [E, D], w_gu [E, 2F, D], w_dn [E, D, F]: fp32 master weights on the
-    GPU, updated in place.  T: tokens per step.  E, D % 32 == 0 (the router's
+    GPU, updated in place.  The gradient of the logits is rounded to bf16 for
+    the BF16 products that take it to x and w_r, as all other gradients that
+    enter a product are (half a step, 2^-8 relative).  T: tokens per step.  E, D % 32 == 0 (the router's
     GEMM), D, F % 128 == 0.  ``adamw``: keyword arguments of optim.AdamW."""
 
     def __init__(self, w_r, w_gu, w_dn, T, k, router_bias=None, score=ops.ROUTER_TOPK_SOFTMAX, **adamw):

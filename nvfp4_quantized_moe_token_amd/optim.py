@@ -32,7 +32,10 @@ class AdamW:
     params_bf16: for each fp32 parameter a bf16 tensor that every step
     overwrites with its rounded value (or None, for all or for one).
     state_bits: 32, or 8 (codes with one fp32 scale per 256 elements, rounded
-    stochastically).  seed: of that rounding.  step: updates already made.
+    stochastically).  seed: of that rounding, whose bits depend on it, the
+    update's number, the tensor's place in the list and the element: several
+    optimizers of one model (groups with other hyperparameters) take different
+    seeds.  step: updates already made.
     state: moments to go on with, a dict of lists: exp_avg, exp_avg_sq, and
     for 8 bits avg_scale, avg_sq_scale (kept, not copied); zeros otherwise.
     capturable: the step count and the learning rate live on the device
