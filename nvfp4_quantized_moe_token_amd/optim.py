@@ -6,7 +6,6 @@ takes; every step of the arithmetic runs in the HIP kernel.
 """
 
 import ctypes
-import types
 
 import torch
 
@@ -23,6 +22,18 @@ _capturing = torch.cuda.is_current_stream_capturing
 # torch's comparison of many tensors' addresses with known ones (183 in 5 us).
 _same_addresses = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal",
                           lambda ts, ptrs, at: list(map(_PTR, ts)) == ptrs)
+
+
+class _State(dict):
+    """A dict that refuses changes; saved and copied as a plain one."""
+
+    def _refuse(self, *args, **kw):
+        raise TypeError("the optimizer's state cannot be assigned to")
+
+    __setitem__ = __delitem__ = __ior__ = update = setdefault = pop = popitem = clear = _refuse
+
+    def __reduce__(self):
+        return dict, (dict(self),)
 
 
 class AdamW:
@@ -56,12 +67,12 @@ class AdamW:
         self.state_bits, self.seed, self.steps = state_bits, seed & 0xFFFFFFFF, step
         n = len(self.params)
         self._params_bf16 = (None,) * n if params_bf16 is None else tuple(params_bf16)
-        self._state = {}
+        self._state = _State()
         self._validate()
         names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
         if state is None:
             state = self._new_state()
-        self._state = {k: tuple(state[k]) for k in names}
+        self._state = _State({k: tuple(state[k]) for k in names})
         self._list = (_lib.AdamWTensor * n)()
         self._words = (ctypes.c_void_p * (_WORDS * n)).from_buffer(self._list)  # its fields, _WORDS per tensor
         self._held = [t for t in (*self.params, *self.params_bf16, *(t for k in names for t in self._state[k]))
@@ -87,7 +98,7 @@ class AdamW:
 
     @property
     def state(self):
-        return types.MappingProxyType(self._state)
+        return self._state
 
     def _validate(self):
         """Refuses tensors of the wrong dtype, size, device or layout."""

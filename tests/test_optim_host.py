@@ -2,7 +2,9 @@
 instead of made, on tensors in host memory."""
 
 import contextlib
+import copy
 import ctypes
+import io
 
 import pytest
 import torch
@@ -211,3 +213,19 @@ def test_moments_are_read_into_tensors_that_fit(library, bits):
     assert library.calls == []
     out = [z(2, 2), z(3)], [z(4), z(3, 1)]
     assert opt.state_values(out=out) is out
+
+
+def test_the_state_can_be_saved_and_gone_on_with(library):
+    opt = optim.AdamW([torch.zeros(300), torch.zeros(4)], state_bits=8)
+    opt.state["exp_avg"][0].fill_(3)
+    file = io.BytesIO()
+    torch.save(opt.state, file)
+    file.seek(0)
+    for state in (torch.load(file, weights_only=True), copy.deepcopy(opt.state), copy.copy(opt.state), dict(opt.state)):
+        assert type(state) is dict and list(state) == ["exp_avg", "exp_avg_sq", "avg_scale", "avg_sq_scale"]
+        again = optim.AdamW([torch.zeros(300), torch.zeros(4)], state_bits=8, state=state, step=opt.steps)
+        for k in state:
+            assert all(torch.equal(a, b) for a, b in zip(again.state[k], opt.state[k]))
+    for change in (lambda s: s.update(exp_avg=()), lambda s: s.pop("exp_avg"), lambda s: s.clear()):
+        with pytest.raises(TypeError):
+            change(opt.state)
