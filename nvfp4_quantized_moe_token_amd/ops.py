@@ -168,7 +168,8 @@ def moe_router_bwd(logits, topk_ids, d_topk_w, score=ROUTER_TOPK_SOFTMAX, scale=
                    d_prob_sum=None, out=None, out_dtype=None):
     """Gradient of moe_router's topk_w, lse and prob_sum with respect to the
     logits (d_topk_w, d_lse, d_prob_sum: None for zeros).  Returns d_logits
-    [T, E] of out_dtype (default: the logits' dtype)."""
+    [T, E] of out_dtype (default: the logits' dtype), written to out when given
+    (which must not overlap the logits)."""
     _need(logits, "logits", _FLOATS, None, None)
     T, E = logits.shape
     _need(topk_ids, "topk_ids", torch.int32, T, None)
@@ -390,7 +391,8 @@ def moe_unpermute_bwd(dout, y_perm, dest, offsets, k, topk_w=None, dy_perm=None,
     dout[t] (rows past offsets[E] are zeros) and d_topk_w[t, j] =
     <dout[t], y_perm[dest[t*k+j]]> (fp32).  y_perm may be None without the
     weight gradient.  amax_out (fp32 [1], optional) receives max |dy_perm|.
-    Returns (dy_perm or None, d_topk_w or None)."""
+    dy_perm must not overlap dout or y_perm.  Returns (dy_perm or None,
+    d_topk_w or None)."""
     _need(dout, "dout", _FLOATS, None, None)
     T, D = dout.shape
     R = T * k
@@ -693,6 +695,8 @@ def grouped_gemm_bf16(layout, a, b, offsets, num_experts=None, out=None, out_dty
         shape = (E, K, N)
     else:
         raise ValueError("layout must be NT, NN or TN")
+    if layout != TN and b.shape[0] < E:
+        raise ValueError("b: %d experts, the offsets are of %d" % (b.shape[0], E))
     _dev(a, b, offsets, out)
     out = torch.empty(shape, dtype=out_dtype, device=a.device) if out is None else out
     rc = _lib.load().grouped_gemm_bf16(layout, _ptr(a), _ptr(b), _ptr(offsets), E, M, N, K, _ptr(out),

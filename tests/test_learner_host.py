@@ -39,6 +39,8 @@ OFF = torch.tensor([0, 3, 6], dtype=torch.int32)
     (ops.NT, z(6, 64, dtype=torch.float16), z(2, 32, 64)),
     (ops.NT, z(6, 96), z(2, 32, 64)),                           # reads past b
     (ops.NN, z(6, 64), z(2, 32, 64)),
+    (ops.NT, z(6, 64), z(1, 32, 64)),                           # fewer experts than the offsets have
+    (ops.NN, z(6, 64), z(1, 64, 32)),
     (ops.TN, z(6, 64), z(5, 32)),
     (ops.TN, z(6, 64), z(6, 32, dtype=torch.float32))])
 def test_bf16_products_take_bf16_operands_that_fit(launched, layout, a, b):
