@@ -24,18 +24,6 @@ _same_addresses = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal",
                           lambda ts, ptrs, at: list(map(_PTR, ts)) == ptrs)
 
 
-class _State(dict):
-    """A dict that refuses changes; saved and copied as a plain one."""
-
-    def _refuse(self, *args, **kw):
-        raise TypeError("the optimizer's state cannot be assigned to")
-
-    __setitem__ = __delitem__ = __ior__ = update = setdefault = pop = popitem = clear = _refuse
-
-    def __reduce__(self):
-        return dict, (dict(self),)
-
-
 class AdamW:
     """AdamW (decoupled weight decay) over a list of contiguous parameters of
     one dtype (fp32, or bf16 rounded stochastically) on one GPU.
@@ -51,7 +39,13 @@ class AdamW:
     for 8 bits avg_scale, avg_sq_scale (kept, not copied); zeros otherwise.
     capturable: the step count and the learning rate live on the device
     (``step_dev`` int64 [1], ``lr_dev`` fp32 [1]), so a captured step counts
-    on at every replay.
+    on at every replay; without it a step is refused while a graph is captured.
+
+    ``params``, ``params_bf16`` and the tuples of ``state`` hold the tensors and
+    cannot be assigned to.  A tensor whose storage was replaced (``p.data =
+    ...``) and a list put in ``state`` in a tuple's place are noticed at the
+    next call, checked like new ones, and used from there on; a captured graph
+    keeps the addresses that it was captured with.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, params_bf16=None,
@@ -67,16 +61,14 @@ class AdamW:
         self.state_bits, self.seed, self.steps = state_bits, seed & 0xFFFFFFFF, step
         n = len(self.params)
         self._params_bf16 = (None,) * n if params_bf16 is None else tuple(params_bf16)
-        self._state = _State()
+        self._state = {}
         self._validate()
-        names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
         if state is None:
             state = self._new_state()
-        self._state = _State({k: tuple(state[k]) for k in names})
+        self._names = ("exp_avg", "exp_avg_sq") + (("avg_scale", "avg_sq_scale") if state_bits == 8 else ())
+        self._state = {k: state[k] for k in self._names}
         self._list = (_lib.AdamWTensor * n)()
         self._words = (ctypes.c_void_p * (_WORDS * n)).from_buffer(self._list)  # its fields, _WORDS per tensor
-        self._held = [t for t in (*self.params, *self.params_bf16, *(t for k in names for t in self._state[k]))
-                      if t is not None]
         self._take()
         dev = self.params[0].device
         self.step_dev = torch.full((1,), step, dtype=torch.int64, device=dev) if capturable else None
@@ -124,6 +116,8 @@ class AdamW:
     def _take(self):
         """Checks the tensors and lists their addresses for the library."""
         self._dtype = None
+        for k in self._names:
+            self._state[k] = tuple(self._state[k])
         self._validate()
         self._numel = list(map(_NUMEL, self.params))
         lists = dict(self._state, param=self.params, param_bf16=self.params_bf16)
@@ -131,13 +125,17 @@ class AdamW:
             d.n = self._numel[i]
             for k, ts in lists.items():
                 setattr(d, k, _ptr(ts[i]))
+        self._moments = [self._state[k] for k in self._names]
+        self._held = [t for ts in (self.params, self.params_bf16, *self._moments) for t in ts if t is not None]
         self._ptrs, self._all = list(map(_PTR, self._held)), list(range(len(self._held)))
         self._dtype = self.params[0].dtype
 
     def _refresh(self):
         """A tensor's storage may be another since the last call (``p.data =``,
         weights moved away and back): then the new one is checked and taken."""
-        if self.params[0].dtype is not self._dtype or not _same_addresses(self._held, self._ptrs, self._all):
+        if (self.params[0].dtype is not self._dtype
+                or any(self._state[k] is not ts for k, ts in zip(self._names, self._moments))
+                or not _same_addresses(self._held, self._ptrs, self._all)):
             self._take()
 
     def _same_sizes(self, name, ts, dtype, required=False, blocks=False):
