@@ -71,9 +71,14 @@ typedef struct ihipStream_t* nvfp4moe_stream_t; /* == hipStream_t */
 #define NVFP4MOE_NN 1 /* C[M,N]   = A[M,K] . B_e[K,N]    (data gradient)     */
 #define NVFP4MOE_TN 2 /* C_e[K,N] = A_e[M_e,K]^T . B_e[M_e,N] (weight grad)  */
 
-/* MX element formats for mx_quantize (the W4A8 variant) */
+/* MX element formats for mx_quantize (the W4A8 variant; activations kept) */
 #define NVFP4MOE_MX_E4M3 0 /* MXFP8: E4M3 elements, one byte each */
 #define NVFP4MOE_MX_E2M1 1 /* MXFP4: E2M1 elements, two per byte */
+#define NVFP4MOE_MX_INT8 2 /* MXINT8: 8-bit integers, one byte each */
+
+/* norms */
+#define NVFP4MOE_NORM_LAYER 0 /* mean and variance */
+#define NVFP4MOE_NORM_RMS 1   /* mean square only */
 
 /* W4A4 GEMM epilogues */
 #define NVFP4MOE_EPI_NONE 0
@@ -87,7 +92,7 @@ typedef struct ihipStream_t* nvfp4moe_stream_t; /* == hipStream_t */
 #define NVFP4MOE_ADAMW_BLOCK 256
 
 /* ABI version of this header; returned by nvfp4moe_abi_version(). */
-#define NVFP4MOE_ABI_VERSION 3
+#define NVFP4MOE_ABI_VERSION 4
 
 int nvfp4moe_abi_version(void);
 /* Static string for a status code (never NULL). */
@@ -316,6 +321,18 @@ int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, const void*
 int moe_permute_mxfp4(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D,
                       uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
                       size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream);
+
+/*
+ * moe_permute_int8 -- moe_permute_mx with 8-bit integer codes and one fp32 scale
+ * per row: the activations of grouped_gemm_int8.  q [T*k][D] (16-byte aligned),
+ * scales [T*k] fp32; D % 16 == 0.  Equal, bit for bit, to int8_quantize(x)
+ * followed by the row gather of codes and scales; rows past offsets[E] (skipped
+ * assignments) are zeros with scale 0.  Other arguments and errors as
+ * moe_permute_mx.
+ */
+int moe_permute_int8(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D,
+                     int8_t* q, float* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
+                     size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream);
 
 /*
  * moe_gather -- out[p] = w[src[p]] * x[src[p] / k] for p < R (w = 1 when
@@ -551,16 +568,34 @@ int grouped_gemm_w4a4_wgrad(const uint8_t* a_q, const uint8_t* a_s, const float*
  * Element = (V / 2^(S-127)) rounded to nearest even and saturated to 448
  * (E4M3) or 6 (E2M1); its sign bit is the sign of V (also for -0).  No global
  * scale, no amax pass: each block is encoded from its own values.
- *   x       [rows][K] F32 or BF16, 16-byte aligned, finite.
+ * NVFP4MOE_MX_INT8 is the form of activations kept for the backward pass: S is
+ * the exponent field of a (2^(S-127) <= a < 2^(S-126); 0 for a subnormal or
+ * zero), an element is V * 2^(133-S) rounded to nearest even, clamped to
+ * [-127, 127], and stands for code * 2^(S-133): off by at most 2^-7 a (2^-6 a
+ * where it was clamped).  A block that holds an infinity or a NaN gets S = 255,
+ * which reads back as NaN.
+ *   x       [rows][K] F32 or BF16, 16-byte aligned, finite (MXINT8: any).
  *   elem    NVFP4MOE_MX_E4M3: q [rows][K] bytes (16-byte aligned);
  *           NVFP4MOE_MX_E2M1: q [rows][K/2] bytes, element 2j in the low
- *           nibble (8-byte aligned).
+ *           nibble (8-byte aligned);
+ *           NVFP4MOE_MX_INT8: q [rows][K] bytes, two's complement (16-byte
+ *           aligned).
  *   scales  [rows][K/32] bytes out, row-major, unswizzled.
  * Bit-exact and independent of launch shape.  Errors: EINVAL (NULL,
  * negative, bad dtype or elem), ESHAPE (K % 32 != 0, alignment).
  */
 int mx_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int elem, uint8_t* q,
                 uint8_t* scales, nvfp4moe_stream_t stream);
+
+/*
+ * mx_dequantize -- the values of mx_quantize's codes (activations kept in 8
+ * bits, read back; [JA] fourth paragraph: the layout's codes and scales).
+ * q, scales, elem as mx_quantize gives them; out [rows][K] F32 or BF16 (RNE;
+ * exact but for values below the type's normal range), 16-byte aligned.  Scale
+ * bytes of 255 give NaN.  Errors as mx_quantize.
+ */
+int mx_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, int elem, void* out,
+                  int out_dtype, nvfp4moe_stream_t stream);
 
 /*
  * grouped_gemm_w4a8 -- the grouped GEMM of the W4A8 variant ([JA], third
@@ -649,6 +684,67 @@ int grouped_gemm_mxfp4_silu_gate(const uint8_t* a_q, const uint8_t* a_s, const u
                                  void* h, float* amax_out, uint8_t* q_h, uint8_t* s_h, nvfp4moe_stream_t stream);
 
 /*
+ * grouped_gemm_mxfp4_silu_gate_ckpt -- grouped_gemm_mxfp4_silu_gate that also
+ * keeps the bf16 Y1 in 8 bits, the form silu_gate_bwd_mx takes: q_y1 [M_total]
+ * [2F] (8-byte aligned) and s_y1 [M_total][2F/32] equal, bit for bit,
+ * mx_quantize(Y1, NVFP4MOE_MX_INT8).  Rows >= offsets[E] are not written.
+ * EINVAL for q_y1 or s_y1 NULL with work to do.
+ */
+int grouped_gemm_mxfp4_silu_gate_ckpt(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,
+                                      const int32_t* expert_offsets, int E, int64_t M_total, int64_t F, int64_t K,
+                                      void* y1, void* h, float* amax_out, uint8_t* q_h, uint8_t* s_h, uint8_t* q_y1,
+                                      uint8_t* s_y1, nvfp4moe_stream_t stream);
+
+/*
+ * int8_quantize -- rows of 8-bit integers with one fp32 scale each (token-wise
+ * quantization, [JA] fourth paragraph; here one scale per token, or per output
+ * channel of a weight).  Per row with amax a, in IEEE fp32: s = a / 127,
+ * q = x / s rounded to nearest even, clamped to [-127, 127], 0 when s is 0;
+ * a value is q * s.  A row that holds an infinity or a NaN gets s = infinity or
+ * NaN and zeros: its products are NaN.
+ *   x [rows][K] F32 or BF16, q [rows][K] out, scales [rows] fp32 out; K % 16 ==
+ *   0; x, q 16-byte aligned.
+ * Bit-exact and independent of launch shape.  Errors: EINVAL (NULL, negative,
+ * bad dtype), ESHAPE (K, alignment).
+ */
+int int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* q, float* scales,
+                  nvfp4moe_stream_t stream);
+
+/*
+ * grouped_gemm_int8 -- the grouped GEMM of 8-bit integers (W8A8, a precision
+ * beside [JA] third paragraph's; fourth: contiguous layout, grouped GEMM):
+ *   C[r][n] = (float)(sum_k a[r][k] b[e][n][k]) * a_s[r] * b_s[e][n],
+ * r in [offsets[e], offsets[e+1]), the sum exact in int32, then three fp32
+ * roundings in that order.  Rows >= offsets[E] are not written.
+ *   a_q [M_total][K], a_s [M_total] fp32   (moe_permute_int8, int8_quantize)
+ *   b_q [E][N][K],    b_s [E][N] fp32      (int8_quantize of the weights' rows)
+ *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).
+ * Codes of -128 count as such (the quantizer gives none).  K % 16 == 0, K <=
+ * 131072, N % 32 == 0, N <= 2^20, M_total < 2^31 - 256; a_q, b_q, c 16-byte
+ * aligned, scales 4-byte aligned.  K == 0 gives zeros.  Errors: EINVAL (NULL,
+ * negative, bad dtype), ESHAPE (shape and alignment rules).
+ */
+int grouped_gemm_int8(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
+                      const int32_t* expert_offsets, int E, int64_t M_total, int64_t N, int64_t K, void* c,
+                      int c_dtype, nvfp4moe_stream_t stream);
+
+/*
+ * grouped_gemm_int8_silu_gate -- the gate+up GEMM of 8-bit integers with the
+ * SiLU gate in the epilogue and, when q_y1 is given, Y1 kept in 8 bits there
+ * too ([JA] fourth paragraph: op fusion): equal, bit for bit, to
+ * grouped_gemm_int8 (N = 2F, B_e = [gate; up] rows, bf16 C), silu_gate_fwd and
+ * mx_quantize(Y1, NVFP4MOE_MX_INT8).
+ *   y1 [M_total][2F] bf16 or NULL, h [M_total][F] bf16, amax_out fp32 [1] or
+ *   NULL (max |H|); q_y1 [M_total][2F] (8-byte aligned) and s_y1
+ *   [M_total][2F/32], both or neither.
+ * F % 128 == 0, F <= 2^19, 2 F K < 2^31.  Other rules and errors as
+ * grouped_gemm_int8.
+ */
+int grouped_gemm_int8_silu_gate(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
+                                const int32_t* expert_offsets, int E, int64_t M_total, int64_t F, int64_t K, void* y1,
+                                void* h, float* amax_out, uint8_t* q_y1, uint8_t* s_y1, nvfp4moe_stream_t stream);
+
+/*
  * grouped_gemm_bf16 -- grouped BF16 GEMM, fp32 accumulation (the BF16
  * backward, [JA] first paragraph; also the BF16 baseline of the forward).
  *   NVFP4MOE_NT: a [M_total][K], b [E][N][K] -> c [M_total][N]
@@ -710,6 +806,50 @@ int silu_gate_fwd(const void* y1, int64_t R, int64_t F, void* h, float* amax_out
  */
 int silu_gate_bwd(const void* y1, const void* dh, int64_t R, int64_t F, void* dy1, float* amax_out,
                   nvfp4moe_stream_t stream);
+
+/*
+ * silu_gate_bwd_mx -- silu_gate_bwd from Y1 kept in 8 bits, and H from the same
+ * values (for the weight gradient of the product it went into): the backward
+ * of a forward pass that stored neither in bf16 ([JA] first paragraph: the BF16
+ * backward).  q_y1 [R][2F], s_y1 [R][2F/32] as grouped_gemm_*_silu_gate and
+ * mx_quantize(NVFP4MOE_MX_INT8) write them; dh [R][F] bf16, dy1 [R][2F] bf16
+ * out, h [R][F] bf16 out or NULL; outputs must not overlap inputs.  F % 32 == 0;
+ * 16-byte aligned q_y1, dh, dy1, h.  Errors: EINVAL (NULL, negative), ESHAPE.
+ */
+int silu_gate_bwd_mx(const uint8_t* q_y1, const uint8_t* s_y1, const void* dh, int64_t R, int64_t F, void* dy1,
+                     void* h, nvfp4moe_stream_t stream);
+
+/*
+ * layer_norm -- the norm in front of the layer (the pages name none; [JA] first
+ * paragraph: the learner's step it belongs to).  Per row of D elements, fp32:
+ *   LAYER: y = (x - m) r w + b, m = mean(x), r = 1/sqrt(mean((x - m)^2) + eps)
+ *   RMS:   y = x r w + b, r = 1/sqrt(mean(x^2) + eps)
+ *   x [T][D] F32 or BF16; w, b [D] of w_dtype (F32 or BF16) or NULL (1 and 0);
+ *   y [T][D] F32 or BF16 (RNE); mean (NULL for RMS), rstd [T] fp32 or NULL: m
+ *   and r for the backward pass.
+ * 1 <= D <= 16384; pointers aligned to their elements (faster at 16 bytes with
+ * D % 8 == 0).  y must not overlap x, w or b.  Errors: EINVAL (NULL, negative, bad dtype or
+ * kind, eps below 0 or NaN, mean with RMS), ESHAPE (D, alignment).
+ */
+int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, const void* w, const void* b, int w_dtype,
+               float eps, int kind, void* y, int y_dtype, float* mean, float* rstd, nvfp4moe_stream_t stream);
+
+/*
+ * layer_norm_bwd -- gradient of layer_norm with respect to x, w and b:
+ *   h = (x - m) r, g = dy w, dx = r (g - mean(g) - h mean(g h))  (RMS: without mean(g))
+ *   dw = sum over rows of dy h, db = sum over rows of dy
+ *   dy [T][D], x [T][D] F32 or BF16 each, w as in layer_norm, mean and rstd of
+ *   the forward pass (mean NULL for RMS).
+ *   dx [T][D] F32 or BF16 or NULL; dw, db [D] fp32 or NULL (overwritten; zeros
+ *   for T == 0).  At least one of the three; none may overlap an input.
+ *   workspace of layer_norm_bwd_workspace_size(T, D) bytes, 16-byte aligned,
+ *   for dw or db (else NULL will do); its content need not be kept.
+ * The same bits on every run (no atomics).  Errors as layer_norm, EWORKSPACE.
+ */
+size_t layer_norm_bwd_workspace_size(int64_t T, int64_t D);
+int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t T, int64_t D, const void* w,
+                   int w_dtype, const float* mean, const float* rstd, int kind, void* dx, int dx_dtype, float* dw,
+                   float* db, void* workspace, size_t ws_bytes, nvfp4moe_stream_t stream);
 
 /*
  * adamw_step -- one AdamW step (decoupled weight decay) over `count` tensors,

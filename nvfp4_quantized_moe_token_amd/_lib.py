@@ -78,6 +78,21 @@ SIGNATURES = {
     "adamw_step": (c_int, [c_vp, c_int, c_int, c_int, c_int, c_double, c_double, c_double, c_double, c_double, c_i64,
                            c_vp, c_vp, c_vp, c_vp, c_u32, c_vp]),
     "adamw_read_state": (c_int, [c_vp, c_int, c_vp, c_vp, c_vp]),
+    "moe_permute_int8": (c_int, [c_vp, c_i64, c_int, c_int, c_vp, c_int, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                 c_size, c_vp, c_vp]),
+    "mx_dequantize": (c_int, [c_vp, c_vp, c_i64, c_i64, c_int, c_vp, c_int, c_vp]),
+    "grouped_gemm_mxfp4_silu_gate_ckpt": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                                  c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "int8_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "grouped_gemm_int8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_int, c_vp]),
+    "grouped_gemm_int8_silu_gate": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                            c_vp, c_vp, c_vp, c_vp]),
+    "silu_gate_bwd_mx": (c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "layer_norm": (c_int, [c_vp, c_int, c_i64, c_i64, c_vp, c_vp, c_int, c_float, c_int, c_vp, c_int, c_vp, c_vp,
+                           c_vp]),
+    "layer_norm_bwd_workspace_size": (c_size, [c_i64, c_i64]),
+    "layer_norm_bwd": (c_int, [c_vp, c_int, c_vp, c_int, c_i64, c_i64, c_vp, c_int, c_vp, c_vp, c_int, c_vp, c_int,
+                               c_vp, c_vp, c_vp, c_size, c_vp]),
     "silu_gate_fwd": (c_int, [c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "silu_gate_bwd": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp]),
 }
@@ -87,10 +102,11 @@ OK, EINVAL, ESHAPE, EARCH, ELAUNCH, EWORKSPACE = 0, -1, -2, -3, -4, -5
 F32, BF16, U8 = 0, 1, 2
 NT, NN, TN = 0, 1, 2
 EPI_NONE, EPI_SILU_GATE = 0, 1
-MX_E4M3, MX_E2M1 = 0, 1
+MX_E4M3, MX_E2M1, MX_INT8 = 0, 1, 2
+NORM_LAYER, NORM_RMS = 0, 1
 ROUTER_TOPK_SOFTMAX, ROUTER_SOFTMAX = 0, 1
 ADAMW_BLOCK = 256
-ABI_VERSION = 3
+ABI_VERSION = 4
 NOALLOC_SCRATCH_BYTES = 2 << 20
 STATUS_BAD_EXPERT = 1
 

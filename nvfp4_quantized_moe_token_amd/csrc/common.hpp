@@ -121,7 +121,10 @@ int mx_quantize_scatter_launch(const void* x, int x_dtype, int64_t T, int k, int
                                const int32_t* offsets, int E, uint8_t* q, uint8_t* scales, hipStream_t st);
 int mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int64_t K, int elem, uint8_t* q, uint8_t* scales,
                        hipStream_t st);
-// The same without clearing amax_out (an earlier launch on the stream did).
+// 8-bit integer quantize-scatter (int8.hip); as above, D % 16 == 0.
+int int8_quantize_scatter_launch(const void* x, int x_dtype, int64_t T, int k, int64_t D, const int32_t* dest,
+                                 const int32_t* offsets, int E, int8_t* q, float* scales, hipStream_t st);
+// launch_amax without clearing amax_out (an earlier launch on the stream did).
 int launch_amax_uncleared(const void* x, int x_dtype, int64_t n16_per_group, int64_t groups, float* amax_out,
                           hipStream_t st);
 

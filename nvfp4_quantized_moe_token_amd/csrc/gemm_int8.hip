@@ -1,0 +1,94 @@
+// Grouped W8A8 GEMM over the contiguous per-expert layout: 8-bit integers with
+// one fp32 scale per row (token) of A and per row (output channel) of B_e,
+//   C[r][n] = (float)(sum_k a[r][k] b[n][k]) * as[r] * bs[e][n],
+// the sum exact in int32 (v_mfma_i32_32x32x32_i8; K <= 131072 keeps it below
+// 2^31), then three fp32 roundings: of the sum and of the two products.
+// The 8-bit integer form of the experts' products stands beside the report's
+// W4A8 and W4A4 ("miniTE報告、NVFP4強化学習の安定性を検証", third paragraph: the
+// precisions compared; fourth: grouped GEMM, op fusion).
+//
+// The kernel and its epilogues are in gemm_codes.hpp.
+#include "gemm_codes.hpp"
+
+namespace nvfp4moe {
+namespace {
+
+// Tiles by the mean rows per expert, as for MXFP4.
+template <int EPI, bool OUT32>
+int launch_epi(const Params& p, hipStream_t st) {
+  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<INT8, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<INT8, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<INT8, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  return launch_tiles<INT8, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+}
+
+// Argument checks shared by both entry points, then the launch parameters.
+int check_operands(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
+                   const int32_t* expert_offsets, int E, int64_t M_total, int64_t N, int64_t K, Params& p) {
+  if (E < 1 || M_total < 0 || N < 0 || K < 0) return NVFP4MOE_EINVAL;
+  if (!expert_offsets) return NVFP4MOE_EINVAL;
+  if (M_total > 0 && N > 0 && (!a_s || !b_s || (K > 0 && (!a_q || !b_q)))) return NVFP4MOE_EINVAL;
+  if (K % 16 != 0 || N % 32 != 0) return NVFP4MOE_ESHAPE;
+  // a tile's operand region is read through 32-bit offsets; the sums stay exact
+  if (M_total >= 0x7FFFFF00LL || N > (1 << 20) || K > (1 << 17)) return NVFP4MOE_ESHAPE;
+  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(expert_offsets, 4))
+    return NVFP4MOE_ESHAPE;
+  p = Params{};
+  p.a = reinterpret_cast<const uint8_t*>(a_q);
+  p.b = reinterpret_cast<const uint8_t*>(b_q);
+  p.as = a_s;
+  p.bs = b_s;
+  p.offsets = expert_offsets;
+  p.M = M_total;
+  p.N = N;
+  p.K = K;
+  p.E = E;
+  return NVFP4MOE_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" int grouped_gemm_int8(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
+                                 const int32_t* expert_offsets, int E, int64_t M_total, int64_t N, int64_t K, void* c,
+                                 int c_dtype, nvfp4moe_stream_t stream) {
+  Params p;
+  if (c_dtype != NVFP4MOE_F32 && c_dtype != NVFP4MOE_BF16) return NVFP4MOE_EINVAL;
+  if (M_total > 0 && N > 0 && !c) return NVFP4MOE_EINVAL;
+  const int rc = check_operands(a_q, a_s, b_q, b_s, expert_offsets, E, M_total, N, K, p);
+  if (rc != NVFP4MOE_OK) return rc;
+  if (!aligned(c, 16)) return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  if (M_total == 0 || N == 0) return NVFP4MOE_OK;
+  p.c = c;
+  hipStream_t st = as_stream(stream);
+  return c_dtype == NVFP4MOE_F32 ? launch_epi<EPI_PLAIN, true>(p, st) : launch_epi<EPI_PLAIN, false>(p, st);
+}
+
+extern "C" int grouped_gemm_int8_silu_gate(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
+                                           const int32_t* expert_offsets, int E, int64_t M_total, int64_t F, int64_t K,
+                                           void* y1, void* h, float* amax_out, uint8_t* q_y1, uint8_t* s_y1,
+                                           nvfp4moe_stream_t stream) {
+  Params p;
+  if (F < 0 || F > 0x3FFFFFFFLL) return F < 0 ? NVFP4MOE_EINVAL : NVFP4MOE_ESHAPE;
+  if ((q_y1 != nullptr) != (s_y1 != nullptr)) return NVFP4MOE_EINVAL;
+  if (M_total > 0 && F > 0 && !h) return NVFP4MOE_EINVAL;
+  const int rc = check_operands(a_q, a_s, b_q, b_s, expert_offsets, E, M_total, 2 * F, K, p);
+  if (rc != NVFP4MOE_OK) return rc;
+  if (F % 128 != 0 || 2 * F * K >= (1LL << 31)) return NVFP4MOE_ESHAPE;  // gate and up rows: one region
+  if (!aligned(y1, 16) || !aligned(h, 16) || !aligned(q_y1, 8) || !aligned(amax_out, 4)) return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  hipStream_t st = as_stream(stream);
+  if (amax_out) fill_u32_kernel<<<1, 64, 0, st>>>(reinterpret_cast<uint32_t*>(amax_out), 0u, 1);
+  if (M_total == 0 || F == 0) return launch_status();
+  p.c = y1;
+  p.h = h;
+  p.amax = amax_out;
+  p.yq = q_y1;
+  p.ys = s_y1;
+  return q_y1 ? launch_epi<EPI_SILU_C, false>(p, st) : launch_epi<EPI_SILU, false>(p, st);
+}

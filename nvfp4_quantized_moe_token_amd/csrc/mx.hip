@@ -1,6 +1,8 @@
 // MX quantization for the W4A8 variant: MXFP8 (E4M3 elements) activations
 // and MXFP4 (E2M1 elements) weights, each 32 consecutive elements along K
-// sharing one E8M0 (power-of-two) scale.
+// sharing one E8M0 (power-of-two) scale; and MXINT8 (8-bit integers, the rule in
+// mx_codec.hpp), in which activations are kept for the backward pass, with the
+// decoder of all three.
 //
 // The W4A8 activation-precision variant is the one the report's ablation
 // sets between W4A16 and W4A4 ("miniTE報告、NVFP4強化学習の安定性を検証",
@@ -36,12 +38,16 @@ __device__ __forceinline__ uint2 encode16_e2m1(const float (&v)[16], int se) {
   return make_uint2(encode8_e2m1(v, se), encode8_e2m1(v + 8, se));
 }
 
+// 16 fp32 values to MXINT8 codes (16 bytes).
+__device__ __forceinline__ uint4 encode16_int8(const float (&v)[16], int s) {
+  return make_uint4(encode4_int8(v, s), encode4_int8(v + 4, s), encode4_int8(v + 8, s), encode4_int8(v + 12, s));
+}
+
 // One thread per 16-element half-block; half-blocks 2b and 2b+1 (lanes of
 // one wave: the count is even) form block b.
-template <int NT, bool BF16, bool E4M3>
+template <int NT, bool BF16, int ELEM>
 __global__ __launch_bounds__(NT) void mx_quantize_kernel(const uint4* __restrict__ x, int64_t nhalf,
                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
-  constexpr int EMAX = E4M3 ? 8 : 2;
   for (int64_t hb = blockIdx.x * (int64_t)NT + threadIdx.x; hb < nhalf; hb += (int64_t)gridDim.x * NT) {
     float v[16];
     if (BF16) {
@@ -62,16 +68,81 @@ __global__ __launch_bounds__(NT) void mx_quantize_kernel(const uint4* __restrict
         v[4 * i + 3] = __uint_as_float(w.w);
       }
     }
-    float a = 0.0f;
+    int S;  // the scale byte
+    if constexpr (ELEM == NVFP4MOE_MX_INT8) {
+      uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));
-    a = fmaxf(a, __shfl_xor(a, 1, 64));  // the partner half of the block
-    const int se = shared_exp<EMAX>(a);
-    if (E4M3)
-      reinterpret_cast<uint4*>(q)[hb] = encode16_e4m3(v, se);
-    else
-      reinterpret_cast<uint2*>(q)[hb] = encode16_e2m1(v, se);
-    if ((hb & 1) == 0) scales[hb >> 1] = (uint8_t)(se + 127);
+      for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+      a = max(a, (uint32_t)__shfl_xor((int)a, 1, 64));  // the partner half of the block
+      S = int8_scale(a);
+      reinterpret_cast<uint4*>(q)[hb] = encode16_int8(v, S);
+    } else {
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));
+      a = fmaxf(a, __shfl_xor(a, 1, 64));  // the partner half of the block
+      const int se = shared_exp<ELEM == NVFP4MOE_MX_E4M3 ? 8 : 2>(a);
+      if constexpr (ELEM == NVFP4MOE_MX_E4M3)
+        reinterpret_cast<uint4*>(q)[hb] = encode16_e4m3(v, se);
+      else
+        reinterpret_cast<uint2*>(q)[hb] = encode16_e2m1(v, se);
+      S = se + 127;
+    }
+    if ((hb & 1) == 0) scales[hb >> 1] = (uint8_t)S;
+  }
+}
+
+// One thread per 16-element half-block: value = element * 2^(S - 127) (MXINT8:
+// code * 2^(S - 133)), exact in fp32 but for what falls below its subnormals;
+// S = 255 reads as NaN.  bf16 holds 8 significant bits, so it holds the 4-bit
+// and MXINT8 values exactly (above its own subnormals) and MXFP8's 4 bits.
+template <int NT, int ELEM, bool BF16>
+__global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __restrict__ q,
+                                                           const uint8_t* __restrict__ scales, int64_t nhalf,
+                                                           uint4* __restrict__ out) {
+  for (int64_t hb = blockIdx.x * (int64_t)NT + threadIdx.x; hb < nhalf; hb += (int64_t)gridDim.x * NT) {
+    const int S = scales[hb >> 1];
+    float v[16];
+    if constexpr (ELEM == NVFP4MOE_MX_E2M1) {
+      const uint2 w = reinterpret_cast<const uint2*>(q)[hb];
+      const uint32_t ws[2] = {w.x, w.y};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t c = ws[i / 8] >> (4 * (i % 8)), m = c & 7;
+        // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
+        const float e = m < 4 ? 0.5f * (float)m : m < 6 ? (float)m - 2.0f : 2.0f * (float)m - 8.0f;
+        v[i] = c & 8 ? -e : e;
+      }
+    } else {
+      const uint4 w = reinterpret_cast<const uint4*>(q)[hb];
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (ELEM == NVFP4MOE_MX_INT8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * i + j] = (float)(int8_t)(ws[i] >> (8 * j));
+        } else {
+          v[4 * i] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i], 0);
+          v[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i], 1);
+          v[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i], 2);
+          v[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8((int)ws[i], 3);
+        }
+      }
+    }
+    constexpr int BIAS = ELEM == NVFP4MOE_MX_INT8 ? 133 : 127;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = S == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[i], S - BIAS);
+    if constexpr (BF16) {
+      out[2 * hb] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+      out[2 * hb + 1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                                   pack_bf16x2(v[14], v[15]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        out[4 * hb + i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    }
   }
 }
 
@@ -170,11 +241,16 @@ int mx_quantize_launch(const void* x, int x_dtype, int64_t rows, int64_t K, int 
   int64_t grid = cdiv(nhalf, NT);
   if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
   const uint4* xv = reinterpret_cast<const uint4*>(x);
-  const bool bf = x_dtype == NVFP4MOE_BF16, e4 = elem == NVFP4MOE_MX_E4M3;
-  if (bf && e4) mx_quantize_kernel<NT, true, true><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);
-  else if (bf) mx_quantize_kernel<NT, true, false><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);
-  else if (e4) mx_quantize_kernel<NT, false, true><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);
-  else mx_quantize_kernel<NT, false, false><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);
+  const bool bf = x_dtype == NVFP4MOE_BF16;
+#define MXQ(EL)                                                                                             \
+  do {                                                                                                      \
+    if (bf) mx_quantize_kernel<NT, true, EL><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);          \
+    else mx_quantize_kernel<NT, false, EL><<<(unsigned)grid, NT, 0, st>>>(xv, nhalf, q, scales);            \
+  } while (0)
+  if (elem == NVFP4MOE_MX_E4M3) MXQ(NVFP4MOE_MX_E4M3);
+  else if (elem == NVFP4MOE_MX_INT8) MXQ(NVFP4MOE_MX_INT8);
+  else MXQ(NVFP4MOE_MX_E2M1);
+#undef MXQ
   return launch_status();
 }
 
@@ -185,12 +261,43 @@ extern "C" int mx_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, 
   using namespace nvfp4moe;
   if (rows < 0 || K < 0) return NVFP4MOE_EINVAL;
   if (x_dtype != NVFP4MOE_F32 && x_dtype != NVFP4MOE_BF16) return NVFP4MOE_EINVAL;
-  if (elem != NVFP4MOE_MX_E4M3 && elem != NVFP4MOE_MX_E2M1) return NVFP4MOE_EINVAL;
+  if (elem != NVFP4MOE_MX_E4M3 && elem != NVFP4MOE_MX_E2M1 && elem != NVFP4MOE_MX_INT8) return NVFP4MOE_EINVAL;
   if (rows * K > 0 && (!x || !q || !scales)) return NVFP4MOE_EINVAL;
   if (K % 32 != 0) return NVFP4MOE_ESHAPE;
-  if (rows * K > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E4M3 ? 16 : 8))) return NVFP4MOE_ESHAPE;
+  if (rows * K > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E2M1 ? 8 : 16))) return NVFP4MOE_ESHAPE;
   const int arch = check_arch();
   if (arch != NVFP4MOE_OK) return arch;
   if (rows * K == 0) return NVFP4MOE_OK;
   return mx_quantize_launch(x, x_dtype, rows, K, elem, q, scales, as_stream(stream));
+}
+
+extern "C" int mx_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t K, int elem, void* out,
+                             int out_dtype, nvfp4moe_stream_t stream) {
+  using namespace nvfp4moe;
+  if (rows < 0 || K < 0) return NVFP4MOE_EINVAL;
+  if (out_dtype != NVFP4MOE_F32 && out_dtype != NVFP4MOE_BF16) return NVFP4MOE_EINVAL;
+  if (elem != NVFP4MOE_MX_E4M3 && elem != NVFP4MOE_MX_E2M1 && elem != NVFP4MOE_MX_INT8) return NVFP4MOE_EINVAL;
+  if (rows * K > 0 && (!out || !q || !scales)) return NVFP4MOE_EINVAL;
+  if (K % 32 != 0) return NVFP4MOE_ESHAPE;
+  if (rows * K > 0 && (!aligned(out, 16) || !aligned(q, elem == NVFP4MOE_MX_E2M1 ? 8 : 16))) return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  if (rows * K == 0) return NVFP4MOE_OK;
+  constexpr int NT = 256;
+  const int64_t nhalf = rows * (K / 16);
+  int64_t grid = cdiv(nhalf, NT);
+  if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
+  hipStream_t st = as_stream(stream);
+  uint4* o = reinterpret_cast<uint4*>(out);
+  const bool bf = out_dtype == NVFP4MOE_BF16;
+#define MXD(EL)                                                                                   \
+  do {                                                                                            \
+    if (bf) mx_dequantize_kernel<NT, EL, true><<<(unsigned)grid, NT, 0, st>>>(q, scales, nhalf, o); \
+    else mx_dequantize_kernel<NT, EL, false><<<(unsigned)grid, NT, 0, st>>>(q, scales, nhalf, o);   \
+  } while (0)
+  if (elem == NVFP4MOE_MX_E4M3) MXD(NVFP4MOE_MX_E4M3);
+  else if (elem == NVFP4MOE_MX_INT8) MXD(NVFP4MOE_MX_INT8);
+  else MXD(NVFP4MOE_MX_E2M1);
+#undef MXD
+  return launch_status();
 }

@@ -1,6 +1,6 @@
-// MX (microscaling) encoding shared by the MX quantizer and the W4A8
-// gate+up epilogue that requantizes H: the E8M0 shared exponent of a block
-// and the E4M3 element encoding.  The rule (the published microscaling one;
+// MX (microscaling) encoding shared by the MX quantizer and the gate+up
+// epilogues that quantize H or Y1: the E8M0 shared exponent of a block and the
+// encodings of its elements.  The rule (the published microscaling one;
 // the pages do not define MX): for a block with amax a > 0 the shared scale
 // is X = 2^(floor(log2 a) - emax) (emax = 8 for E4M3, 2 for E2M1), clamped
 // to 2^[-127, 127], and 2^-127 for an all-zero block; every element is V / X
@@ -54,6 +54,34 @@ __device__ __forceinline__ uint32_t encode8_e2m1(const float* v, int se) {
   MXQ_PAIR(6, 3);
 #undef MXQ_PAIR
   return w;
+}
+
+// MXINT8, the form of activations kept for the backward pass: a block of 32
+// shares S, an element is a whole number q in [-127, 127] and stands for
+// q * 2^(S - 133).  With the block's amax a, S is the exponent field of a
+// (2^(S-127) <= a < 2^(S-126); 0 for a subnormal or zero a), so that a / step is
+// in [64, 128): rounding is off by half a step, 2^-7 of a, and by less than a
+// step where it would give 128.  S = 255 (a block that holds an infinity or a
+// NaN) reads back as NaN, so a gradient shows what the forward pass met.
+
+// S of a block from the greatest of its elements' bits without their signs.
+__device__ __forceinline__ int int8_scale(uint32_t amax_bits) { return (int)(amax_bits >> 23); }
+
+// 4 fp32 values to codes (element i in byte i).  v * 2^(133 - S) is exact or
+// far below a half; adding 1.5 * 2^23 rounds to nearest even and leaves the
+// whole number's low byte in the sum's.
+__device__ __forceinline__ uint32_t encode4_int8(const float* v, int s) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    b[i] = __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_ldexpf(v[i], 133 - s), -127.0f, 127.0f) + 12582912.0f);
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u),
+                               0x05040100u);
+}
+
+// Value of a code.
+__device__ __forceinline__ float decode_int8(int q, int s) {
+  return s == 255 ? __builtin_nanf("") : __builtin_ldexpf((float)q, s - 133);
 }
 
 }  // namespace nvfp4moe

@@ -1,0 +1,414 @@
+// Layer norm in front of the layer, and its RMS form (the norm of the Qwen3
+// layers whose shapes the library's workloads take), forward and backward with
+// the reduction of the weight's and bias's gradients ("miniTE報告、NVFP4強化学習
+// の安定性を検証", first paragraph: the learner's update in BF16; the pages name
+// no norm).
+//
+// Mathematics, per row x of D elements, m its mean (RMS: 0):
+//   r = 1 / sqrt(mean((x - m)^2) + eps),  h = (x - m) r,  y = h w + b
+//   g = dy w,  dx = r (g - mean(g) - h mean(g h))     (RMS: without mean(g))
+//   dw = sum over rows of dy h,  db = sum over rows of dy
+// All sums are fp32; the variance is the mean square of the differences, taken
+// from registers after the mean, so a large mean costs it nothing.
+//
+// Layout.  A row belongs to one wave up to 2048 elements (512 if they are read
+// singly), to a workgroup beyond; its elements stay in registers from the load
+// to the store, so every tensor is read once and written once.  Lanes take 8
+// consecutive elements where the row length and the pointers allow 16-byte
+// accesses, single ones otherwise.  Groups go round over the rows and keep the
+// weights, and in the backward pass the columns' sums, in registers.  The
+// sums of a workgroup go to the workspace as one row, and a second launch adds
+// those rows in order: no atomics, the same bits every time.
+#include <type_traits>
+
+#include "common.hpp"
+
+namespace nvfp4moe {
+namespace {
+
+constexpr int kNormMaxD = 16384;
+constexpr int kNormBwdBlocks = 256;  // rows of partial sums at most
+
+struct NormParams {
+  const void* x;
+  const void* dy;
+  const void* w;
+  const void* b;
+  const float* mean_in;
+  const float* rstd_in;
+  void* out;  // y or dx
+  float* mean;
+  float* rstd;
+  float* part;  // backward: [2][gridDim.x][D] partial sums of dw, db
+  int64_t T;
+  int D;
+  float eps;
+  bool x_bf16, dy_bf16, w_bf16, out_bf16, rms, want_dw, want_db;
+};
+
+// Elements (c * NT + t) * W + 0..W-1, c < NC, of a row, zeros past its end.
+template <int NT, int NC, int W>
+__device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at, int D, int t, float (&v)[NC * W]) {
+  if (bf16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * W;
+      if constexpr (W == 8) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (col < D) q = *reinterpret_cast<const uint4*>(p + col);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[c * W + 2 * i] = bf16_lo(u[i]);
+          v[c * W + 2 * i + 1] = bf16_hi(u[i]);
+        }
+      } else {
+        v[c] = col < D ? bf16_lo(p[col]) : 0.0f;
+      }
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(base) + at;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * W;
+      if constexpr (W == 8) {
+        float4 a = make_float4(0, 0, 0, 0), b = a;
+        if (col < D) {
+          a = *reinterpret_cast<const float4*>(p + col);
+          b = *reinterpret_cast<const float4*>(p + col + 4);
+        }
+        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c * W + i] = u[i];
+      } else {
+        v[c] = col < D ? p[col] : 0.0f;
+      }
+    }
+  }
+}
+
+template <int NT, int NC, int W>
+__device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int D, int t, const float (&v)[NC * W]) {
+  if (bf16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * W;
+      if (col >= D) continue;
+      if constexpr (W == 8) {
+        const float* a = v + c * W;
+        *reinterpret_cast<uint4*>(p + col) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                        pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+      } else {
+        p[col] = (uint16_t)f32_to_bf16_rne(v[c]);
+      }
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(base) + at;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int col = (c * NT + t) * W;
+      if (col >= D) continue;
+      if constexpr (W == 8) {
+        const float* a = v + c * W;
+        *reinterpret_cast<float4*>(p + col) = make_float4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<float4*>(p + col + 4) = make_float4(a[4], a[5], a[6], a[7]);
+      } else {
+        p[col] = v[c];
+      }
+    }
+  }
+}
+
+// Sums over the NT threads of a row (a wave, or the whole workgroup, which then
+// calls this together); every thread receives the same bits.  `turn` alternates
+// between two buffers, so one barrier a call is enough.
+template <int NT, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], int& turn) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], o, 64);
+  if constexpr (NT > 64) {
+    __shared__ float red[2][2][NT / 64];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((threadIdx.x & 63) == 0) red[turn][i][threadIdx.x >> 6] = s[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float a = red[turn][i][0];
+#pragma unroll
+      for (int w = 1; w < NT / 64; ++w) a += red[turn][i][w];
+      s[i] = a;
+    }
+    turn ^= 1;
+  }
+}
+
+template <int NT>
+constexpr int threads() {
+  return NT < 256 ? 256 : NT;
+}
+
+template <int NT, int NC, int W>
+__global__ __launch_bounds__(threads<NT>()) void norm_fwd_kernel(NormParams p) {
+  constexpr int N = NC * W, GROUPS = threads<NT>() / NT;
+  const int t = threadIdx.x % NT, D = p.D;
+  const float inv_d = 1.0f / (float)D;
+  float w[N], b[N];
+  if (p.w) load_row<NT, NC, W>(p.w, p.w_bf16, 0, D, t, w);
+  if (p.b) load_row<NT, NC, W>(p.b, p.w_bf16, 0, D, t, b);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!p.w) w[i] = 1.0f;
+    if (!p.b) b[i] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT; row < p.T; row += (int64_t)gridDim.x * GROUPS) {
+    float v[N];
+    load_row<NT, NC, W>(p.x, p.x_bf16, row * D, D, t, v);
+    float m = 0.0f;
+    if (!p.rms) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[0] += v[i];
+      row_sums<NT, 1>(s, turn);
+      m = s[0] * inv_d;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[c * W + i] = (c * NT + t) * W < D ? v[c * W + i] - m : 0.0f;
+    }
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[0] += v[i] * v[i];
+    row_sums<NT, 1>(s, turn);
+    const float r = 1.0f / sqrtf(s[0] * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i] + b[i];
+    store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, v);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = m;
+      if (p.rstd) p.rstd[row] = r;
+    }
+  }
+}
+
+template <int NT, int NC, int W>
+__global__ __launch_bounds__(threads<NT>()) void norm_bwd_kernel(NormParams p) {
+  constexpr int N = NC * W, GROUPS = threads<NT>() / NT;
+  const int t = threadIdx.x % NT, D = p.D;
+  const float inv_d = 1.0f / (float)D;
+  float w[N], dw[N], db[N];
+  if (p.w) load_row<NT, NC, W>(p.w, p.w_bf16, 0, D, t, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!p.w) w[i] = 1.0f;
+    dw[i] = db[i] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT; row < p.T; row += (int64_t)gridDim.x * GROUPS) {
+    float h[N], dy[N];
+    load_row<NT, NC, W>(p.x, p.x_bf16, row * D, D, t, h);
+    load_row<NT, NC, W>(p.dy, p.dy_bf16, row * D, D, t, dy);
+    const float r = p.rstd_in[row], m = p.rms ? 0.0f : p.mean_in[row];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = c * W; i < c * W + W; ++i) {
+        h[i] = (c * NT + t) * W < D ? (h[i] - m) * r : 0.0f;
+        dw[i] += dy[i] * h[i];
+        db[i] += dy[i];
+        dy[i] *= w[i];
+        s[0] += dy[i] * h[i];
+        s[1] += dy[i];
+      }
+    if (p.out) {
+      row_sums<NT, 2>(s, turn);
+      const float gh = s[0] * inv_d, g = p.rms ? 0.0f : s[1] * inv_d;
+#pragma unroll
+      for (int i = 0; i < N; ++i) h[i] = r * (dy[i] - g - h[i] * gh);
+      store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, h);
+    }
+  }
+  // This workgroup's sums.
+  float* to = p.part + (int64_t)blockIdx.x * D;
+  const int64_t db_at = (int64_t)gridDim.x * D;
+  if constexpr (GROUPS == 1) {
+    if (p.want_dw) store_row<NT, NC, W>(to, false, 0, D, t, dw);
+    if (p.want_db) store_row<NT, NC, W>(to + db_at, false, 0, D, t, db);
+  } else {
+    __shared__ __attribute__((aligned(16))) float sum[NT * N];
+    for (int which = 0; which < 2; ++which) {
+      if (!(which ? p.want_db : p.want_dw)) continue;
+      for (int g = 0; g < GROUPS; ++g) {  // the groups add their sums in turn
+        if ((int)threadIdx.x / NT == g) {
+          float a[N];
+          if (g > 0) load_row<NT, NC, W>(sum, false, 0, D, t, a);
+#pragma unroll
+          for (int i = 0; i < N; ++i) a[i] = (g > 0 ? a[i] : 0.0f) + (which ? db[i] : dw[i]);
+          if (g + 1 < GROUPS) store_row<NT, NC, W>(sum, false, 0, D, t, a);
+          else store_row<NT, NC, W>(to + which * db_at, false, 0, D, t, a);
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// Column sums of rows partial sums: 32 columns a workgroup, 8 groups of rows.
+__global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, int rows, int D, float* dw, float* db) {
+  __shared__ float red[8][33];
+  const float* from = part + (int64_t)blockIdx.y * rows * D;
+  float* to = blockIdx.y ? db : dw;
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  float s = 0.0f;
+  if (to && col < D)
+    for (int r = g; r < rows; r += 8) s += from[(int64_t)r * D + col];
+  red[g][c] = s;
+  __syncthreads();
+  if (g == 0 && to && col < D) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][c];
+    to[col] = s;
+  }
+}
+
+int64_t bwd_blocks(int64_t T, int64_t D, bool vec) {
+  const int64_t per = D <= (vec ? 2048 : 512) ? 4 : 1;  // rows a workgroup takes at a time
+  const int64_t n = cdiv(T, per);
+  return n < kNormBwdBlocks ? n : kNormBwdBlocks;
+}
+
+// Kernels by the row's length: a wave a row, then 256 threads, then 1024.
+template <class F>
+void by_length(int D, bool vec, F&& f) {
+#define NVN(NT, NC, W) return f(std::integral_constant<int, NT>{}, std::integral_constant<int, NC>{}, std::integral_constant<int, W>{})
+  if (vec) {
+    if (D <= 512) NVN(64, 1, 8);
+    if (D <= 1024) NVN(64, 2, 8);
+    if (D <= 2048) NVN(64, 4, 8);
+    if (D <= 4096) NVN(256, 2, 8);
+    if (D <= 8192) NVN(256, 4, 8);
+    NVN(256, 8, 8);
+  }
+  if (D <= 128) NVN(64, 2, 1);
+  if (D <= 512) NVN(64, 8, 1);
+  if (D <= 2048) NVN(256, 8, 1);
+  if (D <= 4096) NVN(256, 16, 1);
+  NVN(1024, 16, 1);
+#undef NVN
+}
+
+bool is_float(int dt) { return dt == NVFP4MOE_F32 || dt == NVFP4MOE_BF16; }
+
+}  // namespace
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, const void* w, const void* b, int w_dtype,
+                          float eps, int kind, void* y, int y_dtype, float* mean, float* rstd,
+                          nvfp4moe_stream_t stream) {
+  if (T < 0 || D < 0 || !is_float(x_dtype) || !is_float(y_dtype) || ((w || b) && !is_float(w_dtype)))
+    return NVFP4MOE_EINVAL;
+  if (kind != NVFP4MOE_NORM_LAYER && kind != NVFP4MOE_NORM_RMS) return NVFP4MOE_EINVAL;
+  if (!(eps >= 0.0f) || (kind == NVFP4MOE_NORM_RMS && mean)) return NVFP4MOE_EINVAL;
+  if (T > 0 && (!x || !y)) return NVFP4MOE_EINVAL;
+  if (D < 1 || D > kNormMaxD) return NVFP4MOE_ESHAPE;
+  const int xb = dtype_bytes(x_dtype), yb = dtype_bytes(y_dtype), wb = w || b ? dtype_bytes(w_dtype) : 1;
+  if (!aligned(x, xb) || !aligned(y, yb) || !aligned(w, wb) || !aligned(b, wb) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  if (T == 0) return NVFP4MOE_OK;
+  NormParams p{};
+  p.x = x;
+  p.w = w;
+  p.b = b;
+  p.out = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.T = T;
+  p.D = (int)D;
+  p.eps = eps;
+  p.x_bf16 = x_dtype == NVFP4MOE_BF16;
+  p.w_bf16 = w_dtype == NVFP4MOE_BF16;
+  p.out_bf16 = y_dtype == NVFP4MOE_BF16;
+  p.rms = kind == NVFP4MOE_NORM_RMS;
+  hipStream_t st = as_stream(stream);
+  const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(w, 16) && aligned(b, 16);
+  by_length(p.D, vec, [&](auto nt, auto nc, auto w_) {
+    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, W = decltype(w_)::value;
+    const int64_t n = cdiv(T, threads<NT>() / NT);
+    norm_fwd_kernel<NT, NC, W><<<(unsigned)(n < kStreamBlocks ? n : kStreamBlocks), threads<NT>(), 0, st>>>(p);
+  });
+  return launch_status();
+}
+
+extern "C" size_t layer_norm_bwd_workspace_size(int64_t T, int64_t D) {
+  if (T < 1 || D < 1 || D > kNormMaxD) return 0;
+  const int64_t n = T < kNormBwdBlocks ? T : kNormBwdBlocks;
+  return (size_t)(2 * n * D * 4);
+}
+
+extern "C" int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t T, int64_t D,
+                              const void* w, int w_dtype, const float* mean, const float* rstd, int kind, void* dx,
+                              int dx_dtype, float* dw, float* db, void* workspace, size_t ws_bytes,
+                              nvfp4moe_stream_t stream) {
+  if (T < 0 || D < 0 || !is_float(dy_dtype) || !is_float(x_dtype) || (w && !is_float(w_dtype)) ||
+      (dx && !is_float(dx_dtype)))
+    return NVFP4MOE_EINVAL;
+  if (kind != NVFP4MOE_NORM_LAYER && kind != NVFP4MOE_NORM_RMS) return NVFP4MOE_EINVAL;
+  if (T > 0 && (!dy || !x || !rstd || (kind == NVFP4MOE_NORM_LAYER && !mean) || (!dx && !dw && !db)))
+    return NVFP4MOE_EINVAL;
+  if (D < 1 || D > kNormMaxD) return NVFP4MOE_ESHAPE;
+  const int xb = dtype_bytes(x_dtype), yb = dtype_bytes(dy_dtype), wb = w ? dtype_bytes(w_dtype) : 1,
+            ob = dx ? dtype_bytes(dx_dtype) : 1;
+  if (!aligned(x, xb) || !aligned(dy, yb) || !aligned(w, wb) || !aligned(dx, ob) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(dw, 4) || !aligned(db, 4))
+    return NVFP4MOE_ESHAPE;
+  if (T > 0 && (dw || db)) {
+    if (!workspace || ws_bytes < layer_norm_bwd_workspace_size(T, D)) return NVFP4MOE_EWORKSPACE;
+    if (!aligned(workspace, 16)) return NVFP4MOE_ESHAPE;
+  }
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  hipStream_t st = as_stream(stream);
+  if (T == 0) {
+    const unsigned blocks = (unsigned)cdiv(D, 256);
+    if (dw) fill_u32_kernel<<<blocks, 256, 0, st>>>(reinterpret_cast<uint32_t*>(dw), 0u, D);
+    if (db) fill_u32_kernel<<<blocks, 256, 0, st>>>(reinterpret_cast<uint32_t*>(db), 0u, D);
+    return launch_status();
+  }
+  NormParams p{};
+  p.x = x;
+  p.dy = dy;
+  p.w = w;
+  p.mean_in = mean;
+  p.rstd_in = rstd;
+  p.out = dx;
+  p.part = reinterpret_cast<float*>(workspace);
+  p.T = T;
+  p.D = (int)D;
+  p.x_bf16 = x_dtype == NVFP4MOE_BF16;
+  p.dy_bf16 = dy_dtype == NVFP4MOE_BF16;
+  p.w_bf16 = w_dtype == NVFP4MOE_BF16;
+  p.out_bf16 = dx_dtype == NVFP4MOE_BF16;
+  p.rms = kind == NVFP4MOE_NORM_RMS;
+  p.want_dw = dw != nullptr;
+  p.want_db = db != nullptr;
+  const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(w, 16) && aligned(dx, 16);
+  const int64_t blocks = bwd_blocks(T, D, vec);
+  by_length(p.D, vec, [&](auto nt, auto nc, auto w_) {
+    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, W = decltype(w_)::value;
+    norm_bwd_kernel<NT, NC, W><<<(unsigned)blocks, threads<NT>(), 0, st>>>(p);
+  });
+  const int rc = launch_status();
+  if (rc != NVFP4MOE_OK || (!dw && !db)) return rc;
+  norm_sum_kernel<<<dim3((unsigned)cdiv(D, 32), db ? 2 : 1), 256, 0, st>>>(p.part, (int)blocks, p.D, dw, db);
+  return launch_status();
+}

@@ -1105,17 +1105,20 @@ int permute_nvfp4_impl(const int32_t* topk_ids, int64_t T, int k, int E, const v
 }  // namespace
 
 namespace {
-// Shared by both MX permutations: routing metadata, then the quantize-scatter.
-int permute_mx_impl(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D, int elem,
-                    uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
-                    size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
+// Shared by the MX and the 8-bit integer permutations: routing metadata, then
+// the quantize-scatter.  elem: NVFP4MOE_MX_E4M3, NVFP4MOE_MX_E2M1 or kElemInt8.
+constexpr int kElemInt8 = -1;
+int permute_codes_impl(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype, int64_t D, int elem,
+                       uint8_t* q, void* scales, int32_t* offsets, int32_t* dest, int32_t* src, void* workspace,
+                       size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
   if (T < 0 || k < 1 || E < 1 || D < 0) return NVFP4MOE_EINVAL;
   if (x_dtype != NVFP4MOE_BF16 && x_dtype != NVFP4MOE_F32) return NVFP4MOE_EINVAL;
   if (E > kMaxExperts || k > 64) return NVFP4MOE_ESHAPE;
   if (!offsets || (T > 0 && (!topk_ids || !dest || !src))) return NVFP4MOE_EINVAL;
   if (T > 0 && D > 0 && (!x || !q || !scales)) return NVFP4MOE_EINVAL;
-  if (D % 32 != 0) return NVFP4MOE_ESHAPE;
-  if (T > 0 && D > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E4M3 ? 16 : 8))) return NVFP4MOE_ESHAPE;
+  if (D % (elem == kElemInt8 ? 16 : 32) != 0) return NVFP4MOE_ESHAPE;
+  if (T > 0 && D > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E2M1 ? 8 : 16))) return NVFP4MOE_ESHAPE;
+  if (elem == kElemInt8 && !aligned(scales, 4)) return NVFP4MOE_ESHAPE;
   const int64_t R = T * k;
   if (R > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
   if (ws_bytes < moe_permute_workspace_size(T, k, E) || (R > 0 && !workspace)) return NVFP4MOE_EWORKSPACE;
@@ -1129,22 +1132,33 @@ int permute_mx_impl(const int32_t* topk_ids, int64_t T, int k, int E, const void
   const int rc = launch_metadata(topk_ids, R, E, nullptr, workspace, offsets, dest, src, status, st);
   if (rc != NVFP4MOE_OK) return rc;
   if (D == 0) return NVFP4MOE_OK;
-  return mx_quantize_scatter_launch(x, x_dtype, T, k, D, elem, dest, offsets, E, q, scales, st);
+  if (elem == kElemInt8)
+    return int8_quantize_scatter_launch(x, x_dtype, T, k, D, dest, offsets, E, reinterpret_cast<int8_t*>(q),
+                                        reinterpret_cast<float*>(scales), st);
+  return mx_quantize_scatter_launch(x, x_dtype, T, k, D, elem, dest, offsets, E, q, reinterpret_cast<uint8_t*>(scales),
+                                    st);
 }
 }  // namespace
 
 extern "C" int moe_permute_mx(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
                               int64_t D, uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src,
                               void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
-  return permute_mx_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E4M3, q, scales, offsets, dest, src, workspace,
+  return permute_codes_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E4M3, q, scales, offsets, dest, src, workspace,
                          ws_bytes, status, stream);
 }
 
 extern "C" int moe_permute_mxfp4(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
                                  int64_t D, uint8_t* q, uint8_t* scales, int32_t* offsets, int32_t* dest, int32_t* src,
                                  void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
-  return permute_mx_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E2M1, q, scales, offsets, dest, src, workspace,
+  return permute_codes_impl(topk_ids, T, k, E, x, x_dtype, D, NVFP4MOE_MX_E2M1, q, scales, offsets, dest, src, workspace,
                          ws_bytes, status, stream);
+}
+
+extern "C" int moe_permute_int8(const int32_t* topk_ids, int64_t T, int k, int E, const void* x, int x_dtype,
+                                int64_t D, int8_t* q, float* scales, int32_t* offsets, int32_t* dest, int32_t* src,
+                                void* workspace, size_t ws_bytes, int32_t* status, nvfp4moe_stream_t stream) {
+  return permute_codes_impl(topk_ids, T, k, E, x, x_dtype, D, kElemInt8, reinterpret_cast<uint8_t*>(q), scales, offsets,
+                            dest, src, workspace, ws_bytes, status, stream);
 }
 
 extern "C" int moe_unpermute_bwd(const void* dout, int dout_dtype, const void* y_perm, int y_dtype,

@@ -2,7 +2,7 @@
 // of its output folded in so the requantization reuses it ("miniTE報告、
 // NVFP4強化学習の安定性を検証", fourth paragraph: op fusion, amax reuse).
 // H = silu(G) * U with Y1 = [G | U] per row; fp32 math, bf16 storage.
-#include "common.hpp"
+#include "mx_codec.hpp"
 
 namespace nvfp4moe {
 namespace {
@@ -91,6 +91,53 @@ __global__ __launch_bounds__(256) void silu_bwd_kernel(const uint16_t* __restric
   if (amax_out) block_atomic_max<256>(amax_out, bf16_lo(pack_bf16x2(m, m)));
 }
 
+// dY1 and H from Y1 kept as MXINT8 (codes [R][2F], scales [R][2F / 32]): the
+// gate's backward of a forward pass that stored neither Y1 nor H in bf16.  H is
+// taken from the same values, for the weight gradient of the product it went
+// into.  HBM bound: 2 F (33/32) + 2 F bytes a row in, 4 F + 2 F out.  A thread
+// takes 16 features: whole 16-byte accesses of every tensor.
+__global__ __launch_bounds__(256) void silu_bwd_mx_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
+                                                          const uint4* __restrict__ dh, int64_t R, int64_t F,
+                                                          uint4* __restrict__ dy1, uint4* __restrict__ h) {
+  const int64_t n16 = F / 16, total = R * n16;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / n16, c = i - r * n16;  // row, 16-feature piece
+    const int64_t at = r * 2 * n16 + c;
+    const uint4 gq = reinterpret_cast<const uint4*>(q)[at], uq = reinterpret_cast<const uint4*>(q)[at + n16];
+    const uint4 d0 = dh[2 * i], d1 = dh[2 * i + 1];
+    const int gs = s[at >> 1], us = s[(at + n16) >> 1];  // (n16 is even)
+    const uint32_t g[4] = {gq.x, gq.y, gq.z, gq.w}, u[4] = {uq.x, uq.y, uq.z, uq.w};
+    const uint32_t d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+    uint32_t og[8], ou[8], oh[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float rg[2], ru[2], rh[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int e = 2 * j + k;
+        const float gv = decode_int8((int8_t)(g[e / 4] >> (8 * (e % 4))), gs);
+        const float uv = decode_int8((int8_t)(u[e / 4] >> (8 * (e % 4))), us);
+        const float dv = k ? bf16_hi(d[j]) : bf16_lo(d[j]);
+        const float sg = sigmoid_f32(gv);
+        rg[k] = dv * uv * (sg * (1.0f + gv * (1.0f - sg)));
+        ru[k] = dv * gv * sg;
+        rh[k] = gv * sg * uv;
+      }
+      og[j] = pack_bf16x2(rg[0], rg[1]);
+      ou[j] = pack_bf16x2(ru[0], ru[1]);
+      oh[j] = pack_bf16x2(rh[0], rh[1]);
+    }
+    dy1[2 * at] = make_uint4(og[0], og[1], og[2], og[3]);
+    dy1[2 * at + 1] = make_uint4(og[4], og[5], og[6], og[7]);
+    dy1[2 * (at + n16)] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    dy1[2 * (at + n16) + 1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
+    if (h) {
+      h[2 * i] = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+      h[2 * i + 1] = make_uint4(oh[4], oh[5], oh[6], oh[7]);
+    }
+  }
+}
+
 // With an amax the grid is capped (one same-address atomic per workgroup).
 inline unsigned grid_for(int64_t work) {
   const int64_t g = cdiv(work, 256);
@@ -141,5 +188,22 @@ extern "C" int silu_gate_bwd(const void* y1, const void* dh, int64_t R, int64_t 
     if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
     silu_bwd_kernel<1><<<(unsigned)grid, 256, 0, st>>>(y1b, dhb, R, F, dy1b, nullptr);
   }
+  return launch_status();
+}
+
+extern "C" int silu_gate_bwd_mx(const uint8_t* q_y1, const uint8_t* s_y1, const void* dh, int64_t R, int64_t F,
+                                void* dy1, void* h, nvfp4moe_stream_t stream) {
+  if (R < 0 || F < 0) return NVFP4MOE_EINVAL;
+  if (R > 0 && F > 0 && (!q_y1 || !s_y1 || !dh || !dy1)) return NVFP4MOE_EINVAL;
+  if (F % 32 != 0 || !aligned(q_y1, 16) || !aligned(dh, 16) || !aligned(dy1, 16) || !aligned(h, 16))
+    return NVFP4MOE_ESHAPE;
+  const int arch = check_arch();
+  if (arch != NVFP4MOE_OK) return arch;
+  if (R == 0 || F == 0) return NVFP4MOE_OK;
+  int64_t grid = cdiv(R * (F / 16), 256);
+  if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
+  silu_bwd_mx_kernel<<<(unsigned)grid, 256, 0, as_stream(stream)>>>(q_y1, s_y1, reinterpret_cast<const uint4*>(dh), R, F,
+                                                                    reinterpret_cast<uint4*>(dy1),
+                                                                    reinterpret_cast<uint4*>(h));
   return launch_status();
 }

@@ -131,7 +131,11 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None, d_top
 
     With ``d_topk_w`` (fp32 [T, k]) the gradient of the routing weights is
     written there, in the pass that scatters dY (moe_unpermute_bwd; buf.y2
-    must still hold the forward's)."""
+    must still hold the forward's).
+
+    With buffers that keep Y1 in 8 bits (``checkpoint``), dY1 and H come from
+    there (silu_gate_bwd_mx writes buf.h again), and the down projection's
+    weight gradient follows that."""
     main = torch.cuda.current_stream()
     off = meta["offsets"]
 
@@ -155,11 +159,15 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None, d_top
         ops.moe_unpermute_bwd(dy, buf.y2, meta["dest"], off, buf.k, topk_w=topk_w, dy_perm=buf.dy2, d_topk_w=d_topk_w)
     else:
         ops.moe_scatter(dy, meta["dest"], meta["offsets"], buf.k, topk_w=topk_w, out=buf.dy2)
-    if wgrad_stream is not None:
+    checkpoint = getattr(buf, "q_y1", None) is not None
+    if wgrad_stream is not None and not checkpoint:
         wgrad(buf.dy2, buf.h, buf.dw_dn)
     ops.grouped_gemm_bf16(ops.NN, buf.dy2, w_dn, off, out=buf.dh)
-    ops.silu_gate_bwd(buf.y1, buf.dh, dy1=buf.dy1)
-    if wgrad_stream is None:
+    if checkpoint:
+        ops.silu_gate_bwd_mx(buf.q_y1, buf.s_y1, buf.dh, dy1=buf.dy1, h=buf.h)
+    else:
+        ops.silu_gate_bwd(buf.y1, buf.dh, dy1=buf.dy1)
+    if wgrad_stream is None or checkpoint:
         wgrad(buf.dy2, buf.h, buf.dw_dn)
     ops.grouped_gemm_bf16(ops.NN, buf.dy1, w_gu, off, out=buf.dx_perm)
     ops.moe_unpermute(buf.dx_perm, meta["dest"], buf.T, buf.k, topk_w=None, out=buf.dx)
@@ -275,13 +283,30 @@ def backward_nvfp4(dy, topk_w, wt_gu, wt_dn, meta, buf, nb, amax_x=None, d_topk_
     ops.grouped_gemm_w4a4_wgrad(nb.c_dy1, nb.c_x, off, R, out=buf.dw_gu)
 
 
+def _backward_buffers(buf, e, dx_dtype, checkpoint):
+    """What ``backward`` reads and writes besides a forward's own buffers:
+    Y1 in bf16, or with ``checkpoint`` in 8 bits (a third of Y1's and H's
+    bytes; H is then made again by the backward pass)."""
+    T, E, D, F, R = buf.T, buf.E, buf.D, buf.F, buf.T * buf.k
+    f32, u8 = torch.float32, torch.uint8
+    buf.y1 = buf.q_y1 = buf.s_y1 = None
+    if checkpoint:
+        buf.q_y1, buf.s_y1 = e(R, 2 * F, dt=u8), e(R, 2 * F // 32, dt=u8)
+    else:
+        buf.y1 = e(R, 2 * F)
+    buf.dy2, buf.dh, buf.dy1, buf.dx_perm = e(R, D), e(R, F), e(R, 2 * F), e(R, D)
+    buf.dx = e(T, D, dt=dx_dtype)
+    buf.dw_dn, buf.dw_gu = e(E, D, F, dt=f32), e(E, 2 * F, D, dt=f32)
+
+
 class BuffersMXFP4:
     """Device buffers of one MXFP4 forward step, allocated once and reused;
-    with ``backward`` also those of ``backward`` (dx in ``dx_dtype``)."""
+    with ``backward`` also those of ``backward`` (dx in ``dx_dtype``), which
+    with ``checkpoint`` takes Y1 from 8 bits."""
 
-    def __init__(self, T, k, E, D, F, device, backward=False, dx_dtype=torch.bfloat16):
+    def __init__(self, T, k, E, D, F, device, backward=False, dx_dtype=torch.bfloat16, checkpoint=False):
         R = T * k
-        bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+        bf, u8 = torch.bfloat16, torch.uint8
         e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=device)  # noqa: E731
         self.T, self.k, self.E, self.D, self.F = T, k, E, D, F
         self.ws = e(max(ops.moe_permute_workspace_size(T, k, E), 1), dt=u8)
@@ -290,49 +315,131 @@ class BuffersMXFP4:
         self.y2 = e(R, D)
         self.out = e(T, D)
         if backward:
-            self.y1, self.h = e(R, 2 * F), e(R, F)
-            self.dy2, self.dh, self.dy1, self.dx_perm = e(R, D), e(R, F), e(R, 2 * F), e(R, D)
-            self.dx = e(T, D, dt=dx_dtype)
-            self.dw_dn, self.dw_gu = e(E, D, F, dt=f32), e(E, 2 * F, D, dt=f32)
+            self.h = e(R, F)
+            _backward_buffers(self, e, dx_dtype, checkpoint)
 
 
 def forward_mxfp4(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep=False):
     """MXFP4 MoE forward (weights from quantize_expert_weights_mx); returns
     the routing metadata dict.  X is quantized inside the permutation and H
     inside the gate+up epilogue.  ``keep``: bf16 Y1 and H are stored too
-    (buf.y1, buf.h), for ``backward``, which then gathers its activation rows
-    from x."""
+    (buf.y1, buf.h; with ``checkpoint`` buffers Y1 in 8 bits alone, buf.q_y1 and
+    buf.s_y1), for ``backward``, which then gathers its activation rows from x."""
+    y1, h, q_y1, s_y1 = _kept(buf, keep)
     ops._need(topk_w, "topk_w", torch.float32, buf.T, buf.k)
     with ops._on_device(x, topk_ids, topk_w, buf.out):
         meta = ops.moe_permute_mxfp4(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
         ops.grouped_gemm_mxfp4_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"],
-                                         y1=buf.y1 if keep else None, want_y1=keep, h=buf.h if keep else None,
-                                         want_h=keep, q_h=buf.a2_q, s_h=buf.a2_s)
+                                         y1=y1, want_y1=False, h=h, want_h=False, q_h=buf.a2_q, s_h=buf.a2_s,
+                                         q_y1=q_y1, s_y1=s_y1)
         ops.grouped_gemm_mxfp4(buf.a2_q, buf.a2_s, wq_dn["q"], wq_dn["s"], meta["offsets"], out=buf.y2)
         ops.moe_unpermute(buf.y2, meta["dest"], buf.T, buf.k, topk_w=topk_w, out=buf.out)
     return meta
 
 
+def _kept(buf, keep):
+    """What the gate+up product stores for ``backward``: (y1, h, q_y1, s_y1)."""
+    if not keep:
+        return None, None, None, None
+    if buf.q_y1 is not None:
+        return None, None, buf.q_y1, buf.s_y1
+    return buf.y1, buf.h, None, None
+
+
+def quantize_expert_weights_int8(w, out=None):
+    """8-bit integer weights of stacked experts [E, N, K] with one scale per
+    output channel, into ``out`` (an earlier result) when given.  Once per
+    optimizer step."""
+    E, N, K = w.shape
+    into = {} if out is None else dict(q=out["q"].view(E * N, K), scales=out["s"].view(E * N))
+    q, sc = ops.int8_quantize(w.reshape(E * N, K), **into)
+    return dict(q=q.view(E, N, K), s=sc.view(E, N))
+
+
+class BuffersInt8:
+    """Device buffers of one W8A8 forward step (8-bit integers), allocated
+    once and reused; with ``backward`` also those of ``backward`` (dx in
+    ``dx_dtype``), which with ``checkpoint`` takes Y1 from 8 bits."""
+
+    def __init__(self, T, k, E, D, F, device, backward=False, dx_dtype=torch.bfloat16, checkpoint=False):
+        R = T * k
+        bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
+        e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=device)  # noqa: E731
+        self.T, self.k, self.E, self.D, self.F = T, k, E, D, F
+        self.ws = e(max(ops.moe_permute_workspace_size(T, k, E), 1), dt=torch.uint8)
+        self.a1_q, self.a1_s = e(R, D, dt=i8), e(R, dt=f32)
+        self.h = e(R, F)
+        self.a2_q, self.a2_s = e(R, F, dt=i8), e(R, dt=f32)
+        self.y2 = e(R, D)
+        self.out = e(T, D)
+        if backward:
+            _backward_buffers(self, e, dx_dtype, checkpoint)
+
+
+def forward_int8(x, topk_ids, topk_w, wq_gu, wq_dn, buf, keep=False):
+    """W8A8 MoE forward in 8-bit integers with a scale per token and per output
+    channel (weights from quantize_expert_weights_int8); returns the routing
+    metadata dict.  X is quantized inside the permutation; H's scale needs its
+    whole row, so H passes through bf16 (buf.h).  ``keep``: as forward_mxfp4."""
+    ops._need(topk_w, "topk_w", torch.float32, buf.T, buf.k)
+    y1, _, q_y1, s_y1 = _kept(buf, keep)
+    with ops._on_device(x, topk_ids, topk_w, buf.out):
+        meta = ops.moe_permute_int8(topk_ids, buf.E, x, q=buf.a1_q, scales=buf.a1_s, workspace=buf.ws)
+        ops.grouped_gemm_int8_silu_gate(buf.a1_q, buf.a1_s, wq_gu["q"], wq_gu["s"], meta["offsets"], y1=y1,
+                                        want_y1=False, h=buf.h, q_y1=q_y1, s_y1=s_y1)
+        ops.int8_quantize(buf.h, q=buf.a2_q, scales=buf.a2_s)
+        ops.grouped_gemm_int8(buf.a2_q, buf.a2_s, wq_dn["q"], wq_dn["s"], meta["offsets"], out=buf.y2)
+        ops.moe_unpermute(buf.y2, meta["dest"], buf.T, buf.k, topk_w=topk_w, out=buf.out)
+    return meta
+
+
+# What Learner(experts=...) takes: buffers, forward and weight quantizer.
+_EXPERTS = dict(mxfp4=(BuffersMXFP4, forward_mxfp4, quantize_expert_weights_mx),
+                int8=(BuffersInt8, forward_int8, quantize_expert_weights_int8))
+
+
 class Learner:
-    """One MoE layer trained in MXFP4: fp32 master weights with bf16 and
-    MXFP4 copies, ``forward``, ``backward`` (to the input, the experts' and
-    the router's weights) and ``update`` (one AdamW step, copies renewed).
+    """One MoE layer trained in MXFP4, or in 8-bit integers: fp32 master
+    weights with bf16 and quantized copies, ``forward``, ``backward`` (to the
+    input, the experts' and the router's weights) and ``update`` (one AdamW
+    step, copies renewed).
 
     w_r [E, D], w_gu [E, 2F, D], w_dn [E, D, F]: fp32 master weights on the
     GPU, updated in place.  The gradient of the logits is rounded to bf16 for
     the BF16 products that take it to x and w_r, as all other gradients that
     enter a product are (half a step, 2^-8 relative).  T: tokens per step.  E, D % 32 == 0 (the router's
-    GEMM), D, F % 128 == 0.  ``adamw``: keyword arguments of optim.AdamW."""
+    GEMM), D, F % 128 == 0.  ``adamw``: keyword arguments of optim.AdamW.
 
-    def __init__(self, w_r, w_gu, w_dn, T, k, router_bias=None, score=ops.ROUTER_TOPK_SOFTMAX, **adamw):
+    experts: "mxfp4" or "int8", the precision of the experts' forward products.
+    checkpoint: Y1 is kept for the backward pass in 8 bits (MXINT8), and H is
+    made from it again.
+    norm: (w, b) of a norm in front of the router and the experts (fp32 [D] on
+    the GPU, updated in place; b may be None), of ``norm_kind`` and
+    ``norm_eps``.  It has an optimizer of its own, ``norm_opt``: the same
+    hyperparameters without weight decay, fp32 moments (``norm_state``: to
+    start from, as optim.AdamW's state)."""
+
+    norm = norm_opt = None
+
+    def __init__(self, w_r, w_gu, w_dn, T, k, router_bias=None, score=ops.ROUTER_TOPK_SOFTMAX, experts="mxfp4",
+                 checkpoint=False, norm=None, norm_kind=ops.NORM_RMS, norm_eps=1e-6, norm_state=None, **adamw):
+        if experts not in _EXPERTS:
+            raise ValueError("experts: %r, expected one of %s" % (experts, sorted(_EXPERTS)))
         E, D = w_r.shape
         F = w_dn.shape[2]
+        if norm is not None:
+            self.norm = [t for t in norm if t is not None]
+            for t in self.norm:
+                ops._need(t, "norm", torch.float32, D)
+            if norm[0] is None or len(norm) != 2:
+                raise ValueError("norm: its weight, and its bias or None")
         dev = w_r.device
         self.k, self.score, self.router_bias = k, score, router_bias
         self.master = [w_r, w_gu, w_dn]
         # (detached: a copy of a leaf would keep the leaf's node of the autograd graph)
         self.w_r, self.w_gu, self.w_dn = self.copies = [w.detach().to(torch.bfloat16) for w in self.master]
-        self.buf = BuffersMXFP4(T, k, E, D, F, dev, backward=True, dx_dtype=torch.float32)
+        buffers, self._forward, self._quantize = _EXPERTS[experts]
+        self.buf = buffers(T, k, E, D, F, dev, backward=True, dx_dtype=torch.float32, checkpoint=checkpoint)
         e = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         self.logits, self.d_logits = e(T, E), e(T, E, dt=torch.bfloat16)
         self.topk_ids, self.topk_w, self.d_topk_w = e(T, k, dt=torch.int32), e(T, k), e(T, k)
@@ -343,8 +450,16 @@ class Learner:
         self.x = self.meta = None        # of the last forward
         self.has_grads = False           # the gradients' buffers hold some
         self.opt = optim.AdamW(self.master, params_bf16=self.copies, **adamw)
+        if norm is not None:
+            self.norm_kind, self.norm_eps = norm_kind, norm_eps
+            self.norm_out, self.norm_rstd = e(T, D, dt=torch.bfloat16), e(T)
+            self.norm_mean = e(T) if norm_kind == ops.NORM_LAYER else None
+            self.norm_dx, self.norm_grads = e(T, D), [e(D) for _ in self.norm]
+            self.norm_ws = e(ops._lib.load().layer_norm_bwd_workspace_size(T, D), dt=torch.uint8)
+            own = {n: v for n, v in adamw.items() if n not in ("state", "state_bits", "weight_decay")}
+            self.norm_opt = optim.AdamW(self.norm, weight_decay=0.0, state=norm_state, **own)
         with ops._on_device(self.w_r):
-            self.wq_gu, self.wq_dn = quantize_expert_weights_mx(self.w_gu), quantize_expert_weights_mx(self.w_dn)
+            self.wq_gu, self.wq_dn = self._quantize(self.w_gu), self._quantize(self.w_dn)
 
     def forward(self, x):
         """The layer's output [T, D] (bf16, the layer's own buffer) for x [T, D]
@@ -352,11 +467,15 @@ class Learner:
         its losses.  x is kept, not copied: ``backward`` reads it again."""
         ops._need(x, "x", torch.bfloat16, self.logits.shape[0], self.w_r.shape[1])
         with ops._on_device(x, self.w_r):
+            if self.norm is not None:
+                self.norm_x = x
+                x = ops.layer_norm(x, *self.norm, eps=self.norm_eps, kind=self.norm_kind, y=self.norm_out,
+                                   mean=self.norm_mean, rstd=self.norm_rstd)["y"]
             self.x = x
             ops.grouped_gemm_bf16(ops.NT, x, self.w_r.unsqueeze(0), self.one_group, out=self.logits)
             ops.moe_router(self.logits, self.k, bias=self.router_bias, score=self.score, topk_ids=self.topk_ids,
                            topk_w=self.topk_w, lse=self.lse, prob_sum=self.prob_sum, workspace=self.router_ws)
-            self.meta = forward_mxfp4(x, self.topk_ids, self.topk_w, self.wq_gu, self.wq_dn, self.buf, keep=True)
+            self.meta = self._forward(x, self.topk_ids, self.topk_w, self.wq_gu, self.wq_dn, self.buf, keep=True)
         return self.buf.out
 
     def backward(self, dy, d_lse=None, d_prob_sum=None):
@@ -373,11 +492,18 @@ class Learner:
             ops.grouped_gemm_bf16(ops.TN, self.d_logits, self.x, self.one_group, out=self.dw_r)
             ops.grouped_gemm_bf16(ops.NN, self.d_logits, self.w_r.unsqueeze(0), self.one_group, out=b.dx,
                                   accumulate=True)
+            dx = b.dx
+            if self.norm is not None:
+                dx = ops.layer_norm_bwd(b.dx, self.norm_x, self.norm[0], self.norm_mean, self.norm_rstd,
+                                        kind=self.norm_kind, dx=self.norm_dx, dw=self.norm_grads[0],
+                                        db=self.norm_grads[1] if len(self.norm) > 1 else None,
+                                        workspace=self.norm_ws)["dx"]
         self.has_grads = True
-        return b.dx
+        return dx
 
     def grads(self):
-        return [self.dw_r[0], self.buf.dw_gu, self.buf.dw_dn]
+        """Gradients of w_r, w_gu, w_dn, then of the norm's w and b."""
+        return [self.dw_r[0], self.buf.dw_gu, self.buf.dw_dn] + (self.norm_grads if self.norm is not None else [])
 
     def update(self, grad_scale=None, skip=None):
         """One optimizer step with the last backward's gradients; the bf16 and
@@ -385,6 +511,9 @@ class Learner:
         if not self.has_grads:
             raise RuntimeError("Learner.update before a backward: there are no gradients")
         with ops._on_device(self.w_r):
-            self.opt.step(self.grads(), grad_scale=grad_scale, skip=skip)
-            quantize_expert_weights_mx(self.w_gu, out=self.wq_gu)
-            quantize_expert_weights_mx(self.w_dn, out=self.wq_dn)
+            grads = self.grads()
+            self.opt.step(grads[:3], grad_scale=grad_scale, skip=skip)
+            if self.norm is not None:
+                self.norm_opt.step(grads[3:], grad_scale=grad_scale, skip=skip)
+            self._quantize(self.w_gu, out=self.wq_gu)
+            self._quantize(self.w_dn, out=self.wq_dn)

@@ -89,6 +89,12 @@ def _on_device(first, *ts):
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
+def _dt_code(t, name="out"):
+    if t.dtype not in _FLOATS:
+        raise ValueError("%s: dtype %s is not supported" % (name, t.dtype))
+    return _DT[t.dtype]
+
+
 def nvfp4_quantize(x, groups=1, amax_in=None, amax_out=None, q=None, scales=None, gscale=None):
     """NVFP4-quantize a [rows, K] fp32/bf16 tensor.  Returns (q, scales,
     gscale, amax) where amax is amax_in when given, else the computed one."""
@@ -276,6 +282,33 @@ def moe_permute_mxfp4(topk_ids, num_experts, x, q=None, scales=None, status=None
                                    _ptr(scales), _ptr(offsets), _ptr(dest), _ptr(src), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(), _ptr(status), _stream())
     _check("moe_permute_mxfp4", rc)
+    return dict(offsets=offsets, dest=dest, src=src, q=q, scales=scales)
+
+
+def moe_permute_int8(topk_ids, num_experts, x, q=None, scales=None, status=None, workspace=None):
+    """moe_permute fused with the 8-bit integer quantization of the permuted
+    rows: codes [T*k, D] int8 and scales [T*k] fp32.  Returns a dict with
+    offsets, dest, src, q and scales."""
+    _need(topk_ids, "topk_ids", torch.int32, None, None)
+    T, k = topk_ids.shape
+    _need(x, "x", _FLOATS, T, None)
+    D, R = x.shape[1], T * k
+    _need(q, "q", torch.int8, R, D)
+    _need(scales, "scales", torch.float32, R)
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status: one int32 on the GPU")
+    with _on_device(topk_ids, x, q, scales, status, workspace):
+        new, i32 = x.new_empty, torch.int32
+        lib = _lib.load()
+        offsets, dest, src = new((num_experts + 1,), dtype=i32), new((R,), dtype=i32), new((R,), dtype=i32)
+        q = new((R, D), dtype=torch.int8) if q is None else q
+        scales = new((R,), dtype=torch.float32) if scales is None else scales
+        if workspace is None:
+            workspace = new((max(lib.moe_permute_workspace_size(T, k, num_experts), 1),), dtype=torch.uint8)
+        rc = lib.moe_permute_int8(_ptr(topk_ids), T, k, num_experts, _ptr(x), _DT[x.dtype], D, _ptr(q), _ptr(scales),
+                                  _ptr(offsets), _ptr(dest), _ptr(src), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream())
+    _check("moe_permute_int8", rc)
     return dict(offsets=offsets, dest=dest, src=src, q=q, scales=scales)
 
 
@@ -551,22 +584,37 @@ def grouped_gemm_w4a4_wgrad(a, b, offsets, M_total, out=None, out_dtype=torch.fl
     return out
 
 
-MX_E4M3, MX_E2M1 = _lib.MX_E4M3, _lib.MX_E2M1
+MX_E4M3, MX_E2M1, MX_INT8 = _lib.MX_E4M3, _lib.MX_E2M1, _lib.MX_INT8
 
 
 def mx_quantize(x, elem=MX_E4M3, q=None, scales=None):
     """MX-quantize a [rows, K] fp32/bf16 tensor (E8M0 scale per 32 along K):
-    elem MX_E4M3 (MXFP8, one byte per element) or MX_E2M1 (MXFP4, packed
-    pairs).  Returns (q, scales)."""
+    elem MX_E4M3 (MXFP8, one byte per element), MX_E2M1 (MXFP4, packed
+    pairs) or MX_INT8 (MXINT8, one two's complement byte per element: the
+    form of activations kept for the backward pass).  Returns (q, scales)."""
     _dev(x, q, scales)
     rows, K = x.shape
     dev = x.device
-    qcols = K if elem == MX_E4M3 else K // 2
+    qcols = K // 2 if elem == MX_E2M1 else K
     q = torch.empty((rows, qcols), dtype=torch.uint8, device=dev) if q is None else q
     scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=dev) if scales is None else scales
     rc = _lib.load().mx_quantize(_ptr(x), _DT[x.dtype], rows, K, elem, _ptr(q), _ptr(scales), _stream())
     _check("mx_quantize", rc)
     return q, scales
+
+
+def mx_dequantize(q, scales, elem=MX_E4M3, out=None, out_dtype=torch.bfloat16):
+    """The values [rows, K] of mx_quantize's codes (fp32 or bf16; a scale byte
+    of 255 gives NaN)."""
+    _need(q, "q", torch.uint8, None, None)
+    rows, K = q.shape[0], q.shape[1] * (2 if elem == MX_E2M1 else 1)
+    _need(scales, "scales", torch.uint8, rows, K // 32)
+    _need(out, "out", _FLOATS, rows, K)
+    with _on_device(q, scales, out):
+        out = q.new_empty((rows, K), dtype=out_dtype) if out is None else out
+        rc = _lib.load().mx_dequantize(_ptr(q), _ptr(scales), rows, K, elem, _ptr(out), _dt_code(out), _stream())
+    _check("mx_dequantize", rc)
+    return out
 
 
 def grouped_gemm_w4a8(a_q, a_s, b_q, b_s, offsets, out=None, out_dtype=torch.float32):
@@ -646,11 +694,14 @@ def grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets, out=None, out_dtype=torch.fl
 
 
 def grouped_gemm_mxfp4_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=True, h=None, want_h=True,
-                                 amax_out=None, q_h=None, s_h=None, want_q=False):
+                                 amax_out=None, q_h=None, s_h=None, want_q=False, q_y1=None, s_y1=None,
+                                 want_ckpt=False):
     """Gate+up MXFP4 GEMM (B_e = [gate; up] rows) with the SiLU gate and,
-    when wanted, the MXFP4 quantization of H in its epilogue.  Returns a dict
-    with y1 [M, 2F] and h [M, F] (bf16), q_h [M, F/2] and s_h [M, F/32] (None
-    unless wanted or given).  amax_out (fp32 [1], optional) receives max |H|."""
+    when wanted, the MXFP4 quantization of H and the MXINT8 form of Y1 (which
+    silu_gate_bwd_mx takes) in its epilogue.  Returns a dict with y1 [M, 2F]
+    and h [M, F] (bf16), q_h [M, F/2], s_h [M, F/32], q_y1 [M, 2F] and s_y1
+    [M, 2F/32] (None unless wanted or given).  amax_out (fp32 [1], optional)
+    receives max |H|."""
     M, K, E, N = _mxfp4_operands(a_q, a_s, b_q, b_s, offsets)
     if N % 2:
         raise ValueError("b_q: gate and up rows, an even number")
@@ -661,19 +712,98 @@ def grouped_gemm_mxfp4_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=T
     _need(amax_out, "amax_out", torch.float32, 1)
     _need(q_h, "q_h", u8, M, F // 2)
     _need(s_h, "s_h", u8, M, F // 32)
+    _need(q_y1, "q_y1", u8, M, N)
+    _need(s_y1, "s_y1", u8, M, N // 32)
     want_q = want_q or q_h is not None or s_h is not None
-    with _on_device(a_q, a_s, b_q, b_s, offsets, y1, h, amax_out, q_h, s_h):
+    want_ckpt = want_ckpt or q_y1 is not None or s_y1 is not None
+    with _on_device(a_q, a_s, b_q, b_s, offsets, y1, h, amax_out, q_h, s_h, q_y1, s_y1):
         new = a_q.new_empty
         y1 = new((M, N), dtype=bf) if y1 is None and want_y1 else y1
         h = new((M, F), dtype=bf) if h is None and want_h else h
         if want_q:
             q_h = new((M, F // 2), dtype=u8) if q_h is None else q_h
             s_h = new((M, F // 32), dtype=u8) if s_h is None else s_h
-        rc = _lib.load().grouped_gemm_mxfp4_silu_gate(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M,
-                                                      F, K, _ptr(y1), _ptr(h), _ptr(amax_out), _ptr(q_h), _ptr(s_h),
-                                                      _stream())
-    _check("grouped_gemm_mxfp4_silu_gate", rc)
-    return dict(y1=y1, h=h, q_h=q_h, s_h=s_h)
+        fn, args = "grouped_gemm_mxfp4_silu_gate", (_ptr(q_h), _ptr(s_h))
+        if want_ckpt:
+            q_y1 = new((M, N), dtype=u8) if q_y1 is None else q_y1
+            s_y1 = new((M, N // 32), dtype=u8) if s_y1 is None else s_y1
+            fn, args = fn + "_ckpt", args + (_ptr(q_y1), _ptr(s_y1))
+        rc = getattr(_lib.load(), fn)(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M, F, K, _ptr(y1),
+                                      _ptr(h), _ptr(amax_out), *args, _stream())
+    _check(fn, rc)
+    return dict(y1=y1, h=h, q_h=q_h, s_h=s_h, q_y1=q_y1, s_y1=s_y1)
+
+
+def int8_quantize(x, q=None, scales=None):
+    """8-bit integers of the rows of x [rows, K] (fp32 or bf16) with one fp32
+    scale per row (amax / 127): a token's, or a weight's output channel's.
+    Returns (q [rows, K] int8, scales [rows])."""
+    _need(x, "x", _FLOATS, None, None)
+    rows, K = x.shape
+    _need(q, "q", torch.int8, rows, K)
+    _need(scales, "scales", torch.float32, rows)
+    with _on_device(x, q, scales):
+        q = x.new_empty((rows, K), dtype=torch.int8) if q is None else q
+        scales = x.new_empty((rows,), dtype=torch.float32) if scales is None else scales
+        rc = _lib.load().int8_quantize(_ptr(x), _DT[x.dtype], rows, K, _ptr(q), _ptr(scales), _stream())
+    _check("int8_quantize", rc)
+    return q, scales
+
+
+def _int8_operands(a_q, a_s, b_q, b_s, offsets):
+    _need(a_q, "a_q", torch.int8, None, None)
+    M, K = a_q.shape
+    _need(a_s, "a_s", torch.float32, M)
+    _need(b_q, "b_q", torch.int8, None, None, K)
+    E, N = b_q.shape[0], b_q.shape[1]
+    _need(b_s, "b_s", torch.float32, E, N)
+    _need(offsets, "offsets", torch.int32, E + 1)
+    return M, K, E, N
+
+
+def grouped_gemm_int8(a_q, a_s, b_q, b_s, offsets, out=None, out_dtype=torch.float32):
+    """C[r] = (a_q[r] . b_q[e]^T) * a_s[r] * b_s[e] for rows r of expert e:
+    8-bit integers a_q [M, K], b_q [E, N, K] (exact sums), one fp32 scale per
+    token a_s [M] and per channel b_s [E, N]."""
+    M, K, E, N = _int8_operands(a_q, a_s, b_q, b_s, offsets)
+    _need(out, "out", _FLOATS, M, N)
+    with _on_device(a_q, a_s, b_q, b_s, offsets, out):
+        out = a_q.new_empty((M, N), dtype=out_dtype) if out is None else out
+        rc = _lib.load().grouped_gemm_int8(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M, N, K,
+                                           _ptr(out), _dt_code(out), _stream())
+    _check("grouped_gemm_int8", rc)
+    return out
+
+
+def grouped_gemm_int8_silu_gate(a_q, a_s, b_q, b_s, offsets, y1=None, want_y1=True, h=None, amax_out=None, q_y1=None,
+                                s_y1=None, want_ckpt=False):
+    """Gate+up GEMM of 8-bit integers (B_e = [gate; up] rows) with the SiLU
+    gate and, when wanted, the MXINT8 form of Y1 (which silu_gate_bwd_mx takes)
+    in its epilogue.  Returns a dict with y1 [M, 2F] and h [M, F] (bf16), q_y1
+    [M, 2F] and s_y1 [M, 2F/32] (y1 None unless wanted or given, q_y1 and s_y1
+    likewise).  amax_out (fp32 [1], optional) receives max |H|."""
+    M, K, E, N = _int8_operands(a_q, a_s, b_q, b_s, offsets)
+    if N % 2:
+        raise ValueError("b_q: gate and up rows, an even number")
+    F, bf, u8 = N // 2, torch.bfloat16, torch.uint8
+    _need(y1, "y1", bf, M, N)
+    _need(h, "h", bf, M, F)
+    _need(amax_out, "amax_out", torch.float32, 1)
+    _need(q_y1, "q_y1", u8, M, N)
+    _need(s_y1, "s_y1", u8, M, N // 32)
+    want_ckpt = want_ckpt or q_y1 is not None or s_y1 is not None
+    with _on_device(a_q, a_s, b_q, b_s, offsets, y1, h, amax_out, q_y1, s_y1):
+        new = a_q.new_empty
+        y1 = new((M, N), dtype=bf) if y1 is None and want_y1 else y1
+        h = new((M, F), dtype=bf) if h is None else h
+        if want_ckpt:
+            q_y1 = new((M, N), dtype=u8) if q_y1 is None else q_y1
+            s_y1 = new((M, N // 32), dtype=u8) if s_y1 is None else s_y1
+        rc = _lib.load().grouped_gemm_int8_silu_gate(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _ptr(offsets), E, M,
+                                                     F, K, _ptr(y1), _ptr(h), _ptr(amax_out), _ptr(q_y1), _ptr(s_y1),
+                                                     _stream())
+    _check("grouped_gemm_int8_silu_gate", rc)
+    return dict(y1=y1, h=h, q_y1=q_y1, s_y1=s_y1)
 
 
 def grouped_gemm_bf16(layout, a, b, offsets, num_experts=None, out=None, out_dtype=torch.float32, accumulate=False):
@@ -744,3 +874,98 @@ def silu_gate_bwd(y1, dh, dy1=None, amax_out=None):
     rc = _lib.load().silu_gate_bwd(_ptr(y1), _ptr(dh), R, F2 // 2, _ptr(dy1), _ptr(amax_out), _stream())
     _check("silu_gate_bwd", rc)
     return dy1
+
+
+def silu_gate_bwd_mx(q_y1, s_y1, dh, dy1=None, h=None, want_h=True):
+    """dY1 = [dG | dU] and H from Y1 kept in 8 bits (q_y1 [R, 2F], s_y1
+    [R, 2F/32]: the products' want_ckpt, or mx_quantize with MX_INT8) and dH
+    [R, F] bf16.  Returns (dy1, h or None); neither may overlap an input."""
+    _need(dh, "dh", torch.bfloat16, None, None)
+    R, F = dh.shape
+    _need(q_y1, "q_y1", torch.uint8, R, 2 * F)
+    _need(s_y1, "s_y1", torch.uint8, R, 2 * F // 32)
+    _need(dy1, "dy1", torch.bfloat16, R, 2 * F)
+    _need(h, "h", torch.bfloat16, R, F)
+    with _on_device(dh, q_y1, s_y1, dy1, h):
+        dy1 = dh.new_empty((R, 2 * F)) if dy1 is None else dy1
+        h = dh.new_empty((R, F)) if h is None and want_h else h
+        rc = _lib.load().silu_gate_bwd_mx(_ptr(q_y1), _ptr(s_y1), _ptr(dh), R, F, _ptr(dy1), _ptr(h), _stream())
+    _check("silu_gate_bwd_mx", rc)
+    return dy1, h
+
+
+NORM_LAYER, NORM_RMS = _lib.NORM_LAYER, _lib.NORM_RMS
+
+
+def _norm_weights(w, b, D):
+    """The weights' dtype code (that of both)."""
+    _need(w, "w", _FLOATS, D)
+    _need(b, "b", _FLOATS, D)
+    if w is not None and b is not None and w.dtype != b.dtype:
+        raise ValueError("w and b: one dtype, got %s and %s" % (w.dtype, b.dtype))
+    t = b if w is None else w
+    return F32 if t is None else _DT[t.dtype]
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, y=None, out_dtype=None, want_stats=True, mean=None,
+               rstd=None):
+    """Layer norm of the rows of x [T, D] (fp32 or bf16): (x - mean) * rstd * w
+    + b, or with kind NORM_RMS without the mean.  w, b [D]: fp32 or bf16, None
+    for ones and zeros.  Returns a dict with y [T, D] (of out_dtype, default
+    x's, which must not overlap x) and mean, rstd [T] fp32, which layer_norm_bwd
+    takes (None unless wanted or given; mean always with NORM_RMS)."""
+    _need(x, "x", _FLOATS, None, None)
+    T, D = x.shape
+    wdt = _norm_weights(w, b, D)
+    _need(y, "y", _FLOATS, T, D)
+    _need(mean, "mean", torch.float32, T)
+    _need(rstd, "rstd", torch.float32, T)
+    with _on_device(x, w, b, y, mean, rstd):
+        y = x.new_empty((T, D), dtype=out_dtype) if y is None else y
+        if want_stats:
+            if mean is None and kind == NORM_LAYER:
+                mean = x.new_empty((T,), dtype=torch.float32)
+            rstd = x.new_empty((T,), dtype=torch.float32) if rstd is None else rstd
+        rc = _lib.load().layer_norm(_ptr(x), _DT[x.dtype], T, D, _ptr(w), _ptr(b), wdt, eps, kind, _ptr(y), _dt_code(y),
+                                    _ptr(mean), _ptr(rstd), _stream())
+    _check("layer_norm", rc)
+    return dict(y=y, mean=mean, rstd=rstd)
+
+
+def layer_norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, dx=None, want_dx=True, dx_dtype=None, dw=None, want_dw=None,
+                   db=None, want_db=False, workspace=None):
+    """Gradient of layer_norm: dx [T, D] (of dx_dtype, default x's) and, summed
+    over the rows, dw and db [D] (fp32; dw is wanted when w is given, unless
+    want_dw says otherwise).  dy, x [T, D] fp32 or bf16; w as in layer_norm, or
+    None; mean (None with NORM_RMS) and rstd as layer_norm gave them.  Outputs
+    must not overlap inputs.  Returns a dict with dx, dw and db (None unless
+    wanted or given)."""
+    _need(x, "x", _FLOATS, None, None)
+    T, D = x.shape
+    _need(dy, "dy", _FLOATS, T, D)
+    wdt = _norm_weights(w, None, D)
+    _need(mean, "mean", torch.float32, T)
+    _need(rstd, "rstd", torch.float32, T)
+    if rstd is None or (mean is None and kind == NORM_LAYER):
+        raise ValueError("layer_norm_bwd needs the forward's rstd, and its mean unless kind is NORM_RMS")
+    f32 = torch.float32
+    _need(dx, "dx", _FLOATS, T, D)
+    _need(dw, "dw", f32, D)
+    _need(db, "db", f32, D)
+    with _on_device(x, dy, w, mean, rstd, dx, dw, db, workspace):
+        dx = x.new_empty((T, D), dtype=dx_dtype) if dx is None and want_dx else dx
+        odt = F32 if dx is None else _dt_code(dx, "dx")
+        if dw is None and (w is not None if want_dw is None else want_dw):
+            dw = x.new_empty((D,), dtype=f32)
+        db = x.new_empty((D,), dtype=f32) if db is None and want_db else db
+        lib = _lib.load()
+        ws_bytes = 0
+        if dw is not None or db is not None:
+            if workspace is None:
+                workspace = x.new_empty((lib.layer_norm_bwd_workspace_size(T, D),), dtype=torch.uint8)
+            ws_bytes = workspace.numel() * workspace.element_size()
+        rc = lib.layer_norm_bwd(_ptr(dy), _DT[dy.dtype], _ptr(x), _DT[x.dtype], T, D, _ptr(w), wdt, _ptr(mean),
+                                _ptr(rstd), kind, _ptr(dx), odt, _ptr(dw),
+                                _ptr(db), _ptr(workspace), ws_bytes, _stream())
+    _check("layer_norm_bwd", rc)
+    return dict(dx=dx, dw=dw, db=db)

@@ -30,7 +30,10 @@ docstring of the function that takes it.
 Modules:
   nvfp4   -- scalar codecs, quantize, dequantize           (fp32 as defined)
   moe     -- permutation metadata, gather, unpermute, SiLU gate (fp64)
-  mx      -- MX formats (MXFP8 / MXFP4, E8M0 per 32) of the W4A8 variant
+  mx      -- MX formats (MXFP8 / MXFP4, E8M0 per 32) of the W4A8 variant, MXINT8 of
+             activations kept
+  norm    -- layer norm and RMS norm with their gradients (fp64)
+  int8    -- 8-bit integers with a scale per row, their grouped products (fp32 as defined)
   gemm    -- grouped W4A4, W4A8 and BF16 GEMMs (fp64 on exact operands)
   router  -- top-k routing, its weights and gradient      (fp64)
   adamw   -- the AdamW step and its 8-bit moments         (fp64; fp32 as defined)
@@ -41,4 +44,4 @@ against hand-worked values (``tests/golden/``), brute force on tiny inputs,
 library routines and invariants -- never against itself.
 """
 
-from . import nvfp4, mx, moe, gemm, router, adamw, layer  # noqa: F401
+from . import nvfp4, mx, moe, norm, int8, gemm, router, adamw, layer  # noqa: F401

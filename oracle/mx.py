@@ -118,3 +118,34 @@ def dequantize(q, scales, elem):
     K = scales.shape[1] * MX_BLOCK
     v = decode_elements(q, elem, K)
     return v * np.repeat(e8m0_decode(scales), MX_BLOCK, axis=1)
+
+
+# MXINT8: the form of activations kept for the backward pass.  The scale byte S
+# of a block is the exponent field of its amax (2^(S-127) <= amax < 2^(S-126), 0
+# for a subnormal or zero); an element is the whole number nearest to
+# V * 2^(133-S), ties to even, clamped to [-127, 127], and stands for
+# code * 2^(S-133).  A block with an infinity or a NaN gets S = 255: NaN.
+
+def quantize_int8(x):
+    """(q int8 [rows, K], scales uint8 [rows, K/32]) of fp32 values."""
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    rows, K = x.shape
+    if K % MX_BLOCK:
+        raise ValueError("K must be a multiple of 32")
+    b = x.astype(np.float64).reshape(rows, K // MX_BLOCK, MX_BLOCK)
+    finite = np.isfinite(b).all(2)
+    a = np.abs(np.where(np.isfinite(b), b, 0.0)).max(2) if K else np.zeros((rows, 0))
+    _, e = np.frexp(a)
+    S = np.where(a > 0, np.maximum(e - 1 + E8M0_BIAS, 0), 0)
+    S = np.where(finite, S, 255)
+    with np.errstate(invalid="ignore"):
+        r = np.clip(np.rint(b * np.ldexp(1.0, 133 - S)[:, :, None]), -127, 127)
+    q = np.where(finite[:, :, None], r, 0)
+    return q.reshape(rows, K).astype(np.int8), S.astype(np.uint8)
+
+
+def dequantize_int8(q, scales):
+    """Exact fp64 values; NaN where the scale byte is 255."""
+    S = np.repeat(np.asarray(scales, np.int64), MX_BLOCK, axis=1)
+    v = np.asarray(q).view(np.int8).astype(np.float64) * np.ldexp(1.0, S - 133)
+    return np.where(S == 255, np.nan, v)
