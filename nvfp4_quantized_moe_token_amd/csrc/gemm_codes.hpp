@@ -18,8 +18,9 @@
 // time), tiles in contiguous ranges per XCD with the row blocks of an expert
 // next to each other.
 //
-// Epilogues.  The tile leaves through LDS in pieces of 64 bytes per row.  SiLU
-// gate: tiles hold matching gate and up columns; Y1 is rounded to bf16 and
+// Epilogues.  The tile leaves in pieces of 64 bytes per row, put together by
+// exchanges between the lanes of a wave (through LDS they took a fifth of the
+// kernel).  SiLU gate: tiles hold matching gate and up columns; Y1 is rounded to bf16 and
 // H = silu(G) * U is taken from the rounded values, as the standalone kernel
 // does; optionally H is quantized to MXFP4 on the way out, or the rounded Y1
 // to MXINT8, the form in which the backward pass takes it back.
@@ -53,10 +54,8 @@ struct Params {
   int E, n_tiles;
 };
 
-constexpr int kRowB = 128;          // code bytes per row and stage: one cache line
 constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
 constexpr int kTiles = 64;          // tiles looked up at a time
-constexpr int kWaveOut = 1024;      // bytes of a wave's epilogue staging: 16 rows of 64 bytes
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -86,10 +85,11 @@ __device__ __forceinline__ typename Operands<FMT>::Frag frag(uint32_t at) {
   else return v;
 }
 
-// 16-byte unit u of code row r lies at unit u ^ swz(r).  The swizzle repeats
-// every 32 rows, so a wave's fragments differ by constant offsets, and unit
-// 2c + h of chunk c is one XOR away from unit h.
-__device__ __forceinline__ int swz(int r) { return kswz(r & 31); }
+// 16-byte unit u of code row r (RB bytes) lies at unit u ^ swz(r).  The swizzle
+// repeats every 32 rows, so a wave's fragments differ by constant offsets, and
+// unit 2c + h of chunk c is one XOR away from unit h.
+template <int RB>
+__device__ __forceinline__ int swz(int r) { return rswz<RB>(r & 31); }
 
 // Accumulators stay in the accumulation registers until an element is used:
 // left to itself the compiler moves whole blocks to vector registers at the
@@ -123,30 +123,78 @@ __device__ __forceinline__ f32x4_t elements(const typename Operands<FMT>::Acc& a
   }
   return v;
 }
-__device__ __forceinline__ uint2 bf16x4(f32x4_t v) { return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])); }
+__device__ __forceinline__ void bf16x4(f32x4_t v, uint32_t* w) {
+  w[0] = pack_bf16x2(v[0], v[1]);
+  w[1] = pack_bf16x2(v[2], v[3]);
+}
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
-__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p) {
-  constexpr int NW = WM * WN;
+// Exchanges between lanes.  swap_halves: a's upper half of the wave against b's
+// lower one; swap_quarters: the same in each half, with quarters.
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap_quarters(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ uint32_t max_of_halves(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(r[0], r[1]);
+}
+// A block's bf16 words, columns 8 g + 4 (l / 32) + 0..3 of row l % 32 in words
+// 2 g, 2 g + 1: afterwards words 0..3 hold columns 8 (l / 32) + 0..7, words 4..7
+// those 16 further.
+__device__ __forceinline__ void pair_up(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; q += 4) {
+    swap_halves(w[q], w[q + 2]);
+    swap_halves(w[q + 1], w[q + 3]);
+  }
+}
+// Then words 0..3 hold 16 bytes of row l % 16, unit 2 ((l / 16) % 2) + l / 32 of
+// 64 bytes, and words 4..7 the same of the row 16 further.
+__device__ __forceinline__ void merge(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) swap_quarters(w[k], w[k + 4]);
+}
+// A 16-byte store at one register offset.  With part of the offset in a scalar
+// register the compiler takes the data registers as free at once and may write
+// them in the next instruction; the store was then seen to take the new value of
+// its third register (32 x 32 blocks of codes, in some lanes).
+__device__ __forceinline__ void store16(i32x4_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
+}
+__device__ __forceinline__ i32x4_t four(const uint32_t* w) { return (i32x4_t){(int)w[0], (int)w[1], (int)w[2], (int)w[3]}; }
+
+// RB: code bytes per row and stage, 128 (a cache line), or 64 for two
+// workgroups per CU.
+template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_kernel(Params p) {
+  constexpr int NW = WM * WN, CHUNKS = RB / 32, LROWS = 1024 / RB, UNITS = RB / 16;  // rows a load, units a row
+  static_assert(RB == 128 || (RB == 64 && FMT == INT8), "MX scales are read for two stages of 128 bytes");
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
   static_assert(FM >= 1 && FN >= 2 && WTM % 32 == 0 && WTN % 64 == 0, "wave tiling");
   constexpr bool SILU = EPI != EPI_PLAIN;
+  constexpr uint32_t GROUP = 8;
   // Scale rows of A (whole loads), and the scales' ring: of two stages' scales,
   // or of tiles'.  The loads run up to S tiles ahead of an epilogue.
   constexpr int SA = FMT == INT8 ? 256 : BM < 64 ? 64 : BM, SROW = FMT == INT8 ? 4 : 16;
-  constexpr int AT_B = BM * kRowB, STAGE = AT_B + BN * kRowB;  // codes of A, then B
+  constexpr int AT_B = BM * RB, STAGE = AT_B + BN * RB;  // codes of A, then B
   constexpr int SBUF = (SA + BN) * SROW, SRING = (FMT == INT8 ? S + 1 : S) * SBUF;
-  // 1 KiB loads of 8 code rows, and of 64 (MX) or 256 rows of scales, dealt to the waves in
+  // 1 KiB loads of LROWS code rows, and of 64 (MX) or 256 rows of scales, dealt to the waves in
   // turn; every wave issues NDMA per stage, whatever is left over landing in a
   // pad, so that its waits are constants.
-  constexpr int A_LOADS = BM / 8, B_LOADS = BN / 8, SC_LOADS = (SA + BN) * SROW / 1024;
+  constexpr int A_LOADS = BM / LROWS, B_LOADS = BN / LROWS, SC_LOADS = (SA + BN) * SROW / 1024;
   constexpr int A_INSTR = A_LOADS / NW, B_INSTR = B_LOADS / NW, SC_INSTR = (SC_LOADS + NW - 1) / NW;
   constexpr int NDMA = A_INSTR + B_INSTR + SC_INSTR, HALF = (NDMA + 1) / 2;
   static_assert(A_LOADS % NW == 0 && B_LOADS % NW == 0 && NW % 4 == 0, "the rows of a wave's loads agree modulo 32");
   constexpr int AHEAD = (S - 2) * NDMA;  // loads of this wave that are younger than the stage waited for
   static_assert(S >= 2 && AHEAD + 32 <= 63, "pipeline depth");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + SRING + NW * kWaveOut + 1024];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + SRING + 1024];
   __shared__ __attribute__((aligned(16))) int4 s_tile[2 * kTiles];  // this workgroup's tiles: expert, n-tile, first and end row
   __shared__ int32_t s_off[kOffsetsInLds + 1];                      // row offsets
   __shared__ int32_t s_blk[kOffsetsInLds + 1];                      // row blocks before each expert
@@ -155,7 +203,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
   const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wid / WN, wn = wid % WN;
   const uint32_t smem_lds = (uint32_t)(uintptr_t)(const lds_void_t*)smem, scales = smem_lds + S * STAGE,
-                 out = S * STAGE + SRING + wid * kWaveOut, pad = smem_lds + S * STAGE + SRING + NW * kWaveOut;
+                 pad = scales + SRING;
   const bool off_in_lds = p.E <= kOffsetsInLds;
   lds_i32_t* off_lds = (lds_i32_t*)s_off;
   if (off_in_lds)
@@ -195,8 +243,10 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 
   // Looks up this workgroup's tiles i0 .. i0 + 63, one per lane, into half
   // (i0 / 64) % 2 of s_tile.  Every wave does so for itself and writes the same
-  // values.  The tiles of an expert are numbered n-tile-major (its row blocks
-  // that share a weight panel are neighbours and run side by side on one XCD).
+  // values.  The tiles of an expert go by groups of GROUP row blocks, n-tile-major
+  // within a group: the 32 tiles that an XCD has in work at once are then at most
+  // 8 by 4, 12 panels of operands in its L2 where whole columns of row blocks
+  // would be 33.
   auto look_up = [&](int i0) {
     int4 t = make_int4(-1, 0, 0, 0);
     if (off_in_lds) {
@@ -212,9 +262,10 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
         expert_range(off_lds, e, p.M, lo, hi);
         const uint32_t in = L - (uint32_t)s_blk[e] * nt, cnt = (uint32_t)(s_blk[e + 1] - s_blk[e]);
         if (in < cnt * nt) {  // (always, with ascending offsets)
+          const uint32_t b0 = in / (GROUP * nt) * GROUP, r = in - b0 * nt, size = cnt - b0 < GROUP ? cnt - b0 : GROUP;
           t.x = e;
-          t.y = (int)(in / cnt);
-          t.z = lo + (int)(in % cnt) * BM;
+          t.y = (int)(r / size);
+          t.z = lo + (int)(b0 + r % size) * BM;
           t.w = hi - t.z < BM ? hi : t.z + BM;
         }
       }
@@ -242,14 +293,14 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
   };
 
   // Loads.  A lane's byte offsets of its first loads of a tile; load i adds
-  // 8 NW i rows (gate and up granules of 32 rows alternate, and 8 NW is a
-  // multiple of 32).  Scales are read 16 bytes a row, for two stages at once:
+  // LROWS NW i rows (gate and up granules of 32 rows alternate, and LROWS NW is
+  // a multiple of 32).  Scales are read 16 bytes a row, for two stages at once:
   // every row is a cache line of its own, and a load of 64 lines takes the
   // address unit 64 to 110 cycles however short they are (measured; a 1 KiB
   // load of whole lines takes 16).
   const int64_t F = p.N / 2;
   const uint32_t rowb = (uint32_t)(FMT == INT8 ? p.K : p.K / 2), srow = FMT == INT8 ? 4u : (uint32_t)(p.K / 32);
-  const int lrow = wid * 8 + lane / 8, lunit = (lane & 7) ^ swz(lrow);
+  const int lrow = wid * LROWS + lane / UNITS, lunit = (lane & (UNITS - 1)) ^ swz<RB>(lrow);
   const uint32_t la0 = (uint32_t)lrow * rowb + lunit * 16;
   const uint32_t lb0 = (uint32_t)(SILU ? gate_up_row(lrow, F, 0) : lrow) * rowb + lunit * 16;
   uint32_t ls0[SC_INSTR];
@@ -262,7 +313,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     const bool real = idx < SC_LOADS && (!is_a || row < BM);
     ls0[x] = real ? (uint32_t)(SILU && !is_a ? gate_up_row(row, F, 0) : row) * srow : kOOB;
   }
-  constexpr int KS = FMT == INT8 ? kRowB : 2 * kRowB;       // reduction elements per stage
+  constexpr int KS = FMT == INT8 ? RB : 2 * RB;       // reduction elements per stage
   const int nk = p.K > 0 ? (int)((p.K + KS - 1) / KS) : 1;  // (K == 0: one stage of zeros)
   // The last stage may be short (MXFP4: by half): units past the row are not
   // read (zeros), and the MX scales of its upper chunks, which would be the
@@ -292,15 +343,15 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
   };
   auto offsets = [&]() {
     const bool last = ld_kt + 1 == nk;
-    la = (la0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
-    lb = (lb0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
+    la = (la0 + (uint32_t)ld_kt * RB) | (last ? beyond : 0u);
+    lb = (lb0 + (uint32_t)ld_kt * RB) | (last ? beyond : 0u);
   };
   auto dma = [&](int x) __attribute__((always_inline)) {  // load x of NDMA of the cursor's stage
     if (x < A_INSTR) {
-      dma16(ra, ld_on ? smem_lds + ld_slot + (wid + NW * x) * 1024 : pad, la + (uint32_t)(8 * NW * x) * rowb);
+      dma16(ra, ld_on ? smem_lds + ld_slot + (wid + NW * x) * 1024 : pad, la + (uint32_t)(LROWS * NW * x) * rowb);
     } else if (x < A_INSTR + B_INSTR) {
       const int i = x - A_INSTR;
-      const uint32_t row = (uint32_t)(SILU ? gate_up_row(8 * NW * i, F, 0) : 8 * NW * i);
+      const uint32_t row = (uint32_t)(SILU ? gate_up_row(LROWS * NW * i, F, 0) : LROWS * NW * i);
       dma16(rb, ld_on ? smem_lds + ld_slot + AT_B + (wid + NW * i) * 1024 : pad, lb + row * rowb);
     } else {
       const int i = x - A_INSTR - B_INSTR;
@@ -327,8 +378,8 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 
   // This lane's fragment addresses in slot 0: row lane % 32 of the wave's
   // first row block, unit lane / 32; and its first scale words.
-  const uint32_t unit0 = (lane & 31) * kRowB + (((lane >> 5) ^ swz(lane & 31)) << 4);
-  const uint32_t fa0 = smem_lds + wm * WTM * kRowB + unit0, fb0 = smem_lds + AT_B + wn * WTN * kRowB + unit0;
+  const uint32_t unit0 = (lane & 31) * RB + (((lane >> 5) ^ swz<RB>(lane & 31)) << 4);
+  const uint32_t fa0 = smem_lds + wm * WTM * RB + unit0, fb0 = smem_lds + AT_B + wn * WTN * RB + unit0;
   const uint32_t sa0 = scales + (wm * WTM + (lane & 31)) * 16, sb0 = scales + (SA + wn * WTN + (lane & 31)) * 16;
   const int sh = 8 * (lane >> 5);
 
@@ -337,9 +388,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
   int sa[FM], sb[FN];      // of the chunks in work
   auto read = [&](uint32_t slot, int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag<FMT>(((fb0 + slot) ^ (32 * c)) + j * 32 * kRowB);
+    for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag<FMT>(((fb0 + slot) ^ (32 * c)) + j * 32 * RB);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag<FMT>(((fa0 + slot) ^ (32 * c)) + i * 32 * kRowB);
+    for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag<FMT>(((fa0 + slot) ^ (32 * c)) + i * 32 * RB);
   };
   auto read_scales = [&](uint32_t at) __attribute__((always_inline)) {
     if constexpr (FMT == INT8) return;
@@ -437,11 +488,13 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       chunk(0, HALF, NDMA, rest);
       if (rest) advance();
       rest = true;
-      read(slot, 2);
-      chunk(1, 0, 0, false);
-      take_scales(1, last && p.K % KS != 0 ? 0 : 24);
-      read(slot, 3);
-      chunk(2, 0, 0, false);
+      if constexpr (CHUNKS == 4) {
+        read(slot, 2);
+        chunk(1, 0, 0, false);
+        take_scales(1, last && p.K % KS != 0 ? 0 : 24);
+        read(slot, 3);
+        chunk(2, 0, 0, false);
+      }
       // The last chunk's fragments are in registers, so the slot is free once
       // every wave is here; the next stage has landed.  Stores of an epilogue
       // are younger than the loads of the S stages after it and need not have
@@ -466,7 +519,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       }
       read(slot, 0);
       read_scales(so);
-      chunk(3, 0, HALF, true);
+      chunk(CHUNKS - 1, 0, HALF, true);
     }
     // The rest of the cursor's stage goes before the epilogue's stores.
 #pragma unroll
@@ -478,31 +531,14 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 
     // Epilogue.  The B fragment is the MFMA's first operand, so lane l holds
     // output row l % 32 and, for g = 0..3, the four consecutive columns
-    // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Pieces of 16 rows and 64
-    // bytes pass through a staging area of the wave's own, so that a store
-    // writes 64 consecutive bytes of each row (which cost a CU what whole lines
-    // do, 20 cycles a KiB; 32-byte pieces cost 32); the next tile's stages land
-    // meanwhile.  LDS serves a wave in order: nothing is waited for between a
-    // piece's writes and reads but the data, and a block is stored while the
-    // next one passes.  Rows past the expert's end are past the store's region.
+    // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Halves and quarters of the
+    // wave exchange registers until a lane has 16 consecutive bytes of a row and
+    // four lanes 64 of them (a store of such pieces costs a CU what whole lines
+    // do, 20 cycles a KiB; 32-byte pieces cost 32).  Rows past the expert's end
+    // are past the store's region.
     settle();
-    const int rq = lane & 15, hh = lane >> 5, half = (lane >> 4) & 1;  // this lane's row in its half
-    uint8_t* reg = smem + out;
-    const int pr = lane >> 2, pu = lane & 3;  // row and 16-byte unit of a piece on its way out
-    uint8_t* put_at = reg + rq * 64 + 8 * hh;
-    const uint8_t* get_at = reg + pr * 64 + ((pu ^ (pr >> 2)) << 4);
-    auto put = [&](const uint2 (&w)[4], int part) __attribute__((always_inline)) {
-      if (half == part) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) *reinterpret_cast<uint2*>(put_at + ((g ^ (rq >> 2)) << 4)) = w[g];
-      }
-    };
-    auto get = [&]() __attribute__((always_inline)) {
-      asm volatile("" ::: "memory");  // other lanes' writes
-      const i32x4_t v = *reinterpret_cast<const i32x4_t*>(get_at);
-      asm volatile("" ::: "memory");
-      return v;
-    };
+    const int hh = lane >> 5;
+    const int pr = lane & 15, pu = ((lane >> 4) & 1) * 2 + hh;  // row of 16 and 16-byte unit of 4 after merge()
     const uint32_t tile_rows = (uint32_t)(cur.w - cur.z);
     // The integers' scales of this lane's row of row block i, and of its columns
     // 8 g + 4 hh + 0..3 of column block j.
@@ -519,98 +555,98 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       const uint32_t yb = (uint32_t)p.N * 2, hb = (uint32_t)F * 2, qb = (uint32_t)F / 2, eb = (uint32_t)F / 32;
       uint16_t *Yp = reinterpret_cast<uint16_t*>(p.c), *Hp = reinterpret_cast<uint16_t*>(p.h);
       const __amdgpu_buffer_rsrc_t ry = region(Yp + m0 * p.N, tile_rows * yb), rh = region(Hp + m0 * F, tile_rows * hb);
-      const __amdgpu_buffer_rsrc_t rq_ = region(p.hq + m0 * qb, tile_rows * qb), re = region(p.hs + m0 * eb, tile_rows * eb);
+      const __amdgpu_buffer_rsrc_t rq = region(p.hq + m0 * qb, tile_rows * qb), re = region(p.hs + m0 * eb, tile_rows * eb);
       const uint32_t kqb = (uint32_t)p.N, keb = (uint32_t)p.N / 32;  // row bytes of Y1's codes and scales
       const __amdgpu_buffer_rsrc_t rkq = region(p.yq + m0 * kqb, tile_rows * kqb), rke = region(p.ys + m0 * keb, tile_rows * keb);
-      const uint32_t vy = pr * yb + pu * 16, vh = pr * hb + pu * 16, vq = pr * qb + pu * 4, ve = pu == 0 ? pr * eb : kOOB;
-      const uint32_t vkq = pr * kqb + pu * 8, vke = pu == 0 ? pr * keb : kOOB;
+      const uint32_t vy = pr * yb + pu * 16, vh = pr * hb + pu * 16;
+      const uint32_t lr = lane & 31;  // codes and scales leave with a row per pair of lanes
+      const uint32_t vq = lr * qb + hh * 8, ve = hh == 0 ? lr * eb : kOOB;
+      const uint32_t vkq = lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
       const bool want_q = EPI == EPI_SILU_Q || (EPI == EPI_SILU_C && FMT == MXFP4 && p.hq);
-      const bool want_y = EPI == EPI_SILU_C || Yp;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float rs = row_scale(i);
 #pragma unroll
         for (int j = 0; j < FN; j += 2) {
           // Y1 is rounded to bf16 first: H is the gate of the stored values.
-          uint2 gv[4], uv[4];
-          i32x4_t o[2][3];
+          uint32_t gv[8], uv[8], hv[8];  // columns 8 g + 4 hh + 0..3 in words 2 g and 2 g + 1
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            gv[g] = bf16x4(elements<FMT>(acc[i][j], g, rs, col_scales(j, g)));
-            uv[g] = bf16x4(elements<FMT>(acc[i][j + 1], g, rs, col_scales(j + 1, g)));
+            bf16x4(elements<FMT>(acc[i][j], g, rs, col_scales(j, g)), gv + 2 * g);
+            bf16x4(elements<FMT>(acc[i][j + 1], g, rs, col_scales(j + 1, g)), uv + 2 * g);
           }
-          if (want_y) {
+          const uint32_t row = wm * WTM + i * 32, f = (uint32_t)n0 / 2 + wn * (WTN / 2) + j * 16;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              put(gv, part);
-              o[part][0] = get();
-              put(uv, part);
-              o[part][1] = get();
+          for (int w = 0; w < 8; ++w)
+            hv[w] = pack_bf16x2(silu_gate(bf16_lo(gv[w]), bf16_lo(uv[w])), silu_gate(bf16_hi(gv[w]), bf16_hi(uv[w])));
+          if constexpr (EPI == EPI_SILU_C) {
+            int sc[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {  // gate, up
+              const uint32_t(&y)[8] = t ? uv : gv;
+              uint32_t am = 0, d[4];
+#pragma unroll
+              for (int w = 0; w < 8; ++w) am = max(am, max((y[w] << 16) & 0x7FFFFFFFu, y[w] & 0x7FFF0000u));
+              sc[t] = int8_scale(max_of_halves(am));
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const float v[4] = {bf16_lo(y[2 * g]), bf16_hi(y[2 * g]), bf16_lo(y[2 * g + 1]), bf16_hi(y[2 * g + 1])};
+                d[g] = encode4_int8(v, sc[t]);
+              }
+              swap_halves(d[0], d[1]);  // 8 columns
+              swap_halves(d[2], d[3]);
+              swap_halves(d[0], d[2]);  // 16 columns
+              swap_halves(d[1], d[3]);
+              store16((i32x4_t){(int)d[0], (int)d[1], (int)d[2], (int)d[3]}, rkq, vkq + row * kqb + t * (uint32_t)F + f);
+            }
+            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(hh ? sc[1] : sc[0]), rke, vke, row * keb + f / 32, 0);
+          }
+          if (Yp) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              uint32_t(&y)[8] = t ? uv : gv;
+              pair_up(y);
+              merge(y);
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+                store16(four(y + 4 * part), ry, vy + (row + part * 16) * yb + (t * (uint32_t)F + f) * 2);
             }
           }
+          if (p.amax || want_q) {
+            // (rows past the end hold 0 or NaN, which the maximum passes over)
+            float am = 0.0f;
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            gv[g] = make_uint2(pack_bf16x2(silu_gate(bf16_lo(gv[g].x), bf16_lo(uv[g].x)),
-                                           silu_gate(bf16_hi(gv[g].x), bf16_hi(uv[g].x))),
-                               pack_bf16x2(silu_gate(bf16_lo(gv[g].y), bf16_lo(uv[g].y)),
-                                           silu_gate(bf16_hi(gv[g].y), bf16_hi(uv[g].y))));
+            for (int w = 0; w < 8; ++w) am = fmaxf(am, fmaxf(fabsf(bf16_lo(hv[w])), fabsf(bf16_hi(hv[w]))));
+            tile_amax = fmaxf(tile_amax, am);
+            pair_up(hv);
+            if (want_q) {
+              // the two halves hold the 32 features of one block of one row
+              const int se = shared_exp<2>(__uint_as_float(max_of_halves(__float_as_uint(am))));
+              uint32_t d[2];
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            put(gv, part);
-            o[part][2] = get();
-          }
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint32_t row = wm * WTM + i * 32 + part * 16, f = (uint32_t)n0 / 2 + wn * (WTN / 2) + j * 16;
-            if (Yp) {
-              __builtin_amdgcn_raw_buffer_store_b128(o[part][0], ry, vy, row * yb + f * 2, 0);
-              __builtin_amdgcn_raw_buffer_store_b128(o[part][1], ry, vy, row * yb + hb + f * 2, 0);
-            }
-            const i32x4_t h = o[part][2];
-            if (Hp) __builtin_amdgcn_raw_buffer_store_b128(h, rh, vh, row * hb + f * 2, 0);
-            if constexpr (EPI == EPI_SILU_C) {
-              // four lanes hold the 32 features of one block of one row
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {  // gate, up
-                const i32x4_t y = o[part][t];
-                float yf[8];
-                uint32_t am = 0;
+              for (int t = 0; t < 2; ++t) {
+                float v[8];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                  yf[2 * w] = bf16_lo((uint32_t)y[w]);
-                  yf[2 * w + 1] = bf16_hi((uint32_t)y[w]);
-                  const uint32_t lo = ((uint32_t)y[w] << 16) & 0x7FFFFFFFu, hi = (uint32_t)y[w] & 0x7FFF0000u;
-                  am = max(am, max(lo, hi));
+                  v[2 * w] = bf16_lo(hv[4 * t + w]);
+                  v[2 * w + 1] = bf16_hi(hv[4 * t + w]);
                 }
-                am = max(am, (uint32_t)__shfl_xor((int)am, 1, 64));
-                am = max(am, (uint32_t)__shfl_xor((int)am, 2, 64));
-                const int sb8 = int8_scale(am);
-                const u32x2_t w = {encode4_int8(yf, sb8), encode4_int8(yf + 4, sb8)};
-                __builtin_amdgcn_raw_buffer_store_b64(w, rkq, vkq, row * kqb + t * (uint32_t)F + f, 0);
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sb8, rke, vke, row * keb + (t * (uint32_t)F + f) / 32, 0);
+                d[t] = encode8_e2m1(v, se);
               }
+              swap_halves(d[0], d[1]);
+              __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){d[0], d[1]}, rq, vq, row * qb + f / 2, 0);
+              __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32, 0);
             }
-            if (want_q || p.amax) {
-              // (rows past the end hold 0 or NaN, which the maximum passes over)
-              float hf[8], am = 0.0f;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                hf[2 * w] = bf16_lo((uint32_t)h[w]);
-                hf[2 * w + 1] = bf16_hi((uint32_t)h[w]);
-                am = fmaxf(am, fmaxf(fabsf(hf[2 * w]), fabsf(hf[2 * w + 1])));
-              }
-              tile_amax = fmaxf(tile_amax, am);
-              if (want_q) {
-                // four lanes hold the 32 features of one block of one row
-                am = fmaxf(am, __shfl_xor(am, 1, 64));
-                am = fmaxf(am, __shfl_xor(am, 2, 64));
-                const int se = shared_exp<2>(am);
-                __builtin_amdgcn_raw_buffer_store_b32(encode8_e2m1(hf, se), rq_, vq, row * qb + f / 2, 0);
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32, 0);
-              }
-            }
+          } else {
+            pair_up(hv);
           }
-          nst += 2 * ((Yp ? 2 : 0) + (Hp ? 1 : 0) + (want_q ? 2 : 0) + (EPI == EPI_SILU_C ? 4 : 0));
+          if (Hp) {
+            merge(hv);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              store16(four(hv + 4 * part), rh, vh + (row + part * 16) * hb + f * 2);
+          }
+          nst += (Yp ? 4 : 0) + (Hp ? 2 : 0) + (want_q ? 2 : 0) + (EPI == EPI_SILU_C ? 3 : 0);
           __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
         }
       }
@@ -619,59 +655,40 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       const uint32_t cb = (uint32_t)p.N * EB;
       const __amdgpu_buffer_rsrc_t rc = region(reinterpret_cast<uint8_t*>(p.c) + m0 * cb, tile_rows * cb);
       const uint32_t vc = pr * cb + pu * 16;
-      i32x4_t v[2][OUT32 ? 2 : 1], before[2][OUT32 ? 2 : 1];
-      auto store = [&](int x, const i32x4_t (&w)[2][OUT32 ? 2 : 1]) __attribute__((always_inline)) {  // block x
-        const uint32_t row = wm * WTM + (x / FN) * 32, col = (uint32_t)n0 + wn * WTN + (x % FN) * 32;
-        if (col < (uint32_t)p.N) {  // (N % 32 == 0)
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (uint32_t q = 0; q < EB / 2; ++q)
-              __builtin_amdgcn_raw_buffer_store_b128(w[part][q], rc, vc, (row + part * 16) * cb + col * EB + q * 64, 0);
-          nst += EB;
-        }
-      };
 #pragma unroll
       for (int x = 0; x < FM * FN; ++x) {
         const typename Operands<FMT>::Acc& a = acc[x / FN][x % FN];
         const float rs = row_scale(x / FN);
+        const uint32_t row = wm * WTM + (x / FN) * 32, col = (uint32_t)n0 + wn * WTN + (x % FN) * 32;
+        if (col >= (uint32_t)p.N) continue;  // (N % 32 == 0)
         if constexpr (OUT32) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {  // 16 columns at a time
-            float4 w[2];
+            uint32_t w[8];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               const f32x4_t e = elements<FMT>(a, 2 * q + g, rs, col_scales(x % FN, 2 * q + g));
-              w[g] = make_float4(e[0], e[1], e[2], e[3]);
-            }
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              if (half == part) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                  *reinterpret_cast<float4*>(reg + rq * 64 + (((2 * g + hh) ^ (rq >> 2)) << 4)) = w[g];
-              }
-              v[part][q] = get();
+              for (int k = 0; k < 4; ++k) w[4 * g + k] = __float_as_uint(e[k]);
             }
+            merge(w);
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+              store16(four(w + 4 * part), rc, vc + (row + part * 16) * cb + col * EB + q * 64);
           }
         } else {
-          uint2 w[4];
+          uint32_t w[8];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) w[g] = bf16x4(elements<FMT>(a, g, rs, col_scales(x % FN, g)));
+          for (int g = 0; g < 4; ++g) bf16x4(elements<FMT>(a, g, rs, col_scales(x % FN, g)), w + 2 * g);
+          pair_up(w);
+          merge(w);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            put(w, part);
-            v[part][0] = get();
-          }
+          for (int part = 0; part < 2; ++part)
+            store16(four(w + 4 * part), rc, vc + (row + part * 16) * cb + col * EB);
         }
-        if (x > 0) store(x - 1, before);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (uint32_t q = 0; q < EB / 2; ++q) before[part][q] = v[part][q];
+        nst += EB;
         __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
       }
-      store(FM * FN - 1, before);
     }
     if constexpr (FMT == INT8) so = so + SBUF == SRING ? 0 : so + SBUF;
   }
@@ -694,12 +711,12 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 }
 
 // Resident workgroups per CU (the same on every gfx950 device).
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 int resident_per_cu() {
   static int cached = 0;
   if (cached > 0) return cached;
   int occ = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32>, WM * WN * 64,
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32>, WM * WN * 64,
                                                    0) != hipSuccess ||
       occ < 1)
     occ = 1;
@@ -707,16 +724,16 @@ int resident_per_cu() {
   return occ;
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 int launch_tiles(const Params& p0, hipStream_t st) {
   Params p = p0;
   p.n_tiles = (int)cdiv(p.N, BN);
   const int64_t upper = (cdiv(p.M, BM) + p.E) * p.n_tiles;  // tiles at most
   if (upper > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
-  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, BM, BN, WM, WN, S, EPI, OUT32>();
+  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32>();
   if (grid > upper) grid = upper;
   grid = cdiv(grid, 8) * 8;  // whole XCD rounds
-  codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
+  codes_kernel<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
   return launch_status();
 }
 

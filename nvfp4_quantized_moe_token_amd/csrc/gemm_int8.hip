@@ -16,10 +16,10 @@ namespace {
 // Tiles by the mean rows per expert, as for MXFP4.
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
-  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<INT8, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<INT8, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<INT8, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
-  return launch_tiles<INT8, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<INT8, 128, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<INT8, 128, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<INT8, 128, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  return launch_tiles<INT8, 128, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 
 // Argument checks shared by both entry points, then the launch parameters.
