@@ -686,8 +686,8 @@ int grouped_gemm_mxfp4_silu_gate(const uint8_t* a_q, const uint8_t* a_s, const u
 /*
  * grouped_gemm_mxfp4_silu_gate_ckpt -- grouped_gemm_mxfp4_silu_gate that also
  * keeps the bf16 Y1 in 8 bits, the form silu_gate_bwd_mx takes: q_y1 [M_total]
- * [2F] (8-byte aligned) and s_y1 [M_total][2F/32] equal, bit for bit,
- * mx_quantize(Y1, NVFP4MOE_MX_INT8).  Rows >= offsets[E] are not written.
+ * [2F] (16-byte aligned) and s_y1 [M_total][2F/32] (2-byte aligned) equal, bit
+ * for bit, mx_quantize(Y1, NVFP4MOE_MX_INT8).  Rows >= offsets[E] are not written.
  * EINVAL for q_y1 or s_y1 NULL with work to do.
  */
 int grouped_gemm_mxfp4_silu_gate_ckpt(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, const uint8_t* b_s,
@@ -735,8 +735,8 @@ int grouped_gemm_int8(const int8_t* a_q, const float* a_s, const int8_t* b_q, co
  * grouped_gemm_int8 (N = 2F, B_e = [gate; up] rows, bf16 C), silu_gate_fwd and
  * mx_quantize(Y1, NVFP4MOE_MX_INT8).
  *   y1 [M_total][2F] bf16 or NULL, h [M_total][F] bf16, amax_out fp32 [1] or
- *   NULL (max |H|); q_y1 [M_total][2F] (8-byte aligned) and s_y1
- *   [M_total][2F/32], both or neither.
+ *   NULL (max |H|); q_y1 [M_total][2F] (16-byte aligned) and s_y1
+ *   [M_total][2F/32] (2-byte aligned), both or neither.
  * F % 128 == 0, F <= 2^19, 2 F K < 2^31.  Other rules and errors as
  * grouped_gemm_int8.
  */

@@ -167,6 +167,17 @@ __device__ __forceinline__ void merge(uint32_t (&w)[8]) {
 __device__ __forceinline__ void store16(i32x4_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
   __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
 }
+// Two such quadruples, a of 64 bytes of rows and b of the next 64: afterwards a
+// holds 16 bytes of row l % 8, unit 4 ((l / 8) % 2) + 2 ((l / 16) % 2) + l / 32 of
+// 128 bytes, and b the same of the row 8 further.
+__device__ __forceinline__ void join(uint32_t* a, uint32_t* b) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int x = (int)a[k], y = (int)b[k];
+    a[k] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);  // lanes 8..15 of 16: b's 0..7
+    b[k] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);  // lanes 0..7: a's 8..15
+  }
+}
 __device__ __forceinline__ i32x4_t four(const uint32_t* w) { return (i32x4_t){(int)w[0], (int)w[1], (int)w[2], (int)w[3]}; }
 
 // RB: code bytes per row and stage, 128 (a cache line), or 64 for two
@@ -533,12 +544,14 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
     // output row l % 32 and, for g = 0..3, the four consecutive columns
     // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Halves and quarters of the
     // wave exchange registers until a lane has 16 consecutive bytes of a row and
-    // four lanes 64 of them (a store of such pieces costs a CU what whole lines
-    // do, 20 cycles a KiB; 32-byte pieces cost 32).  Rows past the expert's end
-    // are past the store's region.
+    // eight lanes a whole line, where two blocks of the wave lie side by side
+    // (the skewed product's 537 MB of stores cost 32 us less than as half
+    // lines), else four lanes half a line.  Rows past the expert's end are past
+    // the store's region.
     settle();
     const int hh = lane >> 5;
-    const int pr = lane & 15, pu = ((lane >> 4) & 1) * 2 + hh;  // row of 16 and 16-byte unit of 4 after merge()
+    const int r16 = lane & 15, u4 = ((lane >> 4) & 1) * 2 + hh;  // row and 16-byte unit after merge()
+    const int r8 = lane & 7, u8 = ((lane >> 3) & 1) * 4 + u4;    // and after join()
     const uint32_t tile_rows = (uint32_t)(cur.w - cur.z);
     // The integers' scales of this lane's row of row block i, and of its columns
     // 8 g + 4 hh + 0..3 of column block j.
@@ -558,136 +571,199 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
       const __amdgpu_buffer_rsrc_t rq = region(p.hq + m0 * qb, tile_rows * qb), re = region(p.hs + m0 * eb, tile_rows * eb);
       const uint32_t kqb = (uint32_t)p.N, keb = (uint32_t)p.N / 32;  // row bytes of Y1's codes and scales
       const __amdgpu_buffer_rsrc_t rkq = region(p.yq + m0 * kqb, tile_rows * kqb), rke = region(p.ys + m0 * keb, tile_rows * keb);
-      const uint32_t vy = pr * yb + pu * 16, vh = pr * hb + pu * 16;
-      const uint32_t lr = lane & 31;  // codes and scales leave with a row per pair of lanes
+      constexpr int P = FN >= 4 ? 2 : 1;  // pairs of a gate and an up block that leave together
+      const uint32_t lr = lane & 31;      // codes and scales of one pair leave with a row per two lanes
       const uint32_t vq = lr * qb + hh * 8, ve = hh == 0 ? lr * eb : kOOB;
-      const uint32_t vkq = lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
+      const uint32_t vkq = P == 2 ? r16 * kqb + u4 * 16 : lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
       const bool want_q = EPI == EPI_SILU_Q || (EPI == EPI_SILU_C && FMT == MXFP4 && p.hq);
+      // Stores P blocks of 32 columns (paired up) at `at` of the region's rows.
+      auto leave = [&](uint32_t (&w)[P][8], __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t rb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) merge(w[q]);
+        if constexpr (P == 2) {
+          at += r8 * rb + u8 * 16;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            join(w[0] + 4 * part, w[1] + 4 * part);
+            store16(four(w[0] + 4 * part), r, at + part * 16 * rb);
+            store16(four(w[1] + 4 * part), r, at + (part * 16 + 8) * rb);
+          }
+        } else {
+          at += r16 * rb + u4 * 16;
+          store16(four(w[0]), r, at);
+          store16(four(w[0] + 4), r, at + 16 * rb);
+        }
+      };
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float rs = row_scale(i);
 #pragma unroll
-        for (int j = 0; j < FN; j += 2) {
+        for (int j = 0; j < FN; j += 2 * P) {
           // Y1 is rounded to bf16 first: H is the gate of the stored values.
-          uint32_t gv[8], uv[8], hv[8];  // columns 8 g + 4 hh + 0..3 in words 2 g and 2 g + 1
+          uint32_t gv[P][8], uv[P][8], hv[P][8];  // columns 8 g + 4 hh + 0..3 in words 2 g and 2 g + 1
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            bf16x4(elements<FMT>(acc[i][j], g, rs, col_scales(j, g)), gv + 2 * g);
-            bf16x4(elements<FMT>(acc[i][j + 1], g, rs, col_scales(j + 1, g)), uv + 2 * g);
+          for (int q = 0; q < P; ++q) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              bf16x4(elements<FMT>(acc[i][j + 2 * q], g, rs, col_scales(j + 2 * q, g)), gv[q] + 2 * g);
+              bf16x4(elements<FMT>(acc[i][j + 2 * q + 1], g, rs, col_scales(j + 2 * q + 1, g)), uv[q] + 2 * g);
+            }
           }
           const uint32_t row = wm * WTM + i * 32, f = (uint32_t)n0 / 2 + wn * (WTN / 2) + j * 16;
+          // The words are unpacked anew by each step that reads them (their halves
+          // kept as floats from one to the next would spill).
+          auto anew = [&](uint32_t (&y)[P][8]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int w = 0; w < 8; ++w)
-            hv[w] = pack_bf16x2(silu_gate(bf16_lo(gv[w]), bf16_lo(uv[w])), silu_gate(bf16_hi(gv[w]), bf16_hi(uv[w])));
+            for (int q = 0; q < P; ++q)
+#pragma unroll
+              for (int w = 0; w < 8; ++w) asm volatile("" : "+v"(y[q][w]));
+          };
           if constexpr (EPI == EPI_SILU_C) {
-            int sc[2];
+            uint32_t sc[2] = {0, 0};  // scale bytes of the P blocks, gate and up
 #pragma unroll
             for (int t = 0; t < 2; ++t) {  // gate, up
-              const uint32_t(&y)[8] = t ? uv : gv;
-              uint32_t am = 0, d[4];
+              uint32_t d[P][4];
 #pragma unroll
-              for (int w = 0; w < 8; ++w) am = max(am, max((y[w] << 16) & 0x7FFFFFFFu, y[w] & 0x7FFF0000u));
-              sc[t] = int8_scale(max_of_halves(am));
+              for (int q = 0; q < P; ++q) {
+                const uint32_t(&y)[8] = t ? uv[q] : gv[q];
+                uint32_t am = 0;
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float v[4] = {bf16_lo(y[2 * g]), bf16_hi(y[2 * g]), bf16_lo(y[2 * g + 1]), bf16_hi(y[2 * g + 1])};
-                d[g] = encode4_int8(v, sc[t]);
+                for (int w = 0; w < 8; ++w) am = max(am, max((y[w] << 16) & 0x7FFFFFFFu, y[w] & 0x7FFF0000u));
+                const int sb8 = int8_scale(max_of_halves(am));
+                anew(t ? uv : gv);
+                sc[t] |= (uint32_t)sb8 << (8 * q);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const float v[4] = {bf16_lo(y[2 * g]), bf16_hi(y[2 * g]), bf16_lo(y[2 * g + 1]), bf16_hi(y[2 * g + 1])};
+                  d[q][g] = encode4_int8(v, sb8);
+                }
+                swap_halves(d[q][0], d[q][1]);  // 8 columns
+                swap_halves(d[q][2], d[q][3]);
+                swap_halves(d[q][0], d[q][2]);  // 16 columns
+                swap_halves(d[q][1], d[q][3]);
               }
-              swap_halves(d[0], d[1]);  // 8 columns
-              swap_halves(d[2], d[3]);
-              swap_halves(d[0], d[2]);  // 16 columns
-              swap_halves(d[1], d[3]);
-              store16((i32x4_t){(int)d[0], (int)d[1], (int)d[2], (int)d[3]}, rkq, vkq + row * kqb + t * (uint32_t)F + f);
+              if constexpr (P == 2) {  // 64 columns of 16 rows
+#pragma unroll
+                for (int k = 0; k < 4; ++k) swap_quarters(d[0][k], d[1][k]);
+              }
+#pragma unroll
+              for (int q = 0; q < P; ++q) store16(four(d[q]), rkq, vkq + (row + 16 * q) * kqb + t * (uint32_t)F + f);
+              anew(t ? uv : gv);
+              __builtin_amdgcn_sched_barrier(0);  // registers
             }
-            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(hh ? sc[1] : sc[0]), rke, vke, row * keb + f / 32, 0);
+            const uint32_t s = hh ? sc[1] : sc[0];
+            if constexpr (P == 2) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)s, rke, vke, row * keb + f / 32, 0);
+            else __builtin_amdgcn_raw_buffer_store_b8((uint8_t)s, rke, vke, row * keb + f / 32, 0);
           }
+#pragma unroll
+          for (int q = 0; q < P; ++q)
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+              hv[q][w] = pack_bf16x2(silu_gate(bf16_lo(gv[q][w]), bf16_lo(uv[q][w])), silu_gate(bf16_hi(gv[q][w]), bf16_hi(uv[q][w])));
           if (Yp) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              uint32_t(&y)[8] = t ? uv : gv;
-              pair_up(y);
-              merge(y);
+              uint32_t(&y)[P][8] = t ? uv : gv;
 #pragma unroll
-              for (int part = 0; part < 2; ++part)
-                store16(four(y + 4 * part), ry, vy + (row + part * 16) * yb + (t * (uint32_t)F + f) * 2);
+              for (int q = 0; q < P; ++q) pair_up(y[q]);
+              leave(y, ry, row * yb + (t * (uint32_t)F + f) * 2, yb);
             }
           }
-          if (p.amax || want_q) {
-            // (rows past the end hold 0 or NaN, which the maximum passes over)
-            float am = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) am = fmaxf(am, fmaxf(fabsf(bf16_lo(hv[w])), fabsf(bf16_hi(hv[w]))));
-            tile_amax = fmaxf(tile_amax, am);
-            pair_up(hv);
-            if (want_q) {
-              // the two halves hold the 32 features of one block of one row
-              const int se = shared_exp<2>(__uint_as_float(max_of_halves(__float_as_uint(am))));
-              uint32_t d[2];
+          for (int q = 0; q < P; ++q) {
+            if (p.amax || want_q) {
+              // (rows past the end hold 0 or NaN, which the maximum passes over)
+              float am = 0.0f;
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                float v[8];
+              for (int w = 0; w < 8; ++w) am = fmaxf(am, fmaxf(fabsf(bf16_lo(hv[q][w])), fabsf(bf16_hi(hv[q][w]))));
+              tile_amax = fmaxf(tile_amax, am);
+              pair_up(hv[q]);
+              if (want_q) {
+                // the two halves hold the 32 features of one block of one row
+                const int se = shared_exp<2>(__uint_as_float(max_of_halves(__float_as_uint(am))));
+                uint32_t d[2];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  v[2 * w] = bf16_lo(hv[4 * t + w]);
-                  v[2 * w + 1] = bf16_hi(hv[4 * t + w]);
+                for (int t = 0; t < 2; ++t) {
+                  float v[8];
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) {
+                    v[2 * w] = bf16_lo(hv[q][4 * t + w]);
+                    v[2 * w + 1] = bf16_hi(hv[q][4 * t + w]);
+                  }
+                  d[t] = encode8_e2m1(v, se);
                 }
-                d[t] = encode8_e2m1(v, se);
+                swap_halves(d[0], d[1]);
+                __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){d[0], d[1]}, rq, vq, row * qb + f / 2 + 16 * q, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32 + q, 0);
               }
-              swap_halves(d[0], d[1]);
-              __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){d[0], d[1]}, rq, vq, row * qb + f / 2, 0);
-              __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32, 0);
+            } else {
+              pair_up(hv[q]);
             }
-          } else {
-            pair_up(hv);
           }
-          if (Hp) {
-            merge(hv);
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-              store16(four(hv + 4 * part), rh, vh + (row + part * 16) * hb + f * 2);
-          }
-          nst += (Yp ? 4 : 0) + (Hp ? 2 : 0) + (want_q ? 2 : 0) + (EPI == EPI_SILU_C ? 3 : 0);
-          __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
+          if (Hp) leave(hv, rh, row * hb + f * 2, hb);
+          nst += P * ((Yp ? 4 : 0) + (Hp ? 2 : 0) + (want_q ? 2 : 0)) + (EPI == EPI_SILU_C ? 2 * P + 1 : 0);
+          __builtin_amdgcn_sched_barrier(0);  // P pairs at a time: registers
         }
       }
     } else {
       constexpr uint32_t EB = OUT32 ? 4 : 2;  // bytes per element
       const uint32_t cb = (uint32_t)p.N * EB;
       const __amdgpu_buffer_rsrc_t rc = region(reinterpret_cast<uint8_t*>(p.c) + m0 * cb, tile_rows * cb);
-      const uint32_t vc = pr * cb + pu * 16;
+      const uint32_t vc = r8 * cb + u8 * 16;
 #pragma unroll
-      for (int x = 0; x < FM * FN; ++x) {
-        const typename Operands<FMT>::Acc& a = acc[x / FN][x % FN];
-        const float rs = row_scale(x / FN);
-        const uint32_t row = wm * WTM + (x / FN) * 32, col = (uint32_t)n0 + wn * WTN + (x % FN) * 32;
-        if (col >= (uint32_t)p.N) continue;  // (N % 32 == 0)
+      for (int i = 0; i < FM; ++i) {
+        const float rs = row_scale(i);
+        const uint32_t row = wm * WTM + i * 32;
         if constexpr (OUT32) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {  // 16 columns at a time
-            uint32_t w[8];
+          for (int j = 0; j < FN; ++j) {
+            const uint32_t col = (uint32_t)n0 + wn * WTN + j * 32;
+            if (col >= (uint32_t)p.N) continue;  // (N % 32 == 0)
+            uint32_t w[2][8];  // 16 columns each
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const f32x4_t e = elements<FMT>(a, 2 * q + g, rs, col_scales(x % FN, 2 * q + g));
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) w[4 * g + k] = __float_as_uint(e[k]);
+              for (int g = 0; g < 2; ++g) {
+                const f32x4_t e = elements<FMT>(acc[i][j], 2 * q + g, rs, col_scales(j, 2 * q + g));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[q][4 * g + k] = __float_as_uint(e[k]);
+              }
+              merge(w[q]);
             }
-            merge(w);
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-              store16(four(w + 4 * part), rc, vc + (row + part * 16) * cb + col * EB + q * 64);
+            for (int part = 0; part < 4; part += 2) {
+              join(w[0] + 2 * part, w[1] + 2 * part);
+              store16(four(w[0] + 2 * part), rc, vc + (row + part * 8) * cb + col * EB);
+              store16(four(w[1] + 2 * part), rc, vc + (row + part * 8 + 8) * cb + col * EB);
+            }
+            nst += 4;
+            __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
           }
         } else {
-          uint32_t w[8];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) bf16x4(elements<FMT>(a, g, rs, col_scales(x % FN, g)), w + 2 * g);
-          pair_up(w);
-          merge(w);
+          for (int j = 0; j < FN; j += 2) {
+            const uint32_t col = (uint32_t)n0 + wn * WTN + j * 32;
+            if (col >= (uint32_t)p.N) continue;  // (N % 32 == 0)
+            uint32_t w[2][8];
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-            store16(four(w + 4 * part), rc, vc + (row + part * 16) * cb + col * EB);
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) bf16x4(elements<FMT>(acc[i][j + t], g, rs, col_scales(j + t, g)), w[t] + 2 * g);
+              pair_up(w[t]);
+              merge(w[t]);
+            }
+            // (N may end between the two blocks: units 4..7 are then dropped)
+            const uint32_t at = (u8 < 4 || col + 32 < (uint32_t)p.N ? vc : kOOB) + row * cb + col * EB;
+#pragma unroll
+            for (int part = 0; part < 4; part += 2) {
+              join(w[0] + 2 * part, w[1] + 2 * part);
+              store16(four(w[0] + 2 * part), rc, at + part * 8 * cb);
+              store16(four(w[1] + 2 * part), rc, at + (part * 8 + 8) * cb);
+            }
+            nst += 4;
+            __builtin_amdgcn_sched_barrier(0);  // two blocks at a time: registers
+          }
         }
-        nst += EB;
-        __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
       }
     }
     if constexpr (FMT == INT8) so = so + SBUF == SRING ? 0 : so + SBUF;

@@ -79,7 +79,7 @@ extern "C" int grouped_gemm_int8_silu_gate(const int8_t* a_q, const float* a_s, 
   const int rc = check_operands(a_q, a_s, b_q, b_s, expert_offsets, E, M_total, 2 * F, K, p);
   if (rc != NVFP4MOE_OK) return rc;
   if (F % 128 != 0 || 2 * F * K >= (1LL << 31)) return NVFP4MOE_ESHAPE;  // gate and up rows: one region
-  if (!aligned(y1, 16) || !aligned(h, 16) || !aligned(q_y1, 8) || !aligned(amax_out, 4)) return NVFP4MOE_ESHAPE;
+  if (!aligned(y1, 16) || !aligned(h, 16) || !aligned(q_y1, 16) || !aligned(s_y1, 2) || !aligned(amax_out, 4)) return NVFP4MOE_ESHAPE;
   const int arch = check_arch();
   if (arch != NVFP4MOE_OK) return arch;
   hipStream_t st = as_stream(stream);

@@ -118,7 +118,7 @@ int silu_gate_impl(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q, c
   const int rc = check_operands(a_q, a_s, b_q, b_s, expert_offsets, E, M_total, 2 * F, K, p);
   if (rc != NVFP4MOE_OK) return rc;
   if (F % 128 != 0 || 2 * F * (K / 2) >= (1LL << 31)) return NVFP4MOE_ESHAPE;  // gate and up rows: one region
-  if (!aligned(y1, 16) || !aligned(h, 16) || !aligned(q_h, 4) || !aligned(q_y1, 8) || !aligned(amax_out, 4))
+  if (!aligned(y1, 16) || !aligned(h, 16) || !aligned(q_h, 4) || !aligned(q_y1, 16) || !aligned(s_y1, 2) || !aligned(amax_out, 4))
     return NVFP4MOE_ESHAPE;
   const int arch = check_arch();
   if (arch != NVFP4MOE_OK) return arch;
