@@ -54,6 +54,7 @@ struct Params {
   int E, n_tiles;
 };
 
+constexpr int kRowB = 128;          // code bytes per row and stage: one cache line
 constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
 constexpr int kTiles = 64;          // tiles looked up at a time
 
@@ -85,11 +86,10 @@ __device__ __forceinline__ typename Operands<FMT>::Frag frag(uint32_t at) {
   else return v;
 }
 
-// 16-byte unit u of code row r (RB bytes) lies at unit u ^ swz(r).  The swizzle
-// repeats every 32 rows, so a wave's fragments differ by constant offsets, and
-// unit 2c + h of chunk c is one XOR away from unit h.
-template <int RB>
-__device__ __forceinline__ int swz(int r) { return rswz<RB>(r & 31); }
+// 16-byte unit u of code row r lies at unit u ^ swz(r).  The swizzle repeats
+// every 32 rows, so a wave's fragments differ by constant offsets, and unit
+// 2c + h of chunk c is one XOR away from unit h.
+__device__ __forceinline__ int swz(int r) { return kswz(r & 31); }
 
 // Accumulators stay in the accumulation registers until an element is used:
 // left to itself the compiler moves whole blocks to vector registers at the
@@ -180,12 +180,9 @@ __device__ __forceinline__ void join(uint32_t* a, uint32_t* b) {
 }
 __device__ __forceinline__ i32x4_t four(const uint32_t* w) { return (i32x4_t){(int)w[0], (int)w[1], (int)w[2], (int)w[3]}; }
 
-// RB: code bytes per row and stage, 128 (a cache line), or 64 for two
-// workgroups per CU.
-template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
-__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_kernel(Params p) {
-  constexpr int NW = WM * WN, CHUNKS = RB / 32, LROWS = 1024 / RB, UNITS = RB / 16;  // rows a load, units a row
-  static_assert(RB == 128 || (RB == 64 && FMT == INT8), "MX scales are read for two stages of 128 bytes");
+template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+__global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p) {
+  constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
   static_assert(FM >= 1 && FN >= 2 && WTM % 32 == 0 && WTN % 64 == 0, "wave tiling");
   constexpr bool SILU = EPI != EPI_PLAIN;
@@ -193,12 +190,12 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
   // Scale rows of A (whole loads), and the scales' ring: of two stages' scales,
   // or of tiles'.  The loads run up to S tiles ahead of an epilogue.
   constexpr int SA = FMT == INT8 ? 256 : BM < 64 ? 64 : BM, SROW = FMT == INT8 ? 4 : 16;
-  constexpr int AT_B = BM * RB, STAGE = AT_B + BN * RB;  // codes of A, then B
+  constexpr int AT_B = BM * kRowB, STAGE = AT_B + BN * kRowB;  // codes of A, then B
   constexpr int SBUF = (SA + BN) * SROW, SRING = (FMT == INT8 ? S + 1 : S) * SBUF;
-  // 1 KiB loads of LROWS code rows, and of 64 (MX) or 256 rows of scales, dealt to the waves in
+  // 1 KiB loads of 8 code rows, and of 64 (MX) or 256 rows of scales, dealt to the waves in
   // turn; every wave issues NDMA per stage, whatever is left over landing in a
   // pad, so that its waits are constants.
-  constexpr int A_LOADS = BM / LROWS, B_LOADS = BN / LROWS, SC_LOADS = (SA + BN) * SROW / 1024;
+  constexpr int A_LOADS = BM / 8, B_LOADS = BN / 8, SC_LOADS = (SA + BN) * SROW / 1024;
   constexpr int A_INSTR = A_LOADS / NW, B_INSTR = B_LOADS / NW, SC_INSTR = (SC_LOADS + NW - 1) / NW;
   constexpr int NDMA = A_INSTR + B_INSTR + SC_INSTR, HALF = (NDMA + 1) / 2;
   static_assert(A_LOADS % NW == 0 && B_LOADS % NW == 0 && NW % 4 == 0, "the rows of a wave's loads agree modulo 32");
@@ -304,14 +301,14 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
   };
 
   // Loads.  A lane's byte offsets of its first loads of a tile; load i adds
-  // LROWS NW i rows (gate and up granules of 32 rows alternate, and LROWS NW is
-  // a multiple of 32).  Scales are read 16 bytes a row, for two stages at once:
+  // 8 NW i rows (gate and up granules of 32 rows alternate, and 8 NW is a
+  // multiple of 32).  Scales are read 16 bytes a row, for two stages at once:
   // every row is a cache line of its own, and a load of 64 lines takes the
   // address unit 64 to 110 cycles however short they are (measured; a 1 KiB
   // load of whole lines takes 16).
   const int64_t F = p.N / 2;
   const uint32_t rowb = (uint32_t)(FMT == INT8 ? p.K : p.K / 2), srow = FMT == INT8 ? 4u : (uint32_t)(p.K / 32);
-  const int lrow = wid * LROWS + lane / UNITS, lunit = (lane & (UNITS - 1)) ^ swz<RB>(lrow);
+  const int lrow = wid * 8 + lane / 8, lunit = (lane & 7) ^ swz(lrow);
   const uint32_t la0 = (uint32_t)lrow * rowb + lunit * 16;
   const uint32_t lb0 = (uint32_t)(SILU ? gate_up_row(lrow, F, 0) : lrow) * rowb + lunit * 16;
   uint32_t ls0[SC_INSTR];
@@ -324,7 +321,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
     const bool real = idx < SC_LOADS && (!is_a || row < BM);
     ls0[x] = real ? (uint32_t)(SILU && !is_a ? gate_up_row(row, F, 0) : row) * srow : kOOB;
   }
-  constexpr int KS = FMT == INT8 ? RB : 2 * RB;       // reduction elements per stage
+  constexpr int KS = FMT == INT8 ? kRowB : 2 * kRowB;       // reduction elements per stage
   const int nk = p.K > 0 ? (int)((p.K + KS - 1) / KS) : 1;  // (K == 0: one stage of zeros)
   // The last stage may be short (MXFP4: by half): units past the row are not
   // read (zeros), and the MX scales of its upper chunks, which would be the
@@ -354,15 +351,15 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
   };
   auto offsets = [&]() {
     const bool last = ld_kt + 1 == nk;
-    la = (la0 + (uint32_t)ld_kt * RB) | (last ? beyond : 0u);
-    lb = (lb0 + (uint32_t)ld_kt * RB) | (last ? beyond : 0u);
+    la = (la0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
+    lb = (lb0 + (uint32_t)ld_kt * kRowB) | (last ? beyond : 0u);
   };
   auto dma = [&](int x) __attribute__((always_inline)) {  // load x of NDMA of the cursor's stage
     if (x < A_INSTR) {
-      dma16(ra, ld_on ? smem_lds + ld_slot + (wid + NW * x) * 1024 : pad, la + (uint32_t)(LROWS * NW * x) * rowb);
+      dma16(ra, ld_on ? smem_lds + ld_slot + (wid + NW * x) * 1024 : pad, la + (uint32_t)(8 * NW * x) * rowb);
     } else if (x < A_INSTR + B_INSTR) {
       const int i = x - A_INSTR;
-      const uint32_t row = (uint32_t)(SILU ? gate_up_row(LROWS * NW * i, F, 0) : LROWS * NW * i);
+      const uint32_t row = (uint32_t)(SILU ? gate_up_row(8 * NW * i, F, 0) : 8 * NW * i);
       dma16(rb, ld_on ? smem_lds + ld_slot + AT_B + (wid + NW * i) * 1024 : pad, lb + row * rowb);
     } else {
       const int i = x - A_INSTR - B_INSTR;
@@ -389,8 +386,8 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
 
   // This lane's fragment addresses in slot 0: row lane % 32 of the wave's
   // first row block, unit lane / 32; and its first scale words.
-  const uint32_t unit0 = (lane & 31) * RB + (((lane >> 5) ^ swz<RB>(lane & 31)) << 4);
-  const uint32_t fa0 = smem_lds + wm * WTM * RB + unit0, fb0 = smem_lds + AT_B + wn * WTN * RB + unit0;
+  const uint32_t unit0 = (lane & 31) * kRowB + (((lane >> 5) ^ swz(lane & 31)) << 4);
+  const uint32_t fa0 = smem_lds + wm * WTM * kRowB + unit0, fb0 = smem_lds + AT_B + wn * WTN * kRowB + unit0;
   const uint32_t sa0 = scales + (wm * WTM + (lane & 31)) * 16, sb0 = scales + (SA + wn * WTN + (lane & 31)) * 16;
   const int sh = 8 * (lane >> 5);
 
@@ -399,9 +396,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
   int sa[FM], sb[FN];      // of the chunks in work
   auto read = [&](uint32_t slot, int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag<FMT>(((fb0 + slot) ^ (32 * c)) + j * 32 * RB);
+    for (int j = 0; j < FN; ++j) fb[c & 1][j] = frag<FMT>(((fb0 + slot) ^ (32 * c)) + j * 32 * kRowB);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag<FMT>(((fa0 + slot) ^ (32 * c)) + i * 32 * RB);
+    for (int i = 0; i < FM; ++i) fa[c & 1][i] = frag<FMT>(((fa0 + slot) ^ (32 * c)) + i * 32 * kRowB);
   };
   auto read_scales = [&](uint32_t at) __attribute__((always_inline)) {
     if constexpr (FMT == INT8) return;
@@ -499,13 +496,11 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
       chunk(0, HALF, NDMA, rest);
       if (rest) advance();
       rest = true;
-      if constexpr (CHUNKS == 4) {
-        read(slot, 2);
-        chunk(1, 0, 0, false);
-        take_scales(1, last && p.K % KS != 0 ? 0 : 24);
-        read(slot, 3);
-        chunk(2, 0, 0, false);
-      }
+      read(slot, 2);
+      chunk(1, 0, 0, false);
+      take_scales(1, last && p.K % KS != 0 ? 0 : 24);
+      read(slot, 3);
+      chunk(2, 0, 0, false);
       // The last chunk's fragments are in registers, so the slot is free once
       // every wave is here; the next stage has landed.  Stores of an epilogue
       // are younger than the loads of the S stages after it and need not have
@@ -530,7 +525,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
       }
       read(slot, 0);
       read_scales(so);
-      chunk(CHUNKS - 1, 0, HALF, true);
+      chunk(3, 0, HALF, true);
     }
     // The rest of the cursor's stage goes before the epilogue's stores.
 #pragma unroll
@@ -787,12 +782,12 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4 * (128 / RB)) void codes_ke
 }
 
 // Resident workgroups per CU (the same on every gfx950 device).
-template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 int resident_per_cu() {
   static int cached = 0;
   if (cached > 0) return cached;
   int occ = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32>, WM * WN * 64,
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32>, WM * WN * 64,
                                                    0) != hipSuccess ||
       occ < 1)
     occ = 1;
@@ -800,16 +795,16 @@ int resident_per_cu() {
   return occ;
 }
 
-template <int FMT, int RB, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 int launch_tiles(const Params& p0, hipStream_t st) {
   Params p = p0;
   p.n_tiles = (int)cdiv(p.N, BN);
   const int64_t upper = (cdiv(p.M, BM) + p.E) * p.n_tiles;  // tiles at most
   if (upper > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
-  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32>();
+  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, BM, BN, WM, WN, S, EPI, OUT32>();
   if (grid > upper) grid = upper;
   grid = cdiv(grid, 8) * 8;  // whole XCD rounds
-  codes_kernel<FMT, RB, BM, BN, WM, WN, S, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
+  codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
   return launch_status();
 }
 

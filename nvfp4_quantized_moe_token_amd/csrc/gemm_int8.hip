@@ -13,13 +13,35 @@
 namespace nvfp4moe {
 namespace {
 
-// Tiles by the mean rows per expert, as for MXFP4.
+// Tiles by the mean rows per expert (the host does not know more).  Up to 112
+// rows the work is reading the weights: small row blocks and a ring three stages
+// deep.  Then it is the MFMAs, the operands' way to LDS and the stores; blocks of
+// 192 where most experts' rows fit in one, or in two of them where they take two
+// of 256 as well.  Measured kernel times in us, 128 experts, gate+up with H
+// stored (768 features, K = 2048) and down (N = 2048, K = 768):
+//   rows      gate+up, blocks of                  down, blocks of
+//             32     64    128    192    256      32     64    128    192    256
+//    16     73.3   75.4   78.6                  33.8   36.1   39.9
+//    24     82.2   75.7   79.2                  37.1   36.5   40.7
+//    32     82.8   76.9   80.2                  37.2   37.1   41.1
+//    48     92.7   91.0   83.1                  42.8   43.4   44.3
+//    64    110.1   93.4   84.7   99.3  111.1    51.2   46.1   45.0   52.2   58.9
+//    96    134.4  106.4   91.0  102.4  111.3    59.9   53.7   48.9   54.0   60.7
+//   128    160.2  125.7  113.0  107.4  112.8    90.9   70.5   64.2   62.2   66.5
+//   160           137.2  129.4  127.1  117.1           87.1   85.1   77.4   73.6
+//   256           193.7  162.6  166.3  168.8          126.1  102.7  112.1  104.8
+//   320           230.7  185.1  177.2  197.7          149.3  120.9  120.9  133.2
+//   384           263.5  218.7  220.0  207.7          177.8  140.1  143.2  135.7
+//   512           337.4  278.7  262.8  265.4          243.2  181.8  176.3  171.4
+//  1024           627.4  505.1  479.6  462.9          424.9  355.4  330.7  317.1
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
-  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<INT8, 128, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<INT8, 128, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<INT8, 128, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
-  return launch_tiles<INT8, 128, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+  const int64_t E = p.E, M = p.M;
+  if (M <= 20 * E) return launch_tiles<INT8, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (M <= 40 * E) return launch_tiles<INT8, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (M <= 112 * E) return launch_tiles<INT8, 128, 256, 2, 4, 3, EPI, OUT32>(p, st);
+  if (M <= 144 * E || (M > 272 * E && M <= 352 * E)) return launch_tiles<INT8, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  return launch_tiles<INT8, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 
 // Argument checks shared by both entry points, then the launch parameters.

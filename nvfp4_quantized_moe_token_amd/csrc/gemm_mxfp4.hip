@@ -55,10 +55,10 @@ namespace {
 //   208                  118.7   96.1                  67.9   55.6
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
-  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 128, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 128, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<MXFP4, 128, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
-  return launch_tiles<MXFP4, 128, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
+  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  return launch_tiles<MXFP4, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 
 // Argument checks shared by both entry points, then the launch parameters.
