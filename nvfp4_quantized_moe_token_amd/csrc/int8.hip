@@ -9,8 +9,8 @@
 // or a NaN gets that infinity or a NaN as its scale and zeros as codes: its
 // products are NaN.
 //
-// Layout.  A wave per row up to 4096 elements, 16 consecutive ones a lane and
-// step, kept in registers between the maximum and the encoding; a workgroup
+// Layout.  Sixteen lanes per row up to 768 elements, a wave up to 4096, 16
+// consecutive elements a lane and step, kept in registers between the maximum and the encoding; a workgroup
 // per row beyond, which reads the row a second time (from the cache).  The
 // permutation's form encodes a token once and writes its k rows.
 #include "common.hpp"
@@ -59,33 +59,61 @@ __device__ __forceinline__ uint32_t amax_bits16(uint32_t m, const float (&v)[16]
   return m;
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t m) {
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+  for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
   return m;
 }
 
-// Codes of 16 elements (element i in byte i).  live: the scale is positive and
-// finite.
-__device__ __forceinline__ uint4 encode16(const float (&v)[16], float s, bool live) {
+// What a row's elements are divided by.  x / s correctly rounded is one product
+// and two fused multiply-adds with the rounded reciprocal y of s (Markstein:
+// q = x y, r = x - q s exactly, q + r y rounds as x / s does), where neither y nor
+// r leaves the normal range or the code is 0 anyway; `direct` scales, below
+// 2^-90, take the division itself.
+struct Divisor {
+  float s, y;
+  bool live, direct;
+};
+__device__ __forceinline__ Divisor divisor(uint32_t amax_bits) {
+  Divisor d;
+  d.s = __uint_as_float(amax_bits) / 127.0f;
+  d.y = 1.0f / d.s;
+  d.live = amax_bits < 0x7F800000u && d.s > 0.0f;  // positive and finite
+  d.direct = d.s < 0x1p-90f;
+  return d;
+}
+
+// Codes of 16 elements (element i in byte i).  The clamp comes before the
+// rounding, which is to whole numbers either way; adding 1.5 * 2^23 rounds to
+// nearest even and leaves the whole number's low byte in the sum's.
+template <bool DIRECT>
+__device__ __forceinline__ uint4 encode16_by(const float (&v)[16], const Divisor& d) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float r = __builtin_amdgcn_fmed3f(rintf(v[4 * i + j] / s), -127.0f, 127.0f);
-      b[j] = (uint32_t)(int)r & 0xFFu;
+      const float x = v[4 * i + j], q = x * d.y;
+      const float t = DIRECT ? x / d.s : __builtin_fmaf(__builtin_fmaf(-q, d.s, x), d.y, q);
+      b[j] = __float_as_uint(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 12582912.0f);
     }
-    w[i] = live ? b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24 : 0u;
+    w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                                 __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
+    w[i] = d.live ? w[i] : 0u;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ uint4 encode16(const float (&v)[16], const Divisor& d) {
+  return d.direct ? encode16_by<true>(v, d) : encode16_by<false>(v, d);
+}
 
-// NC > 0: a wave per row of at most NC * 1024 elements; NC == 0: a workgroup.
-template <bool BF16, int NC, bool SCATTER>
+// LANES lanes per row of at most NC * LANES * 16 elements; NC == 0: a workgroup.
+template <bool BF16, int LANES, int NC, bool SCATTER>
 __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8Params p) {
-  constexpr int NT = NC ? 64 : 256, GROUPS = 256 / NT;
+  constexpr int NT = LANES, GROUPS = 256 / NT;
+  static_assert(NC ? LANES == 16 || LANES == 64 : LANES == 256, "lanes of a row");
   const int t = threadIdx.x % NT;
   const int64_t n16 = p.K / 16, first = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT,
                 step = (int64_t)gridDim.x * GROUPS;
@@ -106,46 +134,45 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8Params p) {
     if constexpr (NC > 0) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        if (c * 64 + t < n16) load16<BF16>(p.x, row * n16 + c * 64 + t, v[c]);
+        if (c * NT + t < n16) load16<BF16>(p.x, row * n16 + c * NT + t, v[c]);
         else
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[c][i] = 0.0f;
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) m = amax_bits16(m, v[c]);
-      m = wave_max_u32(m);
+      m = lanes_max<NT>(m);
     } else {
       __shared__ uint32_t red[4];
       for (int64_t u = t; u < n16; u += NT) {
         load16<BF16>(p.x, row * n16 + u, v[0]);
         m = amax_bits16(m, v[0]);
       }
-      m = wave_max_u32(m);
+      m = lanes_max<64>(m);
       __syncthreads();  // the row before has been read
       if ((t & 63) == 0) red[t >> 6] = m;
       __syncthreads();
       m = max(max(red[0], red[1]), max(red[2], red[3]));
     }
-    const float s = __uint_as_float(m) / 127.0f;
-    const bool live = m < 0x7F800000u && s > 0.0f;
+    const Divisor d = divisor(m);
     if constexpr (NC > 0) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (c * 64 + t < n16) put(row, c * 64 + t, encode16(v[c], s, live));
+        if (c * NT + t < n16) put(row, c * NT + t, encode16(v[c], d));
     } else {
       for (int64_t u = t; u < n16; u += NT) {
         load16<BF16>(p.x, row * n16 + u, v[0]);
-        put(row, u, encode16(v[0], s, live));
+        put(row, u, encode16(v[0], d));
       }
     }
     if (t == 0) {
       if constexpr (SCATTER) {
         for (int j = 0; j < p.k; ++j) {
           const int32_t r = p.dest[row * p.k + j];
-          if (r >= 0) p.scales[r] = s;
+          if (r >= 0) p.scales[r] = d.s;
         }
       } else {
-        p.scales[row] = s;
+        p.scales[row] = d.s;
       }
     }
   }
@@ -161,19 +188,24 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(Int8Params p) {
 
 template <bool SCATTER>
 int launch(const Int8Params& p, bool bf16, hipStream_t st) {
-  const bool wave = p.K <= 4096;
-  int64_t grid = cdiv(p.rows > 0 ? p.rows : 1, wave ? 4 : 1);
-  if (grid > kMaxStreamGrid) grid = kMaxStreamGrid;
-#define NVQ(B, NC) int8_quantize_kernel<B, NC, SCATTER><<<(unsigned)grid, 256, 0, st>>>(p)
-#define NVQ2(NC)          \
-  do {                    \
-    if (bf16) NVQ(true, NC); \
-    else NVQ(false, NC);  \
+  const bool bf = bf16;
+#define NVQ(B, L, NC)                                                                                         \
+  do {                                                                                                        \
+    const int64_t n = cdiv(p.rows > 0 ? p.rows : 1, 256 / (L));                                               \
+    int8_quantize_kernel<B, L, NC, SCATTER><<<(unsigned)(n < kMaxStreamGrid ? n : kMaxStreamGrid), 256, 0, st>>>(p); \
   } while (0)
-  if (!wave) NVQ2(0);
-  else if (p.K <= 1024) NVQ2(1);
-  else if (p.K <= 2048) NVQ2(2);
-  else NVQ2(4);
+#define NVQ2(L, NC)           \
+  do {                        \
+    if (bf) NVQ(true, L, NC); \
+    else NVQ(false, L, NC);   \
+  } while (0)
+  if (p.K <= 256) NVQ2(16, 1);
+  else if (p.K <= 512) NVQ2(16, 2);
+  else if (p.K <= 768) NVQ2(16, 3);
+  else if (p.K <= 1024) NVQ2(64, 1);
+  else if (p.K <= 2048) NVQ2(64, 2);
+  else if (p.K <= 4096) NVQ2(64, 4);
+  else NVQ2(256, 0);
 #undef NVQ2
 #undef NVQ
   return launch_status();

@@ -121,26 +121,27 @@ __device__ __forceinline__ void store_row(void* base, bool bf16, int64_t at, int
   }
 }
 
-// Sums over the NT threads of a row (a wave, or the whole workgroup, which then
-// calls this together); every thread receives the same bits.  `turn` alternates
-// between two buffers, so one barrier a call is enough.
-template <int NT, int N>
+// Sums over the NT threads of a row (a wave, or several: the GROUPS rows of the
+// workgroup then call this together); every thread of a row receives the same
+// bits.  `turn` alternates between two buffers, so one barrier a call is enough.
+template <int NT, int N, int GROUPS>
 __device__ __forceinline__ void row_sums(float (&s)[N], int& turn) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], o, 64);
   if constexpr (NT > 64) {
-    __shared__ float red[2][2][NT / 64];
+    __shared__ float red[2][2][GROUPS * NT / 64];
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if ((threadIdx.x & 63) == 0) red[turn][i][threadIdx.x >> 6] = s[i];
     __syncthreads();
+    const int first = threadIdx.x / NT * (NT / 64);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float a = red[turn][i][0];
+      float a = red[turn][i][first];
 #pragma unroll
-      for (int w = 1; w < NT / 64; ++w) a += red[turn][i][w];
+      for (int w = 1; w < NT / 64; ++w) a += red[turn][i][first + w];
       s[i] = a;
     }
     turn ^= 1;
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(threads<NT>()) void norm_fwd_kernel(NormParams p) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < N; ++i) s[0] += v[i];
-      row_sums<NT, 1>(s, turn);
+      row_sums<NT, 1, GROUPS>(s, turn);
       m = s[0] * inv_d;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(threads<NT>()) void norm_fwd_kernel(NormParams p) {
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < N; ++i) s[0] += v[i] * v[i];
-    row_sums<NT, 1>(s, turn);
+    row_sums<NT, 1, GROUPS>(s, turn);
     const float r = 1.0f / sqrtf(s[0] * inv_d + p.eps);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = v[i] * r * w[i] + b[i];
@@ -196,9 +197,18 @@ __global__ __launch_bounds__(threads<NT>()) void norm_fwd_kernel(NormParams p) {
   }
 }
 
+// Threads of a backward workgroup: eight waves of a row each, so that few
+// workgroups, whose sums the second launch adds, keep two waves per SIMD.
+template <int NT>
+constexpr int bwd_threads() {
+  return NT < 512 ? 512 : NT;
+}
+
 template <int NT, int NC, int W>
-__global__ __launch_bounds__(threads<NT>()) void norm_bwd_kernel(NormParams p) {
-  constexpr int N = NC * W, GROUPS = threads<NT>() / NT;
+__global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_kernel(NormParams p) {
+  constexpr int N = NC * W, GROUPS = bwd_threads<NT>() / NT;
+  // The next row is on its way while one is in work, where the registers allow.
+  constexpr bool AHEAD = 7 * N + 24 <= (bwd_threads<NT>() > 512 ? 128 : 256);
   const int t = threadIdx.x % NT, D = p.D;
   const float inv_d = 1.0f / (float)D;
   float w[N], dw[N], db[N];
@@ -209,29 +219,58 @@ __global__ __launch_bounds__(threads<NT>()) void norm_bwd_kernel(NormParams p) {
     dw[i] = db[i] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT; row < p.T; row += (int64_t)gridDim.x * GROUPS) {
-    float h[N], dy[N];
-    load_row<NT, NC, W>(p.x, p.x_bf16, row * D, D, t, h);
-    load_row<NT, NC, W>(p.dy, p.dy_bf16, row * D, D, t, dy);
-    const float r = p.rstd_in[row], m = p.rms ? 0.0f : p.mean_in[row];
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT;
+  float h[N], dy[N], r = 0.0f, m = 0.0f;
+  const auto load = [&](int64_t at, float(&x)[N], float(&d)[N], float& rr, float& mm) __attribute__((always_inline)) {
+    load_row<NT, NC, W>(p.x, p.x_bf16, at * D, D, t, x);
+    load_row<NT, NC, W>(p.dy, p.dy_bf16, at * D, D, t, d);
+    rr = p.rstd_in[at];
+    mm = p.rms ? 0.0f : p.mean_in[at];
+  };
+  // (The groups of a workgroup that share a barrier per row go round together,
+  // the last ones perhaps without a row.)
+  const bool together = NT > 64;
+  if (AHEAD && row < p.T) load(row, h, dy, r, m);
+  for (; together ? row - threadIdx.x / NT < p.T : row < p.T; row += step) {
+    const bool live = row < p.T;
+    float nh[N], nd[N], nr = 0.0f, nm = 0.0f;
+    if constexpr (AHEAD) {
+      if (row + step < p.T) load(row + step, nh, nd, nr, nm);
+    } else if (live) {
+      load(row, h, dy, r, m);
+    }
     float s[2] = {0.0f, 0.0f};
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int i = c * W; i < c * W + W; ++i) {
-        h[i] = (c * NT + t) * W < D ? (h[i] - m) * r : 0.0f;
-        dw[i] += dy[i] * h[i];
-        db[i] += dy[i];
-        dy[i] *= w[i];
-        s[0] += dy[i] * h[i];
-        s[1] += dy[i];
-      }
+        for (int i = c * W; i < c * W + W; ++i) {
+          h[i] = (c * NT + t) * W < D ? (h[i] - m) * r : 0.0f;
+          dw[i] += dy[i] * h[i];
+          db[i] += dy[i];
+          dy[i] *= w[i];
+          s[0] += dy[i] * h[i];
+          s[1] += dy[i];
+        }
+    }
     if (p.out) {
-      row_sums<NT, 2>(s, turn);
+      row_sums<NT, 2, GROUPS>(s, turn);
       const float gh = s[0] * inv_d, g = p.rms ? 0.0f : s[1] * inv_d;
+      if (live) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) h[i] = r * (dy[i] - g - h[i] * gh);
-      store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, h);
+        for (int i = 0; i < N; ++i) h[i] = r * (dy[i] - g - h[i] * gh);
+        store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, h);
+      }
+    }
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        h[i] = nh[i];
+        dy[i] = nd[i];
+      }
+      r = nr;
+      m = nm;
     }
   }
   // This workgroup's sums.
@@ -259,48 +298,66 @@ __global__ __launch_bounds__(threads<NT>()) void norm_bwd_kernel(NormParams p) {
   }
 }
 
-// Column sums of rows partial sums: 32 columns a workgroup, 8 groups of rows.
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float* part, int rows, int D, float* dw, float* db) {
-  __shared__ float red[8][33];
+// Column sums of rows partial sums (at most kNormBwdBlocks): 32 columns a
+// workgroup, 32 groups of 8 rows, whose loads are all in flight at once.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int rows, int D, float* dw, float* db) {
+  __shared__ float red[32][33];
   const float* from = part + (int64_t)blockIdx.y * rows * D;
   float* to = blockIdx.y ? db : dw;
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  float s = 0.0f;
-  if (to && col < D)
-    for (int r = g; r < rows; r += 8) s += from[(int64_t)r * D + col];
-  red[g][c] = s;
-  __syncthreads();
-  if (g == 0 && to && col < D) {
+  constexpr int PER = kNormBwdBlocks / 32;
+  float v[PER], s = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][c];
-    to[col] = s;
-  }
+  for (int i = 0; i < PER; ++i) v[i] = to && col < D && g + 32 * i < rows ? from[(int64_t)(g + 32 * i) * D + col] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s += v[i];
+  red[c][g] = s;
+  __syncthreads();
+  // the columns' sums: 32 lanes each
+  s = red[threadIdx.x >> 5][threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  const int out = blockIdx.x * 32 + (threadIdx.x >> 5);
+  if ((threadIdx.x & 31) == 0 && to && out < D) to[out] = s;
 }
 
-int64_t bwd_blocks(int64_t T, int64_t D, bool vec) {
-  const int64_t per = D <= (vec ? 2048 : 512) ? 4 : 1;  // rows a workgroup takes at a time
-  const int64_t n = cdiv(T, per);
-  return n < kNormBwdBlocks ? n : kNormBwdBlocks;
-}
-
-// Kernels by the row's length: a wave a row, then 256 threads, then 1024.
+// Kernels by the row's length: a wave a row, then several.
+template <int NT_, int NC_, int W_>
+struct Shape {
+  static constexpr int NT = NT_, NC = NC_, W = W_;
+};
 template <class F>
 void by_length(int D, bool vec, F&& f) {
-#define NVN(NT, NC, W) return f(std::integral_constant<int, NT>{}, std::integral_constant<int, NC>{}, std::integral_constant<int, W>{})
   if (vec) {
-    if (D <= 512) NVN(64, 1, 8);
-    if (D <= 1024) NVN(64, 2, 8);
-    if (D <= 2048) NVN(64, 4, 8);
-    if (D <= 4096) NVN(256, 2, 8);
-    if (D <= 8192) NVN(256, 4, 8);
-    NVN(256, 8, 8);
+    if (D <= 512) return f(Shape<64, 1, 8>{});
+    if (D <= 1024) return f(Shape<64, 2, 8>{});
+    if (D <= 2048) return f(Shape<64, 4, 8>{});
+    if (D <= 4096) return f(Shape<256, 2, 8>{});
+    if (D <= 8192) return f(Shape<256, 4, 8>{});
+    return f(Shape<256, 8, 8>{});
   }
-  if (D <= 128) NVN(64, 2, 1);
-  if (D <= 512) NVN(64, 8, 1);
-  if (D <= 2048) NVN(256, 8, 1);
-  if (D <= 4096) NVN(256, 16, 1);
-  NVN(1024, 16, 1);
-#undef NVN
+  if (D <= 128) return f(Shape<64, 2, 1>{});
+  if (D <= 512) return f(Shape<64, 8, 1>{});
+  if (D <= 2048) return f(Shape<256, 8, 1>{});
+  if (D <= 4096) return f(Shape<256, 16, 1>{});
+  return f(Shape<1024, 16, 1>{});
+}
+// The backward pass keeps three times as much per column in registers.
+template <class F>
+void bwd_by_length(int D, bool vec, F&& f) {
+  if (vec) {
+    if (D <= 512) return f(Shape<64, 1, 8>{});
+    if (D <= 1024) return f(Shape<64, 2, 8>{});
+    if (D <= 2048) return f(Shape<128, 2, 8>{});
+    if (D <= 4096) return f(Shape<256, 2, 8>{});
+    if (D <= 8192) return f(Shape<512, 2, 8>{});
+    return f(Shape<1024, 2, 8>{});
+  }
+  if (D <= 128) return f(Shape<64, 2, 1>{});
+  if (D <= 512) return f(Shape<64, 8, 1>{});
+  if (D <= 2048) return f(Shape<256, 8, 1>{});
+  if (D <= 4096) return f(Shape<256, 16, 1>{});
+  return f(Shape<1024, 16, 1>{});
 }
 
 bool is_float(int dt) { return dt == NVFP4MOE_F32 || dt == NVFP4MOE_BF16; }
@@ -341,8 +398,8 @@ extern "C" int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, cons
   p.rms = kind == NVFP4MOE_NORM_RMS;
   hipStream_t st = as_stream(stream);
   const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(w, 16) && aligned(b, 16);
-  by_length(p.D, vec, [&](auto nt, auto nc, auto w_) {
-    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, W = decltype(w_)::value;
+  by_length(p.D, vec, [&](auto shape) {
+    constexpr int NT = decltype(shape)::NT, NC = decltype(shape)::NC, W = decltype(shape)::W;
     const int64_t n = cdiv(T, threads<NT>() / NT);
     norm_fwd_kernel<NT, NC, W><<<(unsigned)(n < kStreamBlocks ? n : kStreamBlocks), threads<NT>(), 0, st>>>(p);
   });
@@ -402,13 +459,15 @@ extern "C" int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x
   p.want_dw = dw != nullptr;
   p.want_db = db != nullptr;
   const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(w, 16) && aligned(dx, 16);
-  const int64_t blocks = bwd_blocks(T, D, vec);
-  by_length(p.D, vec, [&](auto nt, auto nc, auto w_) {
-    constexpr int NT = decltype(nt)::value, NC = decltype(nc)::value, W = decltype(w_)::value;
-    norm_bwd_kernel<NT, NC, W><<<(unsigned)blocks, threads<NT>(), 0, st>>>(p);
+  int64_t blocks = kNormBwdBlocks;
+  bwd_by_length(p.D, vec, [&](auto shape) {
+    constexpr int NT = decltype(shape)::NT, NC = decltype(shape)::NC, W = decltype(shape)::W;
+    const int64_t n = cdiv(T, bwd_threads<NT>() / NT);
+    if (n < blocks) blocks = n;
+    norm_bwd_kernel<NT, NC, W><<<(unsigned)blocks, bwd_threads<NT>(), 0, st>>>(p);
   });
   const int rc = launch_status();
   if (rc != NVFP4MOE_OK || (!dw && !db)) return rc;
-  norm_sum_kernel<<<dim3((unsigned)cdiv(D, 32), db ? 2 : 1), 256, 0, st>>>(p.part, (int)blocks, p.D, dw, db);
+  norm_sum_kernel<<<dim3((unsigned)cdiv(D, 32), db ? 2 : 1), 1024, 0, st>>>(p.part, (int)blocks, p.D, dw, db);
   return launch_status();
 }

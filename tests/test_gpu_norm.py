@@ -98,8 +98,9 @@ def _check_backward(dy, x, w, mean, rstd, kind, r, blocks, groups):
         tol = rn * (5 * U * (g + gm + h * (gh + egh)) + eg + h * egh + eh * (gh + egh)) * 1.01
         tol = tol + HALF[r["dx"].dtype] * (np.abs(want[0]) + tol) + 1e-37
         assert (np.abs(_f64(r["dx"]) - want[0]) <= tol).all(), float((np.abs(_f64(r["dx"]) - want[0]) / tol).max())
-    # a thread's rows, the groups of its workgroup, then the workgroups: eight at a time, and those eight
-    chain = -(-T // (blocks * groups)) + groups + -(-blocks // 8) + 8 + 1
+    # a thread's rows, the groups of its workgroup, then at most 256 workgroups' sums: eight by a thread, and
+    # five steps across 32 lanes
+    chain = -(-T // (blocks * groups)) + groups + 8 + 5 + 1
     for got, ref, terms, e in ((r["dw"], want[1], dyn * h, (dyn * eh).sum(0)), (r["db"], want[2], dyn, 0)):
         if got is not None:
             assert got.dtype == F32
@@ -108,7 +109,11 @@ def _check_backward(dy, x, w, mean, rstd, kind, r, blocks, groups):
 
 
 def _grid(T, D, vec):
-    groups = 4 if D <= (2048 if vec else 512) else 1
+    """Workgroups, and the rows that one takes at a time."""
+    if vec:
+        groups = 8 if D <= 1024 else 4 if D <= 2048 else 2 if D <= 4096 else 1
+    else:
+        groups = 8 if D <= 512 else 2 if D <= 4096 else 1
     return min(-(-T // groups), 256), groups
 
 
