@@ -623,14 +623,17 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
                 const uint32_t(&y)[8] = t ? uv[q] : gv[q];
                 uint32_t am = 0;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) am = max(am, max((y[w] << 16) & 0x7FFFFFFFu, y[w] & 0x7FFF0000u));
-                const int sb8 = int8_scale(max_of_halves(am));
+                for (int w = 0; w < 8; ++w) am = max_abs_bf16x2(am, y[w]);
+                am = max_of_halves(max_of_pair(am));
+                const Int8Encoder e = int8_encoder(am);
+                sc[t] |= (uint32_t)int8_scale(am) << (8 * q);
                 anew(t ? uv : gv);
-                sc[t] |= (uint32_t)sb8 << (8 * q);
+                // (the way that takes every block: a second one for tiny blocks
+                // would spill)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                   const float v[4] = {bf16_lo(y[2 * g]), bf16_hi(y[2 * g]), bf16_lo(y[2 * g + 1]), bf16_hi(y[2 * g + 1])};
-                  d[q][g] = encode4_int8(v, sb8);
+                  d[q][g] = encode4_int8<true>(v, e);
                 }
                 swap_halves(d[q][0], d[q][1]);  // 8 columns
                 swap_halves(d[q][2], d[q][3]);

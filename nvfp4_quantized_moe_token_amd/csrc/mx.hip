@@ -39,8 +39,10 @@ __device__ __forceinline__ uint2 encode16_e2m1(const float (&v)[16], int se) {
 }
 
 // 16 fp32 values to MXINT8 codes (16 bytes).
-__device__ __forceinline__ uint4 encode16_int8(const float (&v)[16], int s) {
-  return make_uint4(encode4_int8(v, s), encode4_int8(v + 4, s), encode4_int8(v + 8, s), encode4_int8(v + 12, s));
+template <bool TINY>
+__device__ __forceinline__ uint4 encode16_int8(const float (&v)[16], const Int8Encoder& e) {
+  return make_uint4(encode4_int8<TINY>(v, e), encode4_int8<TINY>(v + 4, e), encode4_int8<TINY>(v + 8, e),
+                    encode4_int8<TINY>(v + 12, e));
 }
 
 // One thread per 16-element half-block; half-blocks 2b and 2b+1 (lanes of
@@ -75,7 +77,8 @@ __global__ __launch_bounds__(NT) void mx_quantize_kernel(const uint4* __restrict
       for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       a = max(a, (uint32_t)__shfl_xor((int)a, 1, 64));  // the partner half of the block
       S = int8_scale(a);
-      reinterpret_cast<uint4*>(q)[hb] = encode16_int8(v, S);
+      const Int8Encoder e = int8_encoder(a);
+      reinterpret_cast<uint4*>(q)[hb] = any_tiny(e) ? encode16_int8<true>(v, e) : encode16_int8<false>(v, e);
     } else {
       float a = 0.0f;
 #pragma unroll
@@ -129,9 +132,10 @@ __global__ __launch_bounds__(NT) void mx_dequantize_kernel(const uint8_t* __rest
         }
       }
     }
-    constexpr int BIAS = ELEM == NVFP4MOE_MX_INT8 ? 133 : 127;
+    const float step = ELEM == NVFP4MOE_MX_INT8 ? int8_step(S) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = S == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[i], S - BIAS);
+    for (int i = 0; i < 16; ++i)
+      v[i] = ELEM == NVFP4MOE_MX_INT8 ? v[i] * step : S == 255 ? __builtin_nanf("") : __builtin_ldexpf(v[i], S - 127);
     if constexpr (BF16) {
       out[2 * hb] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7]));

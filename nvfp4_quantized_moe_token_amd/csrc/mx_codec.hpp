@@ -67,21 +67,44 @@ __device__ __forceinline__ uint32_t encode8_e2m1(const float* v, int se) {
 // S of a block from the greatest of its elements' bits without their signs.
 __device__ __forceinline__ int int8_scale(uint32_t amax_bits) { return (int)(amax_bits >> 23); }
 
-// 4 fp32 values to codes (element i in byte i).  v * 2^(133 - S) is exact or
-// far below a half; adding 1.5 * 2^23 rounds to nearest even and leaves the
-// whole number's low byte in the sum's.
-__device__ __forceinline__ uint32_t encode4_int8(const float* v, int s) {
+// The greater of two bf16 pairs' bits without their signs, half by half.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t m, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m),
+                                                                __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu)));
+}
+// The greatest of a pair as fp32 bits.
+__device__ __forceinline__ uint32_t max_of_pair(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
+
+// Codes of a block with S, four elements at a time (element i in byte i).
+// v * 2^(133 - S) is exact or far below a half, so adding 1.5 * 2^23 in the same
+// step rounds to nearest even and leaves the whole number's low byte in the
+// sum's.  Blocks below 2^-120, whose power is no fp32 number, take another way.
+struct Int8Encoder {
+  float scale;
+  int exponent;
+  bool tiny;
+};
+__device__ __forceinline__ Int8Encoder int8_encoder(uint32_t amax_bits) {
+  const int s = int8_scale(amax_bits);
+  return {__uint_as_float((uint32_t)(260 - s) << 23), 133 - s, s < 7 && amax_bits != 0};  // (zeros: any scale)
+}
+template <bool TINY>
+__device__ __forceinline__ uint32_t encode4_int8(const float* v, const Int8Encoder& e) {
   uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    b[i] = __float_as_uint(__builtin_amdgcn_fmed3f(__builtin_ldexpf(v[i], 133 - s), -127.0f, 127.0f) + 12582912.0f);
+  for (int i = 0; i < 4; ++i) {
+    const float n = TINY ? __builtin_ldexpf(v[i], e.exponent) + 12582912.0f : __builtin_fmaf(v[i], e.scale, 12582912.0f);
+    b[i] = __float_as_uint(__builtin_amdgcn_fmed3f(n, 12582912.0f - 127.0f, 12582912.0f + 127.0f));
+  }
   return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u),
                                0x05040100u);
 }
+// Whether any lane's block needs the other way (the same answer in every lane).
+__device__ __forceinline__ bool any_tiny(const Int8Encoder& e) { return __any(e.tiny); }
 
-// Value of a code.
-__device__ __forceinline__ float decode_int8(int q, int s) {
-  return s == 255 ? __builtin_nanf("") : __builtin_ldexpf((float)q, s - 133);
-}
+// What a block's codes are multiplied with: 2^(S - 133), or NaN.
+__device__ __forceinline__ float int8_step(int s) { return s == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, s - 133); }
+__device__ __forceinline__ float decode_int8(int q, float step) { return (float)q * step; }
 
 }  // namespace nvfp4moe

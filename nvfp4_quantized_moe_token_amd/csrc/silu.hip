@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void silu_bwd_mx_kernel(const uint8_t* __restr
     const int64_t at = r * 2 * n16 + c;
     const uint4 gq = reinterpret_cast<const uint4*>(q)[at], uq = reinterpret_cast<const uint4*>(q)[at + n16];
     const uint4 d0 = dh[2 * i], d1 = dh[2 * i + 1];
-    const int gs = s[at >> 1], us = s[(at + n16) >> 1];  // (n16 is even)
+    const float gs = int8_step(s[at >> 1]), us = int8_step(s[(at + n16) >> 1]);  // (n16 is even)
     const uint32_t g[4] = {gq.x, gq.y, gq.z, gq.w}, u[4] = {uq.x, uq.y, uq.z, uq.w};
     const uint32_t d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
     uint32_t og[8], ou[8], oh[8];

@@ -63,8 +63,13 @@ def _need(t, name, dtype, *shape):
     dt, sh = t.dtype, t.shape
     if dt is not dtype and (isinstance(dtype, torch.dtype) or dt not in dtype):
         raise ValueError("%s: dtype %s is not supported" % (name, dt))
-    if sh != shape and (len(sh) != len(shape) or any(n is not None and n != m for n, m in zip(shape, sh))):
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(sh), tuple(shape)))
+    if sh != shape:
+        ok = len(sh) == len(shape)
+        for n, m in zip(shape, sh):
+            if n is not None and n != m:
+                ok = False
+        if not ok:
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(sh), tuple(shape)))
 
 
 _SAME_DEVICE = contextlib.nullcontext()
