@@ -843,7 +843,8 @@ int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, const void* w, 
  *   dx [T][D] F32 or BF16 or NULL; dw, db [D] fp32 or NULL (overwritten; zeros
  *   for T == 0).  At least one of the three; none may overlap an input.
  *   workspace of layer_norm_bwd_workspace_size(T, D) bytes, 16-byte aligned,
- *   for dw or db (else NULL will do); its content need not be kept.
+ *   for dw or db (else, and where that is 0, NULL will do); its content need not
+ *   be kept.
  * The same bits on every run (no atomics).  Errors as layer_norm, EWORKSPACE.
  */
 size_t layer_norm_bwd_workspace_size(int64_t T, int64_t D);

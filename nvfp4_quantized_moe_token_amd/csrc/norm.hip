@@ -18,7 +18,8 @@
 // accesses, single ones otherwise.  Groups go round over the rows and keep the
 // weights, and in the backward pass the columns' sums, in registers.  The
 // sums of a workgroup go to the workspace as one row, and a second launch adds
-// those rows in order: no atomics, the same bits every time.
+// those rows in order: no atomics, the same bits every time.  Few rows take one
+// launch, some workgroups of which sum columns while the others write dx.
 #include <type_traits>
 
 #include "common.hpp"
@@ -28,6 +29,14 @@ namespace {
 
 constexpr int kNormMaxD = 16384;
 constexpr int kNormBwdBlocks = 256;  // rows of partial sums at most
+// Up to so many rows the gradient takes one launch.  Measured (us through the C
+// entry point, both gradients; one launch and two):
+//   rows   512 columns   2048         2557 fp32    8192
+//     16   3.7   6.9     3.5   8.0    4.8   9.1    3.6   7.5
+//    256   5.9   7.2     5.8   8.7    5.2  11.1   10.7  17.0
+//    512   9.5   7.2     9.5   9.4    7.4  13.4   22.3  17.8
+//   1024  17.2   7.6    21.2  10.9   14.5  15.8   43.3  22.3
+constexpr int kNormFewRows = 384;
 
 struct NormParams {
   const void* x;
@@ -40,6 +49,8 @@ struct NormParams {
   float* mean;
   float* rstd;
   float* part;  // backward: [2][gridDim.x][D] partial sums of dw, db
+  float* dw;    // the same at once (few rows)
+  float* db;
   int64_t T;
   int D;
   float eps;
@@ -298,6 +309,76 @@ __global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_kernel(NormParams 
   }
 }
 
+// Few rows: one launch.  The first workgroups take 32 columns each and sum them
+// over all rows, which the cache then holds for the others, each of which takes
+// rows and writes dx.
+template <int NT, int NC, int W>
+__global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_few_kernel(NormParams p, int strips) {
+  constexpr int N = NC * W, BT = bwd_threads<NT>(), GROUPS = BT / NT;
+  const int D = p.D;
+  if ((int)blockIdx.x < strips) {
+    constexpr int G = BT / 32;  // threads of a column
+    __shared__ float red[2][32][G + 1];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+    float dw = 0.0f, db = 0.0f;
+    if (col < D) {
+#pragma unroll 4
+      for (int64_t t = g; t < p.T; t += G) {
+        const int64_t at = t * D + col;
+        const float x = p.x_bf16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p.x)[at]) : reinterpret_cast<const float*>(p.x)[at];
+        const float dy = p.dy_bf16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p.dy)[at]) : reinterpret_cast<const float*>(p.dy)[at];
+        dw += dy * ((x - (p.rms ? 0.0f : p.mean_in[t])) * p.rstd_in[t]);
+        db += dy;
+      }
+    }
+    red[0][c][g] = dw;
+    red[1][c][g] = db;
+    __syncthreads();
+    const int oc = threadIdx.x / G, og = threadIdx.x % G, out = blockIdx.x * 32 + oc;
+    dw = red[0][oc][og];
+    db = red[1][oc][og];
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) {
+      dw += __shfl_xor(dw, o, 64);
+      db += __shfl_xor(db, o, 64);
+    }
+    if (og == 0 && out < D) {
+      if (p.dw) p.dw[out] = dw;
+      if (p.db) p.db[out] = db;
+    }
+    return;
+  }
+  const int t = threadIdx.x % NT;
+  const int64_t row = ((int64_t)blockIdx.x - strips) * GROUPS + threadIdx.x / NT;
+  const bool live = row < p.T;
+  const float inv_d = 1.0f / (float)D;
+  float h[N], g[N], w[N], s[2] = {0.0f, 0.0f}, r = 0.0f;
+  if (live) {
+    load_row<NT, NC, W>(p.x, p.x_bf16, row * D, D, t, h);
+    load_row<NT, NC, W>(p.dy, p.dy_bf16, row * D, D, t, g);
+    if (p.w) load_row<NT, NC, W>(p.w, p.w_bf16, 0, D, t, w);
+    r = p.rstd_in[row];
+    const float m = p.rms ? 0.0f : p.mean_in[row];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = c * W; i < c * W + W; ++i) {
+        h[i] = (c * NT + t) * W < D ? (h[i] - m) * r : 0.0f;
+        if (p.w) g[i] *= w[i];
+        s[0] += g[i] * h[i];
+        s[1] += g[i];
+      }
+  }
+  int turn = 0;
+  row_sums<NT, 2, GROUPS>(s, turn);
+  if (live) {
+    const float gh = s[0] * inv_d, gm = p.rms ? 0.0f : s[1] * inv_d;
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = r * (g[i] - gm - h[i] * gh);
+    store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, h);
+  }
+}
+
 // Column sums of rows partial sums (at most kNormBwdBlocks): 32 columns a
 // workgroup, 32 groups of 8 rows, whose loads are all in flight at once.
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* part, int rows, int D, float* dw, float* db) {
@@ -407,7 +488,7 @@ extern "C" int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, cons
 }
 
 extern "C" size_t layer_norm_bwd_workspace_size(int64_t T, int64_t D) {
-  if (T < 1 || D < 1 || D > kNormMaxD) return 0;
+  if (T <= kNormFewRows || D < 1 || D > kNormMaxD) return 0;
   const int64_t n = T < kNormBwdBlocks ? T : kNormBwdBlocks;
   return (size_t)(2 * n * D * 4);
 }
@@ -428,7 +509,7 @@ extern "C" int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x
   if (!aligned(x, xb) || !aligned(dy, yb) || !aligned(w, wb) || !aligned(dx, ob) || !aligned(mean, 4) ||
       !aligned(rstd, 4) || !aligned(dw, 4) || !aligned(db, 4))
     return NVFP4MOE_ESHAPE;
-  if (T > 0 && (dw || db)) {
+  if (T > kNormFewRows && (dw || db)) {
     if (!workspace || ws_bytes < layer_norm_bwd_workspace_size(T, D)) return NVFP4MOE_EWORKSPACE;
     if (!aligned(workspace, 16)) return NVFP4MOE_ESHAPE;
   }
@@ -458,7 +539,18 @@ extern "C" int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x
   p.rms = kind == NVFP4MOE_NORM_RMS;
   p.want_dw = dw != nullptr;
   p.want_db = db != nullptr;
+  p.dw = dw;
+  p.db = db;
   const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(w, 16) && aligned(dx, 16);
+  if (T <= kNormFewRows) {
+    const int strips = dw || db ? (int)cdiv(D, 32) : 0;
+    bwd_by_length(p.D, vec, [&](auto shape) {
+      constexpr int NT = decltype(shape)::NT, NC = decltype(shape)::NC, W = decltype(shape)::W;
+      const int64_t rows = dx ? cdiv(T, bwd_threads<NT>() / NT) : 0;
+      norm_bwd_few_kernel<NT, NC, W><<<(unsigned)(strips + rows), bwd_threads<NT>(), 0, st>>>(p, strips);
+    });
+    return launch_status();
+  }
   int64_t blocks = kNormBwdBlocks;
   bwd_by_length(p.D, vec, [&](auto shape) {
     constexpr int NT = decltype(shape)::NT, NC = decltype(shape)::NC, W = decltype(shape)::W;

@@ -966,9 +966,11 @@ def layer_norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, dx=None, want_dx=True,
         lib = _lib.load()
         ws_bytes = 0
         if dw is not None or db is not None:
-            if workspace is None:
-                workspace = x.new_empty((lib.layer_norm_bwd_workspace_size(T, D),), dtype=torch.uint8)
-            ws_bytes = workspace.numel() * workspace.element_size()
+            if workspace is not None:
+                ws_bytes = workspace.numel() * workspace.element_size()
+            else:
+                ws_bytes = lib.layer_norm_bwd_workspace_size(T, D)
+                workspace = x.new_empty((ws_bytes,), dtype=torch.uint8) if ws_bytes else None
         rc = lib.layer_norm_bwd(_ptr(dy), _DT[dy.dtype], _ptr(x), _DT[x.dtype], T, D, _ptr(w), wdt, _ptr(mean),
                                 _ptr(rstd), kind, _ptr(dx), odt, _ptr(dw),
                                 _ptr(db), _ptr(workspace), ws_bytes, _stream())

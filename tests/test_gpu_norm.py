@@ -98,9 +98,13 @@ def _check_backward(dy, x, w, mean, rstd, kind, r, blocks, groups):
         tol = rn * (5 * U * (g + gm + h * (gh + egh)) + eg + h * egh + eh * (gh + egh)) * 1.01
         tol = tol + HALF[r["dx"].dtype] * (np.abs(want[0]) + tol) + 1e-37
         assert (np.abs(_f64(r["dx"]) - want[0]) <= tol).all(), float((np.abs(_f64(r["dx"]) - want[0]) / tol).max())
-    # a thread's rows, the groups of its workgroup, then at most 256 workgroups' sums: eight by a thread, and
-    # five steps across 32 lanes
-    chain = -(-T // (blocks * groups)) + groups + 8 + 5 + 1
+    if T <= 384:
+        # one launch: a thread's rows of a column (every 16th), then five steps across lanes at most
+        chain = -(-T // 16) + 5 + 1
+    else:
+        # a thread's rows, the groups of its workgroup, then at most 256 workgroups' sums: eight by a thread,
+        # and five steps across 32 lanes
+        chain = -(-T // (blocks * groups)) + groups + 8 + 5 + 1
     for got, ref, terms, e in ((r["dw"], want[1], dyn * h, (dyn * eh).sum(0)), (r["db"], want[2], dyn, 0)):
         if got is not None:
             assert got.dtype == F32
@@ -134,9 +138,10 @@ def test_backward_by_length(D):
 
 
 @pytest.mark.parametrize("T,D", [(1, 2048), (3, 256), (1023, 256), (1024, 2048), (1025, 512), (5000, 64), (333, 2557),
-                                 (257, 4096), (700, 5000), (300, 9001)])
+                                 (257, 4096), (700, 5000), (300, 9001), (384, 1000), (385, 1000), (600, 2557), (400, 16384),
+                                 (390, 9001), (2100, 8192), (3000, 2048), (513, 33), (2500, 1536)])
 def test_backward_by_rows(T, D):
-    """Fewer rows than workgroups, as many, more, and groups that go round."""
+    """Few rows in one launch and more in two: fewer than workgroups take, as many, and groups that go round."""
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
     x, rng = _data(T + D, T, D, BF16)
@@ -205,18 +210,19 @@ def test_rows_where_it_can_go_wrong():
 def test_parts_of_the_gradient_and_no_rows():
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
-    x, rng = _data(6, 50, 300, BF16)
-    dy = to_gpu(rng.standard_normal((50, 300)).astype(np.float32), F32)
-    w, b = _weights(rng, 300, 2, F32)
-    f = ops.layer_norm(x, w, b)
-    args = (dy, x, w, f["mean"], f["rstd"])
-    whole = ops.layer_norm_bwd(*args, want_db=True)
-    for kw, names in ((dict(want_dw=False), ["dx"]), (dict(want_dx=False), ["dw"]),
-                      (dict(want_dx=False, want_dw=False, want_db=True), ["db"])):
-        part = ops.layer_norm_bwd(*args, **kw)
-        assert [n for n in ("dx", "dw", "db") if part[n] is not None] == names
-        for n in names:
-            assert torch.equal(part[n], whole[n])
+    for T in (50, 500):
+        x, rng = _data(6, T, 300, BF16)
+        dy = to_gpu(rng.standard_normal((T, 300)).astype(np.float32), F32)
+        w, b = _weights(rng, 300, 2, F32)
+        f = ops.layer_norm(x, w, b)
+        args = (dy, x, w, f["mean"], f["rstd"])
+        whole = ops.layer_norm_bwd(*args, want_db=True)
+        for kw, names in ((dict(want_dw=False), ["dx"]), (dict(want_dx=False), ["dw"]),
+                          (dict(want_dx=False, want_dw=False, want_db=True), ["db"])):
+            part = ops.layer_norm_bwd(*args, **kw)
+            assert [n for n in ("dx", "dw", "db") if part[n] is not None] == names
+            for n in names:
+                assert torch.equal(part[n], whole[n])
     r = ops.layer_norm(x, w, b, want_stats=False)
     assert r["mean"] is None and r["rstd"] is None and torch.equal(r["y"], f["y"])
     e = x[:0]
@@ -230,7 +236,7 @@ def test_parts_of_the_gradient_and_no_rows():
 def test_outputs_stay_inside_their_tensors():
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
-    for T, D in ((5, 777), (9, 2048), (2, 5000)):
+    for T, D in ((5, 777), (9, 2048), (2, 5000), (400, 777), (401, 2048)):
         x, rng = _data(T, T, D, BF16)
         dy = to_gpu(rng.standard_normal((T, D)).astype(np.float32), BF16)
         w, b = _weights(rng, D, 2, F32)
@@ -244,10 +250,11 @@ def test_outputs_stay_inside_their_tensors():
             assert (t[-64:] == 3).all()
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("T", [300, 900])
+def test_streams_and_graphs(T):
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
-    T, D = 900, 2048
+    D = 2048
     x, rng = _data(8, T, D, BF16)
     dy = to_gpu(rng.standard_normal((T, D)).astype(np.float32), F32)
     w, b = _weights(rng, D, 2, F32)

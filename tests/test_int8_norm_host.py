@@ -38,15 +38,15 @@ def test_layer_norm(lib):
         (3, 0, -2), (3, 16385, -2), (0, FAKE + 1, -2), (9, FAKE + 1, -2), (4, FAKE + 2, -2), (11, FAKE + 2, -2),
         (12, FAKE + 1, -2)])
     size = lib.layer_norm_bwd_workspace_size
-    assert size(1, 64) == 2 * 64 * 4 and size(100000, 2048) == 2 * 256 * 2048 * 4
-    assert size(0, 64) == size(4, 0) == size(4, 16385) == 0
-    #      dy   dd  x   xd T  D   w   wd mean  rstd kind dx  od  dw    db    ws   bytes     stream
-    ok = [FAKE, 0, FAKE, 1, 4, 64, FAKE, 0, FAKE, FAKE, 0, FAKE, 0, FAKE, FAKE, FAKE, 1 << 20, None]
+    assert size(385, 64) == 2 * 256 * 64 * 4 and size(100000, 2048) == 2 * 256 * 2048 * 4
+    assert size(0, 64) == size(384, 64) == size(4000, 0) == size(4000, 16385) == 0  # (few rows need none)
+    #      dy   dd  x   xd T    D   w   wd mean  rstd kind dx  od  dw    db    ws   bytes     stream
+    ok = [FAKE, 0, FAKE, 1, 400, 64, FAKE, 0, FAKE, FAKE, 0, FAKE, 0, FAKE, FAKE, FAKE, 1 << 20, None]
     _refused(lib.layer_norm_bwd, ok, [
         (0, None, -1), (1, 2, -1), (2, None, -1), (3, 2, -1), (4, -1, -1), (7, 2, -1), (8, None, -1), (9, None, -1),
         (10, 2, -1), (12, 2, -1), ((11, 13, 14), (None, None, None), -1),
         (5, 0, -2), (5, 16385, -2), (0, FAKE + 2, -2), (11, FAKE + 2, -2), (13, FAKE + 2, -2), (15, FAKE + 8, -2),
-        (15, None, -5), (16, size(4, 64) - 1, -5)])
+        (15, None, -5), (16, size(400, 64) - 1, -5)])
 
 
 def test_int8_entry_points(lib):
