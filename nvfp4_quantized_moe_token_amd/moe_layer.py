@@ -341,7 +341,7 @@ def _kept(buf, keep):
     """What the gate+up product stores for ``backward``: (y1, h, q_y1, s_y1)."""
     if not keep:
         return None, None, None, None
-    if buf.q_y1 is not None:
+    if getattr(buf, "q_y1", None) is not None:
         return None, None, buf.q_y1, buf.s_y1
     return buf.y1, buf.h, None, None
 

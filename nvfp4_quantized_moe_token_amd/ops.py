@@ -601,6 +601,9 @@ def mx_quantize(x, elem=MX_E4M3, q=None, scales=None):
     rows, K = x.shape
     dev = x.device
     qcols = K // 2 if elem == MX_E2M1 else K
+    if elem == MX_INT8:
+        _need(q, "q", torch.uint8, rows, K)
+        _need(scales, "scales", torch.uint8, rows, K // 32)
     q = torch.empty((rows, qcols), dtype=torch.uint8, device=dev) if q is None else q
     scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=dev) if scales is None else scales
     rc = _lib.load().mx_quantize(_ptr(x), _DT[x.dtype], rows, K, elem, _ptr(q), _ptr(scales), _stream())
@@ -892,8 +895,8 @@ def silu_gate_bwd_mx(q_y1, s_y1, dh, dy1=None, h=None, want_h=True):
     _need(dy1, "dy1", torch.bfloat16, R, 2 * F)
     _need(h, "h", torch.bfloat16, R, F)
     with _on_device(dh, q_y1, s_y1, dy1, h):
-        dy1 = dh.new_empty((R, 2 * F)) if dy1 is None else dy1
-        h = dh.new_empty((R, F)) if h is None and want_h else h
+        dy1 = dh.new_empty(R, 2 * F) if dy1 is None else dy1
+        h = torch.empty_like(dh) if h is None and want_h else h
         rc = _lib.load().silu_gate_bwd_mx(_ptr(q_y1), _ptr(s_y1), _ptr(dh), R, F, _ptr(dy1), _ptr(h), _stream())
     _check("silu_gate_bwd_mx", rc)
     return dy1, h
@@ -926,11 +929,11 @@ def layer_norm(x, w=None, b=None, eps=1e-5, kind=NORM_LAYER, y=None, out_dtype=N
     _need(mean, "mean", torch.float32, T)
     _need(rstd, "rstd", torch.float32, T)
     with _on_device(x, w, b, y, mean, rstd):
-        y = x.new_empty((T, D), dtype=out_dtype) if y is None else y
+        y = torch.empty_like(x, dtype=out_dtype) if y is None else y
         if want_stats:
             if mean is None and kind == NORM_LAYER:
-                mean = x.new_empty((T,), dtype=torch.float32)
-            rstd = x.new_empty((T,), dtype=torch.float32) if rstd is None else rstd
+                mean = x.new_empty(T, dtype=torch.float32)
+            rstd = x.new_empty(T, dtype=torch.float32) if rstd is None else rstd
         rc = _lib.load().layer_norm(_ptr(x), _DT[x.dtype], T, D, _ptr(w), _ptr(b), wdt, eps, kind, _ptr(y), _dt_code(y),
                                     _ptr(mean), _ptr(rstd), _stream())
     _check("layer_norm", rc)
@@ -958,11 +961,11 @@ def layer_norm_bwd(dy, x, w, mean, rstd, kind=NORM_LAYER, dx=None, want_dx=True,
     _need(dw, "dw", f32, D)
     _need(db, "db", f32, D)
     with _on_device(x, dy, w, mean, rstd, dx, dw, db, workspace):
-        dx = x.new_empty((T, D), dtype=dx_dtype) if dx is None and want_dx else dx
+        dx = torch.empty_like(x, dtype=dx_dtype) if dx is None and want_dx else dx
         odt = F32 if dx is None else _dt_code(dx, "dx")
         if dw is None and (w is not None if want_dw is None else want_dw):
-            dw = x.new_empty((D,), dtype=f32)
-        db = x.new_empty((D,), dtype=f32) if db is None and want_db else db
+            dw = x.new_empty(D, dtype=f32)
+        db = x.new_empty(D, dtype=f32) if db is None and want_db else db
         lib = _lib.load()
         ws_bytes = 0
         if dw is not None or db is not None:

@@ -103,6 +103,7 @@ def launched(monkeypatch):
     monkeypatch.setattr(ops._lib, "load", lambda *a: Library())
     monkeypatch.setattr(ops, "_stream", lambda: None)
     monkeypatch.setattr(ops, "_on_device", lambda *ts: contextlib.nullcontext())
+    monkeypatch.setattr(ops, "_dev", lambda *ts: None)
     return calls
 
 
@@ -149,6 +150,8 @@ GEMM = dict(a_q=z(6, 64, dtype=I8), a_s=f(6), b_q=z(2, 256, 64, dtype=I8), b_s=f
     lambda: ops.grouped_gemm_int8_silu_gate(**GEMM, h=z(6, 256)),
     lambda: ops.grouped_gemm_int8_silu_gate(**GEMM, q_y1=z(6, 256, dtype=I8)),
     lambda: ops.grouped_gemm_int8_silu_gate(**GEMM, s_y1=z(6, 9, dtype=U8)),
+    lambda: ops.mx_quantize(z(4, 64), ops.MX_INT8, q=z(4, 32, dtype=U8)),          # a buffer of 4-bit codes
+    lambda: ops.mx_quantize(z(4, 64), ops.MX_INT8, scales=z(4, 1, dtype=U8)),
     lambda: ops.mx_dequantize(z(4, 64, dtype=I8), z(4, 2, dtype=U8), ops.MX_INT8),
     lambda: ops.mx_dequantize(z(4, 64, dtype=U8), z(4, 3, dtype=U8), ops.MX_INT8),
     lambda: ops.mx_dequantize(z(4, 64, dtype=U8), z(4, 2, dtype=U8), ops.MX_E2M1),
