@@ -10,28 +10,26 @@
 //
 // The kernel and its epilogues are in gemm_codes.hpp.
 //
-// Bounds and measurements (us of the kernel; 128 experts, top-8).  A 256x256
-// tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS per MFMA; by the counters
-// the LDS is then busy 81% as long as the MFMAs (gate+up of 8192 tokens; 107% in
-// the skewed product, its epilogue included), writes of the loads not counted.
-// 64x64 waves (128x256 and 256x128 tiles, or two workgroups per CU) read a third
-// more and lose more than finer tiles save: gate+up of 8192 tokens 209 against
-// 216 to 244.  Stages of 128 elements and a
-// ring of four are no faster either (155 against 138 for a dense 4096 x 8192 x
-// 8192 product, 4.0 PFLOP/s): lines are then read in halves.
-//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      210
-//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         243
-//   gate+up, 8192 tokens, H quantized and nothing else stored      181
-//   the same with Y1 and H stored too (the learner's form)         235
-//   the skewed product with fp32 output (266 of bytes)             328
-//   gate+up, 512 tokens    51 (4.2 TB/s)     down, 512 tokens       30
+// Bounds and measurements (us of the kernel, several sets of inputs in turn; 128
+// experts, top-8).  A 256x256 tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS
+// per MFMA.  64x64 waves (128x256 and 256x128 tiles, or two workgroups per CU)
+// read a third more and lose more than finer tiles save: gate+up of 8192 tokens
+// 209 against 216 to 244.  Stages of 128 elements and a ring of four are no faster
+// either (155 against 138 for a dense 4096 x 8192 x 8192 product, 4.0 PFLOP/s):
+// lines are then read in halves.
+//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      212
+//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         225
+//   gate+up, 8192 tokens, H quantized and nothing else stored      175
+//   the same with Y1 and H stored too                              229
+//   the same with Y1 in 8 bits instead (the learner's checkpoint)  207
+//   the skewed product with fp32 output (266 of bytes)             331
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts (140 MB)
-//                                                     28 to 33 (4.3 to 4.9 TB/s)
-// In copies without their stores the first two take 170 and 161, without any
-// epilogue 129 and 117, where the MFMAs alone need 52 and 47: a workgroup's
-// stores and SiLU are not hidden behind its products, since its accumulators
-// fill the registers and its stages the LDS; the loop itself is held up by its
-// LDS reads and by row padding (a fifth of gate+up's MFMAs).
+//                                                     28 to 35 (4.0 to 4.9 TB/s)
+// Without any epilogue the first two take 129 and 117, where the MFMAs alone need
+// 52 and 47: a workgroup's stores and SiLU are not hidden behind its products,
+// since its accumulators fill the registers and its stages the LDS; the loop
+// itself is held up by its operands' way to LDS and by row padding (a fifth of
+// gate+up's MFMAs).
 #include "gemm_codes.hpp"
 
 namespace nvfp4moe {
@@ -42,22 +40,24 @@ namespace {
 // three stages deep; with many it is the MFMAs, the LDS reads that feed them
 // and the stores.  The row block is one that most experts' rows fit in, up to
 // 256, where blocks of 192 need two.  Measured kernel times in us, 128 experts,
-// gate+up (768 features, K = 2048) and down (N = 2048, K = 768):
+// random routing, gate+up with Y1 and H stored (768 features, K = 2048) and down
+// (N = 2048, K = 768):
 //   rows      gate+up, blocks of           down, blocks of
 //             32     64    192    256      32     64    192    256
-//    16     45.4   48.8          67.5
-//    32     56.1   51.0          68.8    30.3   30.2          41.0
-//    64     74.6   64.9   67.2   71.9    41.5   35.6   38.4   42.0
-//    80            72.5   69.2   73.9           43.3   39.9   43.4
-//    96     96.9   75.2   72.1   76.6    54.2   44.1   40.6   44.5
-//   128    119.7   91.6   75.8   79.5    67.8   53.2   43.2   46.3
-//   160                   79.9   85.5                  47.3   49.3
-//   208                  118.7   96.1                  67.9   55.6
+//    16     37.6   40.7   50.6   61.2    22.9   25.0   31.6   34.8
+//    32     44.0   42.5   51.7   60.6    25.4   25.9   31.6   35.3
+//    64     59.7   56.1   56.9   65.9    35.4   32.3   36.1   39.0
+//    80     71.0   63.7   59.9   68.0    40.6   38.2   36.6   39.7
+//    96     89.6   68.0   64.9   71.3    43.0   37.6   38.0   41.5
+//   128    112.5   88.1   75.5   79.2    52.8   44.1   40.6   44.8
+//   160    130.1   97.8   94.0   85.0    63.0   52.2   46.8   46.2
+//   208    162.1  123.9  116.9   92.3    80.3   62.4   64.1   48.8
+//   512    354.1  268.9  210.0  210.1   220.4  176.0  126.2  125.3
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
   if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 176 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  if (p.M <= 144 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
   return launch_tiles<MXFP4, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 

