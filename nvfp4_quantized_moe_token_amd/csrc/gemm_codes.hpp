@@ -18,12 +18,12 @@
 // time), tiles in contiguous ranges per XCD with the row blocks of an expert
 // next to each other.
 //
-// Epilogues.  The tile leaves in pieces of 64 bytes per row, put together by
-// exchanges between the lanes of a wave (through LDS the int8 gate+up with Y1 in
-// 8 bits took 14 us more).  SiLU gate: tiles hold matching gate and up columns; Y1 is rounded to bf16 and
-// H = silu(G) * U is taken from the rounded values, as the standalone kernel
-// does; optionally H is quantized to MXFP4 on the way out, or the rounded Y1
-// to MXINT8, the form in which the backward pass takes it back.
+// Epilogues.  The tile leaves in pieces of 64 or 128 bytes per row, put together
+// by exchanges between the lanes of a wave (through LDS the int8 gate+up with Y1
+// in 8 bits took 14 us more).  SiLU gate: tiles hold matching gate and up columns;
+// Y1 is rounded to bf16 and H = silu(G) * U is taken from the rounded values, as
+// the standalone kernel does; optionally H is quantized to MXFP4 on the way out,
+// or the rounded Y1 to MXINT8, the form in which the backward pass takes it back.
 #pragma once
 
 #include "gemm_tiles.hpp"
@@ -144,21 +144,38 @@ __device__ __forceinline__ uint32_t max_of_halves(uint32_t v) {
   const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return max(r[0], r[1]);
 }
-// A block's bf16 words, columns 8 g + 4 (l / 32) + 0..3 of row l % 32 in words
-// 2 g, 2 g + 1: afterwards words 0..3 hold columns 8 (l / 32) + 0..7, words 4..7
-// those 16 further.
-__device__ __forceinline__ void pair_up(uint32_t (&w)[8]) {
-#pragma unroll
-  for (int q = 0; q < 8; q += 4) {
-    swap_halves(w[q], w[q + 2]);
-    swap_halves(w[q + 1], w[q + 3]);
-  }
+// Row of an operand block of 32 that its LDS row m holds (B's): the rows go in
+// such an order that a lane's elements of a block's tile, MFMA columns 8 g +
+// 4 (l / 32) + 0..3 for g = 0..3, are the columns 16 (l / 32) + 0..15.
+__device__ __forceinline__ int column(int m) { return (m & ~31) | (m & 3) | ((m & 24) >> 1) | ((m & 4) << 2); }
+// Exchange between neighbouring lanes (rows l and l ^ 1): afterwards a holds the
+// even lane's row and b the odd one's, in each an even lane what was in its a, an
+// odd lane what was in b.
+// (Written out because the compiler keeps each move apart from its selection, twice
+// the instructions.  The waits are those between a register's write and its read by
+// another lane, before and behind.)
+__device__ __forceinline__ void turn(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {  // (a, b) and (c, d)
+  uint32_t t, u;
+  asm("s_mov_b32 vcc_lo, 0xAAAAAAAA\n\t"
+      "s_mov_b32 vcc_hi, 0xAAAAAAAA\n\t"
+      "v_cndmask_b32_dpp %0, %2, %4, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %1, %3, %5, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_not_b64 vcc, vcc\n\t"
+      "v_cndmask_b32_dpp %2, %4, %2, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %3, %5, %3, vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1"
+      : "=&v"(t), "=&v"(u), "+v"(a), "+v"(c)
+      : "v"(b), "v"(d)
+      : "vcc", "scc");
+  b = t;
+  d = u;
 }
-// Then words 0..3 hold 16 bytes of row l % 16, unit 2 ((l / 16) % 2) + l / 32 of
-// 64 bytes, and words 4..7 the same of the row 16 further.
-__device__ __forceinline__ void merge(uint32_t (&w)[8]) {
+// A block's words, 32 bytes of a row per lane: afterwards words 0..3 are 16
+// bytes of row l % 32 without its bit 0, unit 2 (l / 32) + l % 2 of 64 bytes, and
+// words 4..7 those of the next row.
+__device__ __forceinline__ void turn8(uint32_t (&w)[8]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) swap_quarters(w[k], w[k + 4]);
+  for (int k = 0; k < 4; k += 2) turn(w[k], w[k + 4], w[k + 1], w[k + 5]);
 }
 // A 16-byte store at one register offset.  With part of the offset in a scalar
 // register the compiler takes the data registers as free at once and may write
@@ -167,16 +184,12 @@ __device__ __forceinline__ void merge(uint32_t (&w)[8]) {
 __device__ __forceinline__ void store16(i32x4_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
   __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
 }
-// Two such quadruples, a of 64 bytes of rows and b of the next 64: afterwards a
-// holds 16 bytes of row l % 8, unit 4 ((l / 8) % 2) + 2 ((l / 16) % 2) + l / 32 of
-// 128 bytes, and b the same of the row 8 further.
-__device__ __forceinline__ void join(uint32_t* a, uint32_t* b) {
+// Of two such quadruples side by side, a of 64 bytes of rows and b of the next 64:
+// afterwards a holds row l % 16 without bit 0, unit 4 ((l / 16) % 2) + 2 (l / 32) +
+// l % 2 of 128 bytes, and b the same of the row 16 further.
+__device__ __forceinline__ void line(uint32_t* a, uint32_t* b) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int x = (int)a[k], y = (int)b[k];
-    a[k] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xF, 0xC, false);  // lanes 8..15 of 16: b's 0..7
-    b[k] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xF, 0x3, false);  // lanes 0..7: a's 8..15
-  }
+  for (int k = 0; k < 4; ++k) swap_quarters(a[k], b[k]);
 }
 __device__ __forceinline__ i32x4_t four(const uint32_t* w) { return (i32x4_t){(int)w[0], (int)w[1], (int)w[2], (int)w[3]}; }
 
@@ -310,7 +323,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
   const uint32_t rowb = (uint32_t)(FMT == INT8 ? p.K : p.K / 2), srow = FMT == INT8 ? 4u : (uint32_t)(p.K / 32);
   const int lrow = wid * 8 + lane / 8, lunit = (lane & 7) ^ swz(lrow);
   const uint32_t la0 = (uint32_t)lrow * rowb + lunit * 16;
-  const uint32_t lb0 = (uint32_t)(SILU ? gate_up_row(lrow, F, 0) : lrow) * rowb + lunit * 16;
+  const uint32_t lb0 = (uint32_t)(SILU ? gate_up_row(column(lrow), F, 0) : column(lrow)) * rowb + lunit * 16;
   uint32_t ls0[SC_INSTR];
 #pragma unroll
   for (int x = 0; x < SC_INSTR; ++x) {
@@ -319,7 +332,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     const bool is_a = idx * ROWS < SA;
     const int row = (is_a ? idx * ROWS : idx * ROWS - SA) + lane * (16 / SROW);
     const bool real = idx < SC_LOADS && (!is_a || row < BM);
-    ls0[x] = real ? (uint32_t)(SILU && !is_a ? gate_up_row(row, F, 0) : row) * srow : kOOB;
+    ls0[x] = real ? (uint32_t)(is_a ? row : SILU ? gate_up_row(column(row), F, 0) : column(row)) * srow : kOOB;
   }
   constexpr int KS = FMT == INT8 ? kRowB : 2 * kRowB;       // reduction elements per stage
   const int nk = p.K > 0 ? (int)((p.K + KS - 1) / KS) : 1;  // (K == 0: one stage of zeros)
@@ -536,22 +549,25 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     nst = 0;
 
     // Epilogue.  The B fragment is the MFMA's first operand, so lane l holds
-    // output row l % 32 and, for g = 0..3, the four consecutive columns
-    // 8 g + 4 (l / 32) + 0..3 in registers 4g..4g+3.  Halves and quarters of the
-    // wave exchange registers until a lane has 16 consecutive bytes of a row and
-    // eight lanes a whole line, where two blocks of the wave lie side by side
-    // (the skewed product's 537 MB of stores cost 20 us less than as half
-    // lines), else four lanes half a line.  Rows past the expert's end are past
-    // the store's region.
+    // output row l % 32 and, by the order of B's rows in LDS, 16 consecutive
+    // columns of each block.  Neighbouring lanes exchange registers until a store
+    // writes 64 bytes of 16 rows, pairs of units in pairs of lanes: with units in
+    // higher lane bits alone a quad of lanes touches four rows, and a CU's stores
+    // to the L2 take half as long again (31 against 20 us for eight 128 KiB tiles on
+    // every CU; to HBM 38.5 against 37).  Where nothing but C leaves, quarters of
+    // the wave exchange too and a store writes whole lines (skewed product 212
+    // against 224 us).  Rows past the expert's end are past the store's region.
     settle();
-    const int hh = lane >> 5;
-    const int r16 = lane & 15, u4 = ((lane >> 4) & 1) * 2 + hh;  // row and 16-byte unit after merge()
-    const int r8 = lane & 7, u8 = ((lane >> 3) & 1) * 4 + u4;    // and after join()
+    int ln = lane;
+    asm volatile("" : "+v"(ln));  // (what follows from it is not kept from tile to tile: registers)
+    const int hh = ln >> 5;
+    const int r2 = ln & 30, u4 = 2 * hh + (ln & 1);         // row and 16-byte unit after turn8()
+    const int r4 = ln & 14, u8 = ((ln >> 4) & 1) * 4 + u4;  // and after line()
     const uint32_t tile_rows = (uint32_t)(cur.w - cur.z);
     // The integers' scales of this lane's row of row block i, and of its columns
     // 8 g + 4 hh + 0..3 of column block j.
     auto row_scale = [&](int i) __attribute__((always_inline)) {
-      if constexpr (FMT == INT8) return *(lds_f32_t*)(uintptr_t)(scales + so + (wm * WTM + i * 32 + (lane & 31)) * 4);
+      if constexpr (FMT == INT8) return *(lds_f32_t*)(uintptr_t)(scales + so + (wm * WTM + i * 32 + (ln & 31)) * 4);
       else return 0.0f;
     };
     auto col_scales = [&](int j, int g) __attribute__((always_inline)) {
@@ -567,26 +583,19 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       const uint32_t kqb = (uint32_t)p.N, keb = (uint32_t)p.N / 32;  // row bytes of Y1's codes and scales
       const __amdgpu_buffer_rsrc_t rkq = region(p.yq + m0 * kqb, tile_rows * kqb), rke = region(p.ys + m0 * keb, tile_rows * keb);
       constexpr int P = FN >= 4 ? 2 : 1;  // pairs of a gate and an up block that leave together
-      const uint32_t lr = lane & 31;      // codes and scales of one pair leave with a row per two lanes
-      const uint32_t vq = lr * qb + hh * 8, ve = hh == 0 ? lr * eb : kOOB;
-      const uint32_t vkq = P == 2 ? r16 * kqb + u4 * 16 : lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
+      const uint32_t lr = ln & 31;      // codes and scales of one pair leave with a row per two lanes
+      const uint32_t vq = lr * qb + hh * (P == 2 ? 16 : 8), ve = P == 2 ? lr * eb + hh : hh == 0 ? lr * eb : kOOB;
+      const uint32_t vkq = P == 2 ? r2 * kqb + ((ln & 1) * 2 + hh) * 16 : lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
       const bool want_q = EPI == EPI_SILU_Q || (EPI == EPI_SILU_C && FMT == MXFP4 && p.hq);
       // Stores P blocks of 32 columns (paired up) at `at` of the region's rows.
       auto leave = [&](uint32_t (&w)[P][8], __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t rb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < P; ++q) merge(w[q]);
-        if constexpr (P == 2) {
-          at += r8 * rb + u8 * 16;
+        for (int q = 0; q < P; ++q) turn8(w[q]);
+        at += r2 * rb + u4 * 16;
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            join(w[0] + 4 * part, w[1] + 4 * part);
-            store16(four(w[0] + 4 * part), r, at + part * 16 * rb);
-            store16(four(w[1] + 4 * part), r, at + (part * 16 + 8) * rb);
-          }
-        } else {
-          at += r16 * rb + u4 * 16;
-          store16(four(w[0]), r, at);
-          store16(four(w[0] + 4), r, at + 16 * rb);
+        for (int q = 0; q < P; ++q) {
+          store16(four(w[q]), r, at + 64 * q);
+          store16(four(w[q] + 4), r, at + rb + 64 * q);
         }
       };
 #pragma unroll
@@ -635,17 +644,13 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
                   const float v[4] = {bf16_lo(y[2 * g]), bf16_hi(y[2 * g]), bf16_lo(y[2 * g + 1]), bf16_hi(y[2 * g + 1])};
                   d[q][g] = encode4_int8<true>(v, e);
                 }
-                swap_halves(d[q][0], d[q][1]);  // 8 columns
-                swap_halves(d[q][2], d[q][3]);
-                swap_halves(d[q][0], d[q][2]);  // 16 columns
-                swap_halves(d[q][1], d[q][3]);
               }
-              if constexpr (P == 2) {  // 64 columns of 16 rows
+              if constexpr (P == 2) {  // 64 columns of every other row
 #pragma unroll
-                for (int k = 0; k < 4; ++k) swap_quarters(d[0][k], d[1][k]);
+                for (int k = 0; k < 4; k += 2) turn(d[0][k], d[1][k], d[0][k + 1], d[1][k + 1]);
               }
 #pragma unroll
-              for (int q = 0; q < P; ++q) store16(four(d[q]), rkq, vkq + (row + 16 * q) * kqb + t * (uint32_t)F + f);
+              for (int q = 0; q < P; ++q) store16(four(d[q]), rkq, vkq + (row + q) * kqb + t * (uint32_t)F + f);
               anew(t ? uv : gv);
               __builtin_amdgcn_sched_barrier(0);  // registers
             }
@@ -660,26 +665,21 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
               hv[q][w] = pack_bf16x2(silu_gate(bf16_lo(gv[q][w]), bf16_lo(uv[q][w])), silu_gate(bf16_hi(gv[q][w]), bf16_hi(uv[q][w])));
           if (Yp) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              uint32_t(&y)[P][8] = t ? uv : gv;
-#pragma unroll
-              for (int q = 0; q < P; ++q) pair_up(y[q]);
-              leave(y, ry, row * yb + (t * (uint32_t)F + f) * 2, yb);
-            }
+            for (int t = 0; t < 2; ++t) leave(t ? uv : gv, ry, row * yb + (t * (uint32_t)F + f) * 2, yb);
           }
+          if (p.amax || want_q) {
+            uint32_t d[P][2];
+            int se[P];
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            if (p.amax || want_q) {
+            for (int q = 0; q < P; ++q) {
               // (rows past the end hold 0 or NaN, which the maximum passes over)
               float am = 0.0f;
 #pragma unroll
               for (int w = 0; w < 8; ++w) am = fmaxf(am, fmaxf(fabsf(bf16_lo(hv[q][w])), fabsf(bf16_hi(hv[q][w]))));
               tile_amax = fmaxf(tile_amax, am);
-              pair_up(hv[q]);
               if (want_q) {
                 // the two halves hold the 32 features of one block of one row
-                const int se = shared_exp<2>(__uint_as_float(max_of_halves(__float_as_uint(am))));
-                uint32_t d[2];
+                se[q] = shared_exp<2>(__uint_as_float(max_of_halves(__float_as_uint(am))));
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   float v[8];
@@ -688,18 +688,25 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
                     v[2 * w] = bf16_lo(hv[q][4 * t + w]);
                     v[2 * w + 1] = bf16_hi(hv[q][4 * t + w]);
                   }
-                  d[t] = encode8_e2m1(v, se);
+                  d[q][t] = encode8_e2m1(v, se[q]);
                 }
-                swap_halves(d[0], d[1]);
-                __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){d[0], d[1]}, rq, vq, row * qb + f / 2 + 16 * q, 0);
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se + 127), re, ve, row * eb + f / 32 + q, 0);
               }
-            } else {
-              pair_up(hv[q]);
+            }
+            if (want_q) {
+              const uint32_t at = row * qb + f / 2, es = row * eb + f / 32;
+              if constexpr (P == 2) {  // a block per half of the wave
+                swap_halves(d[0][0], d[1][0]);
+                swap_halves(d[0][1], d[1][1]);
+                store16((i32x4_t){(int)d[0][0], (int)d[0][1], (int)d[1][0], (int)d[1][1]}, rq, vq + at);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)((hh ? se[1] : se[0]) + 127), re, ve + es, 0, 0);
+              } else {
+                __builtin_amdgcn_raw_buffer_store_b64((u32x2_t){d[0][0], d[0][1]}, rq, vq, at, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(se[0] + 127), re, ve, es, 0);
+              }
             }
           }
           if (Hp) leave(hv, rh, row * hb + f * 2, hb);
-          nst += P * ((Yp ? 4 : 0) + (Hp ? 2 : 0) + (want_q ? 2 : 0)) + (EPI == EPI_SILU_C ? 2 * P + 1 : 0);
+          nst += P * ((Yp ? 4 : 0) + (Hp ? 2 : 0)) + (want_q ? 2 : 0) + (EPI == EPI_SILU_C ? 2 * P + 1 : 0);
           __builtin_amdgcn_sched_barrier(0);  // P pairs at a time: registers
         }
       }
@@ -707,37 +714,38 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       constexpr uint32_t EB = OUT32 ? 4 : 2;  // bytes per element
       const uint32_t cb = (uint32_t)p.N * EB;
       const __amdgpu_buffer_rsrc_t rc = region(reinterpret_cast<uint8_t*>(p.c) + m0 * cb, tile_rows * cb);
-      const uint32_t vc = r8 * cb + u8 * 16;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float rs = row_scale(i);
         const uint32_t row = wm * WTM + i * 32;
         if constexpr (OUT32) {
+          // after line() lane bit 4 is unit bit 1 and lane / 32 unit bit 2
+          const uint32_t vo = r4 * cb + (4 * hh + 2 * ((ln >> 4) & 1) + (ln & 1)) * 16;
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
             const uint32_t col = (uint32_t)n0 + wn * WTN + j * 32;
             if (col >= (uint32_t)p.N) continue;  // (N % 32 == 0)
-            uint32_t w[2][8];  // 16 columns each
+            uint32_t w[2][8];  // units 0 and 2, 1 and 3 of this lane's 64 bytes
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int g = 0; g < 4; ++g) {
+              const f32x4_t e = elements<FMT>(acc[i][j], g, rs, col_scales(j, g));
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const f32x4_t e = elements<FMT>(acc[i][j], 2 * q + g, rs, col_scales(j, 2 * q + g));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[q][4 * g + k] = __float_as_uint(e[k]);
-              }
-              merge(w[q]);
+              for (int k = 0; k < 4; ++k) w[g >> 1][(g & 1) * 4 + k] = __float_as_uint(e[k]);
             }
+            // unit 4 h + g of 128 bytes: bit 0 to lane bit 0, bit 1 to lane bit 4
 #pragma unroll
-            for (int part = 0; part < 4; part += 2) {
-              join(w[0] + 2 * part, w[1] + 2 * part);
-              store16(four(w[0] + 2 * part), rc, vc + (row + part * 8) * cb + col * EB);
-              store16(four(w[1] + 2 * part), rc, vc + (row + part * 8 + 8) * cb + col * EB);
+            for (int q = 0; q < 2; ++q) turn8(w[q]);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              line(w[0] + 4 * part, w[1] + 4 * part);
+              store16(four(w[0] + 4 * part), rc, vo + (row + part) * cb + col * EB);
+              store16(four(w[1] + 4 * part), rc, vo + (row + part + 16) * cb + col * EB);
             }
             nst += 4;
             __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
           }
         } else {
+          const uint32_t vc = r4 * cb + u8 * 16;
 #pragma unroll
           for (int j = 0; j < FN; j += 2) {
             const uint32_t col = (uint32_t)n0 + wn * WTN + j * 32;
@@ -747,16 +755,15 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
               for (int g = 0; g < 4; ++g) bf16x4(elements<FMT>(acc[i][j + t], g, rs, col_scales(j + t, g)), w[t] + 2 * g);
-              pair_up(w[t]);
-              merge(w[t]);
+              turn8(w[t]);
             }
             // (N may end between the two blocks: units 4..7 are then dropped)
             const uint32_t at = (u8 < 4 || col + 32 < (uint32_t)p.N ? vc : kOOB) + row * cb + col * EB;
 #pragma unroll
-            for (int part = 0; part < 4; part += 2) {
-              join(w[0] + 2 * part, w[1] + 2 * part);
-              store16(four(w[0] + 2 * part), rc, at + part * 8 * cb);
-              store16(four(w[1] + 2 * part), rc, at + (part * 8 + 8) * cb);
+            for (int part = 0; part < 2; ++part) {
+              line(w[0] + 4 * part, w[1] + 4 * part);
+              store16(four(w[0] + 4 * part), rc, at + part * cb);
+              store16(four(w[1] + 4 * part), rc, at + (part + 16) * cb);
             }
             nst += 4;
             __builtin_amdgcn_sched_barrier(0);  // two blocks at a time: registers
