@@ -23,10 +23,11 @@
 //
 // Bounds and measurements (us).  HBM: 16384 x 2048 bf16 forward 27 to 28 (134 MB at
 // 4.8 TB/s, other inputs each time; 20 of the same), gradient of 8192 x 2048 (bf16
-// rows, fp32 dy) 34 and 4 for the sums of 256 workgroups (10 when each thread of
-// 256 added 32 of them one after another); without the next row in flight and with
-// four waves a workgroup 30 against 25 of the same inputs; a wave for rows of 2048
-// with twice the columns a lane 49.  16 rows of 2048: 3.5.
+// rows, fp32 dy) 28 and 4 for the sums of 256 workgroups (10 when each thread of
+// 256 added 32 of them one after another); of the same inputs together 27, 31 when
+// the next row's loads branch on its type (each branch then waits for the other's),
+// 29 with two rows in flight; a wave for rows of 2048 with twice the columns a lane
+// 49.  16 rows of 2048: 3.5.
 #include <type_traits>
 
 #include "common.hpp"
@@ -103,6 +104,55 @@ __device__ __forceinline__ void load_row(const void* base, bool bf16, int64_t at
         v[c] = col < D ? p[col] : 0.0f;
       }
     }
+  }
+}
+
+// The same as they are stored, by buffer loads of `row`, a region of D elements
+// or of none: no branch, so that nothing waits for them before values().
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_region(const void* base, bool bf16, int64_t at, int n, bool live) {
+  const int size = bf16 ? 2 : 4;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(base)) + at * size, (short)0,
+                                           live ? n * size : 0, kRawBufferWord3);
+}
+template <int NT, int NC, int W>
+__device__ __forceinline__ void load_raw(__amdgpu_buffer_rsrc_t row, bool bf16, int t, uint32_t (&v)[NC * W]) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const uint32_t col = (c * NT + t) * W;
+    if constexpr (W == 8) {
+      const uint32_t off = col * (bf16 ? 2 : 4);
+      const u32x4_t a = __builtin_amdgcn_raw_buffer_load_b128(row, off, 0, 0);
+      const u32x4_t b = __builtin_amdgcn_raw_buffer_load_b128(row, bf16 ? kOOB : off + 16, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[c * 8 + i] = a[i];
+        v[c * 8 + 4 + i] = b[i];
+      }
+    } else {
+      if (bf16) v[c] = __builtin_amdgcn_raw_buffer_load_b16(row, col * 2, 0, 0);
+      else v[c] = __builtin_amdgcn_raw_buffer_load_b32(row, col * 4, 0, 0);
+    }
+  }
+}
+template <int NC, int W>
+__device__ __forceinline__ void values(const uint32_t (&raw)[NC * W], bool bf16, float (&v)[NC * W]) {
+  if (bf16) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (W == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[c * W + 2 * i] = bf16_lo(raw[c * W + i]);
+          v[c * W + 2 * i + 1] = bf16_hi(raw[c * W + i]);
+        }
+      } else {
+        v[c] = bf16_lo(raw[c]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC * W; ++i) v[i] = __uint_as_float(raw[i]);
   }
 }
 
@@ -238,25 +288,36 @@ __global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_kernel(NormParams 
   }
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * GROUPS;
-  int64_t row = (int64_t)blockIdx.x * GROUPS + threadIdx.x / NT;
-  float h[N], dy[N], r = 0.0f, m = 0.0f;
-  const auto load = [&](int64_t at, float(&x)[N], float(&d)[N], float& rr, float& mm) __attribute__((always_inline)) {
-    load_row<NT, NC, W>(p.x, p.x_bf16, at * D, D, t, x);
-    load_row<NT, NC, W>(p.dy, p.dy_bf16, at * D, D, t, d);
-    rr = p.rstd_in[at];
-    mm = p.rms ? 0.0f : p.mean_in[at];
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+  uint32_t nx[AHEAD ? N : 1], ndy[AHEAD ? N : 1];  // the next row as stored
+  float nr = 0.0f, nm = 0.0f;
+  const auto next = [&](int64_t at) __attribute__((always_inline)) {
+    const bool live = at < p.T;
+    if constexpr (AHEAD) {
+      load_raw<NT, NC, W>(row_region(p.x, p.x_bf16, at * D, D, live), p.x_bf16, t, nx);
+      load_raw<NT, NC, W>(row_region(p.dy, p.dy_bf16, at * D, D, live), p.dy_bf16, t, ndy);
+      nr = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row_region(p.rstd_in, false, at, 1, live), 0, 0, 0));
+      nm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(row_region(p.mean_in, false, at, 1, live && !p.rms), 0, 0, 0));
+    }
   };
   // (The groups of a workgroup that share a barrier per row go round together,
   // the last ones perhaps without a row.)
   const bool together = NT > 64;
-  if (AHEAD && row < p.T) load(row, h, dy, r, m);
-  for (; together ? row - threadIdx.x / NT < p.T : row < p.T; row += step) {
+  next(row);
+  for (; together ? row - group < p.T : row < p.T; row += step) {
     const bool live = row < p.T;
-    float nh[N], nd[N], nr = 0.0f, nm = 0.0f;
+    float h[N], dy[N], r = 0.0f, m = 0.0f;
     if constexpr (AHEAD) {
-      if (row + step < p.T) load(row + step, nh, nd, nr, nm);
+      values<NC, W>(nx, p.x_bf16, h);
+      values<NC, W>(ndy, p.dy_bf16, dy);
+      r = nr;
+      m = nm;
     } else if (live) {
-      load(row, h, dy, r, m);
+      load_row<NT, NC, W>(p.x, p.x_bf16, row * D, D, t, h);
+      load_row<NT, NC, W>(p.dy, p.dy_bf16, row * D, D, t, dy);
+      r = p.rstd_in[row];
+      m = p.rms ? 0.0f : p.mean_in[row];
     }
     float s[2] = {0.0f, 0.0f};
     if (live) {
@@ -272,6 +333,7 @@ __global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_kernel(NormParams 
           s[1] += dy[i];
         }
     }
+    next(row + step);
     if (p.out) {
       row_sums<NT, 2, GROUPS>(s, turn);
       const float gh = s[0] * inv_d, g = p.rms ? 0.0f : s[1] * inv_d;
@@ -280,15 +342,6 @@ __global__ __launch_bounds__(bwd_threads<NT>()) void norm_bwd_kernel(NormParams 
         for (int i = 0; i < N; ++i) h[i] = r * (dy[i] - g - h[i] * gh);
         store_row<NT, NC, W>(p.out, p.out_bf16, row * D, D, t, h);
       }
-    }
-    if constexpr (AHEAD) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        h[i] = nh[i];
-        dy[i] = nd[i];
-      }
-      r = nr;
-      m = nm;
     }
   }
   // This workgroup's sums.
