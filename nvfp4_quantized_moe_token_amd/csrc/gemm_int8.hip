@@ -11,11 +11,11 @@
 //
 // Bounds and measurements (us of the kernel, several sets of inputs in turn; 128
 // experts, top-8).
-//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      290 (1.4 PFLOP/s)
-//   the same, H stored alone                                       276
-//   the same, H and Y1 in 8 bits                                   303
-//   down, 8192 tokens (N = 2048, K = 768)                          180
-//   down, 16384 tokens, skewed routing                             315 (1.3 PFLOP/s)
+//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      287 (1.4 PFLOP/s)
+//   the same, H stored alone                                       272
+//   the same, H and Y1 in 8 bits                                   296
+//   down, 8192 tokens (N = 2048, K = 768)                          175
+//   down, 16384 tokens, skewed routing                             308 (1.3 PFLOP/s)
 //   dense, 4096 x 8192 x 8192                                      228 (2.4 PFLOP/s)
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts
 //                                  (264 MB of weights)             46 to 50 (5.3 to 5.8 TB/s)
@@ -24,16 +24,18 @@
 // (35 and 28 us when taken away singly); torch's integer product of 8192 x 8192 x
 // 8192 reaches 2.5 PFLOP/s.  Gate+up: 224 without an epilogue, 185 without MFMAs
 // (the operands' way from HBM: 128-byte pieces of 2 KiB rows, 614 MB at 3.3 TB/s
-// by the L2's misses), 150 with MFMAs and barriers alone, a quarter of them row
-// padding; the epilogue's arithmetic (scales, SiLU, rounding: 20 each for SiLU and
-// for the 8-bit codes) and stores come on top, as a workgroup fills a CU's
-// registers and LDS.  Measured instead and not kept: four waves of 128x128 (dense
-// 236, skewed 386); two workgroups per CU of 128x128 (309, 367) or of 128x256 with
-// 64-byte stages (281, 369); rings of three and four 64-byte stages (no change);
-// loads that bring lines of later stages to the L2 (20 more); leaving out waves
-// without rows (no change); accumulators in vector registers (no change, 16 tokens
-// 3 us slower); half of a tile's stores held in registers until the next tile's
-// first stages (no change); staggered starts (no change).
+// by the L2's misses), 178 without loads, 150 with MFMAs and barriers alone (119
+// of MFMAs, a quarter of them row padding: while they run, the fragments read and
+// the stages written take all of the LDS's 128 bytes a cycle, 96 and 32); the
+// epilogue's arithmetic (scales, SiLU, rounding: 20 each for SiLU and for the
+// 8-bit codes) and stores come on top, as a workgroup fills a CU's registers and
+// LDS.  Measured instead and not kept: four waves of 128x128 (dense 236, skewed
+// 386); two workgroups per CU of 128x128 (309, 367) or of 128x256 with 64-byte
+// stages (281, 369); rings of three and four 64-byte stages (no change); loads
+// that bring lines of later stages to the L2 (20 more); leaving out waves without
+// rows (no change); accumulators in vector registers (no change, 16 tokens 3 us
+// slower); half of a tile's stores held in registers until the next tile's first
+// stages (no change); staggered starts (no change).
 #include "gemm_codes.hpp"
 
 namespace nvfp4moe {

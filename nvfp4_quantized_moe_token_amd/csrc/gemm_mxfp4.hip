@@ -14,17 +14,17 @@
 // experts, top-8).  A 256x256 tile of 8 waves, 64x128 each, reads 0.75 KiB of LDS
 // per MFMA.  64x64 waves (128x256 and 256x128 tiles, or two workgroups per CU)
 // read a third more and lose more than finer tiles save: gate+up of 8192 tokens
-// 209 against 216 to 244.  Stages of 128 elements and a ring of four are no faster
-// either (155 against 138 for a dense 4096 x 8192 x 8192 product, 4.0 PFLOP/s):
-// lines are then read in halves.
-//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      212
-//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         225
-//   gate+up, 8192 tokens, H quantized and nothing else stored      175
-//   the same with Y1 and H stored too                              229
+// 209 (198 by now) against 216 to 244.  Stages of 128 elements and a ring of four
+// are no faster either (155 against 138 for a dense 4096 x 8192 x 8192 product,
+// 4.0 PFLOP/s): lines are then read in halves.
+//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      198
+//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         211
+//   gate+up, 8192 tokens, H quantized and nothing else stored      174
+//   the same with Y1 and H stored too                              221
 //   the same with Y1 in 8 bits instead (the learner's checkpoint)  207
-//   the skewed product with fp32 output (266 of bytes)             331
+//   the skewed product with fp32 output (266 of bytes)             295
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts (140 MB)
-//                                                     28 to 35 (4.0 to 4.9 TB/s)
+//                                                     28 to 33 (4.3 to 4.9 TB/s)
 // Without any epilogue the first two take 129 and 117, where the MFMAs alone need
 // 52 and 47: a workgroup's stores and SiLU are not hidden behind its products,
 // since its accumulators fill the registers and its stages the LDS; the loop
@@ -53,11 +53,15 @@ namespace {
 //   160    130.1   97.8   94.0   85.0    63.0   52.2   46.8   46.2
 //   208    162.1  123.9  116.9   92.3    80.3   62.4   64.1   48.8
 //   512    354.1  268.9  210.0  210.1   220.4  176.0  126.2  125.3
+// Near the end of the blocks of 192 (other inputs each time; 192, 256):
+//   144                   78.8   81.7                   45.1   47.6
+//   152                   81.0   83.4                   45.4   48.4
+//   160                   91.8   85.2                   49.1   49.2
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
   if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 144 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
+  if (p.M <= 152 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
   return launch_tiles<MXFP4, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
 }
 
