@@ -137,6 +137,26 @@ def test_backward_by_length(D):
         _check_backward(dy, x, w, f["mean"], f["rstd"], kind, r, *_grid(T, D, D % 8 == 0))
 
 
+@pytest.mark.parametrize("D", [520, 1001, 2048, 12000])
+@pytest.mark.parametrize("xd,dd,od,wd,kind", [(F32, F32, F32, F32, 1), (F32, BF16, BF16, BF16, 0), (BF16, BF16, F32, F32, 1),
+                                              (BF16, F32, BF16, BF16, 1)])
+def test_backward_in_two_launches_by_type(xd, dd, od, wd, kind, D):
+    """Rows of either type, more than go in one launch, with and without means."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    T = 611
+    x, rng = _data(D + kind, T, D, xd)
+    dy = to_gpu(rng.standard_normal((T, D)).astype(np.float32), dd)
+    w, b = _weights(rng, D, 2, wd)
+    f = ops.layer_norm(x, w, b, kind=kind, want_stats=True)
+    mean = f["mean"] if kind == 0 else None
+    r = ops.layer_norm_bwd(dy, x, w, mean, f["rstd"], kind=kind, dx_dtype=od, want_db=True)
+    assert r["dx"].dtype == od
+    _check_backward(dy, x, w, mean, f["rstd"], kind, r, *_grid(T, D, D % 8 == 0))
+    sums = ops.layer_norm_bwd(dy, x, w, mean, f["rstd"], kind=kind, want_dx=False, want_db=True)
+    assert sums["dx"] is None and torch.equal(sums["dw"], r["dw"]) and torch.equal(sums["db"], r["db"])
+
+
 @pytest.mark.parametrize("T,D", [(1, 2048), (3, 256), (1023, 256), (1024, 2048), (1025, 512), (5000, 64), (333, 2557),
                                  (257, 4096), (700, 5000), (300, 9001), (384, 1000), (385, 1000), (600, 2557), (400, 16384),
                                  (390, 9001), (2100, 8192), (3000, 2048), (513, 33), (2500, 1536)])
