@@ -52,11 +52,21 @@ struct Params {
   uint8_t* ys;
   int64_t M, N, K;
   int E, n_tiles;
+  bool stream;  // C or Y1 is stored past the caches
 };
 
 constexpr int kRowB = 128;          // code bytes per row and stage: one cache line
 constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
 constexpr int kTiles = 64;          // tiles looked up at a time
+// C, or Y1, of so many bytes is stored non-temporally: the 256 MB cache behind the
+// L2s would not hold it for whoever reads it next, and the operands stay there
+// instead.  Measured (us, down of 16384 skewed tokens, 537 MB): MXFP4 212 -> 166,
+// fp32 output 288 -> 212, int8 306 -> 267.  Layer forward, whose combine reads C
+// next, MXFP4 and int8, cached and non-temporal: 8192 tokens (268 MB) 367, 370 and
+// 553, 555; 10240 (336 MB) 434, 436 and 653, 649; 12288 (403 MB) 522, 513 and 778,
+// 766; 16384 679, 658 and 1012, 993, with Y1 (403 MB) kept too 798, 768 and 1071,
+// 1051.
+constexpr int64_t kStreamBytes = 336LL << 20;
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -181,8 +191,9 @@ __device__ __forceinline__ void turn8(uint32_t (&w)[8]) {
 // register the compiler takes the data registers as free at once and may write
 // them in the next instruction; the store was then seen to take the new value of
 // its third register (32 x 32 blocks of codes, in some lanes).
+template <int HINT = 0>
 __device__ __forceinline__ void store16(i32x4_t v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, HINT);
 }
 // Of two such quadruples side by side, a of 64 bytes of rows and b of the next 64:
 // afterwards a holds row l % 16 without bit 0, unit 4 ((l / 16) % 2) + 2 (l / 32) +
@@ -192,6 +203,21 @@ __device__ __forceinline__ void line(uint32_t* a, uint32_t* b) {
   for (int k = 0; k < 4; ++k) swap_quarters(a[k], b[k]);
 }
 __device__ __forceinline__ i32x4_t four(const uint32_t* w) { return (i32x4_t){(int)w[0], (int)w[1], (int)w[2], (int)w[3]}; }
+// The quadruples of a and b to their places; as a stream (non-temporal) or not.
+__device__ __forceinline__ void store_four(bool stream, __amdgpu_buffer_rsrc_t r, const uint32_t (&a)[8],
+                                           const uint32_t (&b)[8], uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
+  if (stream) {
+    store16<2>(four(a), r, a0);
+    store16<2>(four(b), r, b0);
+    store16<2>(four(a + 4), r, a1);
+    store16<2>(four(b + 4), r, b1);
+  } else {
+    store16(four(a), r, a0);
+    store16(four(b), r, b0);
+    store16(four(a + 4), r, a1);
+    store16(four(b + 4), r, b1);
+  }
+}
 
 template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p) {
@@ -588,14 +614,15 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
       const uint32_t vkq = P == 2 ? r2 * kqb + ((ln & 1) * 2 + hh) * 16 : lr * kqb + hh * 16, vke = lr * keb + hh * ((uint32_t)F / 32);
       const bool want_q = EPI == EPI_SILU_Q || (EPI == EPI_SILU_C && FMT == MXFP4 && p.hq);
       // Stores P blocks of 32 columns (paired up) at `at` of the region's rows.
-      auto leave = [&](uint32_t (&w)[P][8], __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t rb) __attribute__((always_inline)) {
+      auto leave = [&](bool stream, uint32_t (&w)[P][8], __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t rb) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < P; ++q) turn8(w[q]);
         at += r2 * rb + u4 * 16;
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          store16(four(w[q]), r, at + 64 * q);
-          store16(four(w[q] + 4), r, at + rb + 64 * q);
+        if constexpr (P == 2) {
+          store_four(stream, r, w[0], w[1], at, at + 64, at + rb, at + rb + 64);
+        } else {
+          store16(four(w[0]), r, at);
+          store16(four(w[0] + 4), r, at + rb);
         }
       };
 #pragma unroll
@@ -665,7 +692,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
               hv[q][w] = pack_bf16x2(silu_gate(bf16_lo(gv[q][w]), bf16_lo(uv[q][w])), silu_gate(bf16_hi(gv[q][w]), bf16_hi(uv[q][w])));
           if (Yp) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) leave(t ? uv : gv, ry, row * yb + (t * (uint32_t)F + f) * 2, yb);
+            for (int t = 0; t < 2; ++t) leave(p.stream, t ? uv : gv, ry, row * yb + (t * (uint32_t)F + f) * 2, yb);
           }
           if (p.amax || want_q) {
             uint32_t d[P][2];
@@ -705,7 +732,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
               }
             }
           }
-          if (Hp) leave(hv, rh, row * hb + f * 2, hb);
+          if (Hp) leave(false, hv, rh, row * hb + f * 2, hb);
           nst += P * ((Yp ? 4 : 0) + (Hp ? 2 : 0)) + (want_q ? 2 : 0) + (EPI == EPI_SILU_C ? 2 * P + 1 : 0);
           __builtin_amdgcn_sched_barrier(0);  // P pairs at a time: registers
         }
@@ -736,11 +763,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 #pragma unroll
             for (int q = 0; q < 2; ++q) turn8(w[q]);
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              line(w[0] + 4 * part, w[1] + 4 * part);
-              store16(four(w[0] + 4 * part), rc, vo + (row + part) * cb + col * EB);
-              store16(four(w[1] + 4 * part), rc, vo + (row + part + 16) * cb + col * EB);
-            }
+            for (int part = 0; part < 2; ++part) line(w[0] + 4 * part, w[1] + 4 * part);
+            const uint32_t at = vo + row * cb + col * EB;
+            store_four(p.stream, rc, w[0], w[1], at, at + 16 * cb, at + cb, at + 17 * cb);
             nst += 4;
             __builtin_amdgcn_sched_barrier(0);  // one block at a time: registers
           }
@@ -760,11 +785,8 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
             // (N may end between the two blocks: units 4..7 are then dropped)
             const uint32_t at = (u8 < 4 || col + 32 < (uint32_t)p.N ? vc : kOOB) + row * cb + col * EB;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              line(w[0] + 4 * part, w[1] + 4 * part);
-              store16(four(w[0] + 4 * part), rc, at + part * cb);
-              store16(four(w[1] + 4 * part), rc, at + (part + 16) * cb);
-            }
+            for (int part = 0; part < 2; ++part) line(w[0] + 4 * part, w[1] + 4 * part);
+            store_four(p.stream, rc, w[0], w[1], at, at + 16 * cb, at + cb, at + 17 * cb);
             nst += 4;
             __builtin_amdgcn_sched_barrier(0);  // two blocks at a time: registers
           }
@@ -809,6 +831,7 @@ template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
 int launch_tiles(const Params& p0, hipStream_t st) {
   Params p = p0;
   p.n_tiles = (int)cdiv(p.N, BN);
+  p.stream = p.M * p.N * (OUT32 ? 4 : 2) >= kStreamBytes;  // (SiLU: Y1)
   const int64_t upper = (cdiv(p.M, BM) + p.E) * p.n_tiles;  // tiles at most
   if (upper > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
   int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, BM, BN, WM, WN, S, EPI, OUT32>();
