@@ -67,6 +67,21 @@ constexpr int kTiles = 64;          // tiles looked up at a time
 // 766; 16384 679, 658 and 1012, 993, with Y1 (403 MB) kept too 798, 768 and 1071,
 // 1051.
 constexpr int64_t kStreamBytes = 336LL << 20;
+// Up to so many rows per expert in the mean most experts have one row block, so
+// each of B's lines is read once: its loads are non-temporal and leave the caches
+// to what is read again.  Measured (us, cached and non-temporal, gate+up with H
+// alone (MXFP4: quantized) | down; several inputs in turn), rows per expert:
+//             int8                        MXFP4
+//      1   51.3  45.9 | 28.8  25.7     30.2  27.4 | 17.0  17.4
+//     32   77.2  70.3 | 44.0  41.3     46.5  42.3 | 28.2  27.4
+//    128  110.5 101.5 | 65.6  65.1     65.9  64.2 | 43.6  42.5
+//    200  127.9 118.2 | 81.0  76.4     76.7  73.2 | 54.2  50.0
+//    240  151.8 144.5 | 96.0  89.9     92.8  89.4 | 62.6  60.2
+//    288  175.6 184.8 | 114  114      124.9 124.0 | 83.7  82.7
+//    384  209   238   | 137  147      129.5 125.4 | 94.2  93.1
+// (16384 skewed tokens, 1024 rows: 270 and 314 | MXFP4 169 and 220.)  Skewed
+// routing of up to 256 rows in the mean: -6 to +2%.
+constexpr int64_t kOnceRows = 240;
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -110,6 +125,13 @@ __device__ __forceinline__ float element(float a) {
   float v;
   asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
   return v;
+}
+// dma16 of lines that no other workgroup reads soon (non-temporal).
+__device__ __forceinline__ void dma16_once(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
+               "v"(voff), "s"(r)
+               : "memory", "m0");
 }
 // A buffer region of less than 2^31 bytes: reads past it are zeros, writes are
 // dropped.
@@ -219,7 +241,7 @@ __device__ __forceinline__ void store_four(bool stream, __amdgpu_buffer_rsrc_t r
   }
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int BM, int BN, int WM, int WN, int S, bool ONCE, int EPI, bool OUT32>
 __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p) {
   constexpr int NW = WM * WN;
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
@@ -399,7 +421,9 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     } else if (x < A_INSTR + B_INSTR) {
       const int i = x - A_INSTR;
       const uint32_t row = (uint32_t)(SILU ? gate_up_row(8 * NW * i, F, 0) : 8 * NW * i);
-      dma16(rb, ld_on ? smem_lds + ld_slot + AT_B + (wid + NW * i) * 1024 : pad, lb + row * rowb);
+      const uint32_t to = ld_on ? smem_lds + ld_slot + AT_B + (wid + NW * i) * 1024 : pad;
+      if constexpr (ONCE) dma16_once(rb, to, lb + row * rowb);
+      else dma16(rb, to, lb + row * rowb);
     } else {
       const int i = x - A_INSTR - B_INSTR;
       const bool real = (SC_LOADS % NW == 0 || wid + NW * i < SC_LOADS) && ld_on && (FMT == INT8 ? ld_kt == 0 : (ld_kt & 1) == 0);
@@ -814,12 +838,12 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 }
 
 // Resident workgroups per CU (the same on every gfx950 device).
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int BM, int BN, int WM, int WN, int S, bool ONCE, int EPI, bool OUT32>
 int resident_per_cu() {
   static int cached = 0;
   if (cached > 0) return cached;
   int occ = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32>, WM * WN * 64,
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, codes_kernel<FMT, BM, BN, WM, WN, S, ONCE, EPI, OUT32>, WM * WN * 64,
                                                    0) != hipSuccess ||
       occ < 1)
     occ = 1;
@@ -827,17 +851,17 @@ int resident_per_cu() {
   return occ;
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int S, int EPI, bool OUT32>
+template <int FMT, int BM, int BN, int WM, int WN, int S, bool ONCE, int EPI, bool OUT32>
 int launch_tiles(const Params& p0, hipStream_t st) {
   Params p = p0;
   p.n_tiles = (int)cdiv(p.N, BN);
   p.stream = p.M * p.N * (OUT32 ? 4 : 2) >= kStreamBytes;  // (SiLU: Y1)
   const int64_t upper = (cdiv(p.M, BM) + p.E) * p.n_tiles;  // tiles at most
   if (upper > 0x7FFFFFFFLL) return NVFP4MOE_ESHAPE;
-  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, BM, BN, WM, WN, S, EPI, OUT32>();
+  int64_t grid = (int64_t)device_cu_count() * resident_per_cu<FMT, BM, BN, WM, WN, S, ONCE, EPI, OUT32>();
   if (grid > upper) grid = upper;
   grid = cdiv(grid, 8) * 8;  // whole XCD rounds
-  codes_kernel<FMT, BM, BN, WM, WN, S, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
+  codes_kernel<FMT, BM, BN, WM, WN, S, ONCE, EPI, OUT32><<<(unsigned)grid, WM * WN * 64, 0, st>>>(p);
   return launch_status();
 }
 

@@ -65,11 +65,13 @@ namespace {
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   const int64_t E = p.E, M = p.M;
-  if (M <= 20 * E) return launch_tiles<INT8, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (M <= 40 * E) return launch_tiles<INT8, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (M <= 112 * E) return launch_tiles<INT8, 128, 256, 2, 4, 3, EPI, OUT32>(p, st);
-  if (M <= 144 * E || (M > 272 * E && M <= 352 * E)) return launch_tiles<INT8, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
-  return launch_tiles<INT8, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+  if (M <= 20 * E) return launch_tiles<INT8, 32, 256, 1, 4, 3, true, EPI, OUT32>(p, st);
+  if (M <= 40 * E) return launch_tiles<INT8, 64, 256, 1, 4, 3, true, EPI, OUT32>(p, st);
+  if (M <= 112 * E) return launch_tiles<INT8, 128, 256, 2, 4, 3, true, EPI, OUT32>(p, st);
+  if (M <= 144 * E) return launch_tiles<INT8, 192, 256, 2, 4, 2, true, EPI, OUT32>(p, st);
+  if (M <= kOnceRows * E) return launch_tiles<INT8, 256, 256, 4, 2, 2, true, EPI, OUT32>(p, st);
+  if (M > 272 * E && M <= 352 * E) return launch_tiles<INT8, 192, 256, 2, 4, 2, false, EPI, OUT32>(p, st);
+  return launch_tiles<INT8, 256, 256, 4, 2, 2, false, EPI, OUT32>(p, st);
 }
 
 // Argument checks shared by both entry points, then the launch parameters.

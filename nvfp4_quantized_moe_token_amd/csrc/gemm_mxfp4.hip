@@ -59,10 +59,11 @@ namespace {
 //   160                   91.8   85.2                   49.1   49.2
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
-  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 64, 256, 1, 4, 3, EPI, OUT32>(p, st);
-  if (p.M <= 152 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, EPI, OUT32>(p, st);
-  return launch_tiles<MXFP4, 256, 256, 4, 2, 2, EPI, OUT32>(p, st);
+  if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, true, EPI, OUT32>(p, st);
+  if (p.M <= 72 * (int64_t)p.E) return launch_tiles<MXFP4, 64, 256, 1, 4, 3, true, EPI, OUT32>(p, st);
+  if (p.M <= 152 * (int64_t)p.E) return launch_tiles<MXFP4, 192, 256, 2, 4, 2, true, EPI, OUT32>(p, st);
+  if (p.M <= kOnceRows * p.E) return launch_tiles<MXFP4, 256, 256, 4, 2, 2, true, EPI, OUT32>(p, st);
+  return launch_tiles<MXFP4, 256, 256, 4, 2, 2, false, EPI, OUT32>(p, st);
 }
 
 // Argument checks shared by both entry points, then the launch parameters.
