@@ -60,8 +60,9 @@ constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
 constexpr int kTiles = 64;          // tiles looked up at a time
 // C, or Y1, of so many bytes is stored non-temporally: the 256 MB cache behind the
 // L2s would not hold it for whoever reads it next, and the operands stay there
-// instead.  Measured (us, down of 16384 skewed tokens, 537 MB): MXFP4 212 -> 166,
-// fp32 output 288 -> 212, int8 306 -> 267.  Layer forward, whose combine reads C
+// instead.  Measured (us, down of 16384 skewed tokens, 537 MB, other inputs each
+// time): MXFP4 210 -> 199, fp32 output 289 -> 269, int8 306 -> 295 (of the same
+// inputs, which the cache then holds, 207 -> 161 and 303 -> 266).  Layer forward, whose combine reads C
 // next, MXFP4 and int8, cached and non-temporal: 8192 tokens (268 MB) 367, 370 and
 // 553, 555; 10240 (336 MB) 434, 436 and 653, 649; 12288 (403 MB) 522, 513 and 778,
 // 766; 16384 679, 658 and 1012, 993, with Y1 (403 MB) kept too 798, 768 and 1071,
@@ -79,7 +80,7 @@ constexpr int64_t kStreamBytes = 336LL << 20;
 //    240  151.8 144.5 | 96.0  89.9     92.8  89.4 | 62.6  60.2
 //    288  175.6 184.8 | 114  114      124.9 124.0 | 83.7  82.7
 //    384  209   238   | 137  147      129.5 125.4 | 94.2  93.1
-// (16384 skewed tokens, 1024 rows: 270 and 314 | MXFP4 169 and 220.)  Skewed
+// (16384 skewed tokens, 1024 rows, the same inputs: 270, 314 | MXFP4 169, 220.)  Skewed
 // routing of up to 256 rows in the mean: -6 to +2%.
 constexpr int64_t kOnceRows = 240;
 

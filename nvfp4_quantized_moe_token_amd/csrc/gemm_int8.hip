@@ -15,10 +15,10 @@
 //   the same, H stored alone                                       272
 //   the same, H and Y1 in 8 bits                                   296
 //   down, 8192 tokens (N = 2048, K = 768)                          175
-//   down, 16384 tokens, skewed routing                             308 (1.3 PFLOP/s)
+//   down, 16384 tokens, skewed routing                             295 (1.4 PFLOP/s)
 //   dense, 4096 x 8192 x 8192                                      228 (2.4 PFLOP/s)
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts
-//                                  (264 MB of weights)             46 to 50 (5.3 to 5.8 TB/s)
+//                                  (264 MB of weights)             40 to 41 (6.4 to 6.6 TB/s)
 // The dense product is held by power: the clock falls to 1.7 GHz, where the MFMAs
 // alone take 154 us, and LDS reads and loads add to the energy and so to the time
 // (35 and 28 us when taken away singly); torch's integer product of 8192 x 8192 x

@@ -18,13 +18,13 @@
 // are no faster either (155 against 138 for a dense 4096 x 8192 x 8192 product,
 // 4.0 PFLOP/s): lines are then read in halves.
 //   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      198
-//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         211
+//   down, 16384 tokens, skewed routing (N = 2048, K = 768)         199
 //   gate+up, 8192 tokens, H quantized and nothing else stored      174
 //   the same with Y1 and H stored too                              221
 //   the same with Y1 in 8 bits instead (the learner's checkpoint)  207
-//   the skewed product with fp32 output (266 of bytes)             295
+//   the skewed product with fp32 output (266 of bytes)             269
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts (140 MB)
-//                                                     28 to 33 (4.3 to 4.9 TB/s)
+//                                                     26 to 28 (5.0 to 5.4 TB/s)
 // Without any epilogue the first two take 129 and 117, where the MFMAs alone need
 // 52 and 47: a workgroup's stores and SiLU are not hidden behind its products,
 // since its accumulators fill the registers and its stages the LDS; the loop

@@ -1,6 +1,7 @@
 """Grouped products of codes whose output is too large for the caches and leaves
 non-temporally: the same bits as from calls on parts of the rows, whose output
-is small, with rows behind the last sequence left as they were."""
+is small, with rows behind the last sequence left as they were; and every tile,
+with weights loaded once or kept in the caches, against another one."""
 
 import pytest
 import torch
@@ -70,3 +71,27 @@ def test_gate(bits):
         assert want["y1"].numel() * 2 < LARGE
         for n in ("y1", "h") + (("q_h", "s_h") if more else ()):
             assert torch.equal(whole[n][lo:lo + end], want[n][:end]), n
+
+
+@pytest.mark.parametrize("rows", [10, 30, 100, 130, 150, 200, 250, 300, 400])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_same_bits_by_rows_per_expert(bits, rows):
+    """Every tile, with weights loaded once or kept: the sums go the same way, so empty experts, which lower the
+    mean and so choose another tile, change nothing."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    gemm = ops.grouped_gemm_int8 if bits == 8 else ops.grouped_gemm_mxfp4
+    gate = ops.grouped_gemm_int8_silu_gate if bits == 8 else ops.grouped_gemm_mxfp4_silu_gate
+    N, M = 256 + 256 * (bits == 4), E * rows
+    a, b, _ = _operands(bits, M, N)
+    off = torch.tensor([0, rows + 7, rows + 7, M], dtype=torch.int32, device="cuda")
+    more, at = [torch.cat([t, t.flip(0), t, t, t]) for t in b], torch.cat([off, off[-1:].expand(4 * E)])
+    out = gemm(*a, *b, off)
+    assert torch.equal(out, gemm(*a, *more, at))
+    if bits == 8:  # sums below 2^24 are exact in fp32
+        e = torch.repeat_interleave(torch.arange(E, device="cuda"), (off[1:] - off[:-1]).long())
+        for i in range(E):
+            p = (a[0][e == i].double().cpu() @ b[0][i].double().cpu().T).float().cuda()
+            assert torch.equal(out[e == i], p * a[1][e == i][:, None] * b[1][i])
+    x, y = gate(*a, *b, off), gate(*a, *more, at)
+    assert torch.equal(x["y1"], y["y1"]) and torch.equal(x["h"], y["h"])
