@@ -41,12 +41,13 @@
 namespace nvfp4moe {
 namespace {
 
-// Tiles by the mean rows per expert (the host does not know more).  Up to 112
-// rows the work is reading the weights: small row blocks and a ring three stages
-// deep.  Then it is the MFMAs, the operands' way to LDS and the stores; blocks of
-// 192 where most experts' rows fit in one, or in two of them where they take two
-// of 256 as well.  Measured kernel times in us, 128 experts, gate+up with H
-// stored (768 features, K = 2048) and down (N = 2048, K = 768):
+// Tiles by the mean rows per expert (the host does not know more).  Up to 112 rows
+// the work is reading the weights: small row blocks and a ring three stages deep.
+// Then it is the MFMAs, the operands' way to LDS and the stores; blocks of 192
+// where most experts' rows fit in one, or in two of them where they take two of
+// 256 as well.  Measured kernel times in us (before any non-temporal access), 128
+// experts, gate+up with H stored (768 features, K = 2048) and down (N = 2048, K =
+// 768):
 //   rows      gate+up, blocks of                  down, blocks of
 //             32     64    128    192    256      32     64    128    192    256
 //    16     73.3   75.4   78.6                  33.8   36.1   39.9

@@ -35,13 +35,13 @@
 namespace nvfp4moe {
 namespace {
 
-// Tiles by the mean rows per expert (the host does not know more): with few
-// rows the work is reading the weights, so the row block is small and the ring
-// three stages deep; with many it is the MFMAs, the LDS reads that feed them
-// and the stores.  The row block is one that most experts' rows fit in, up to
-// 256, where blocks of 192 need two.  Measured kernel times in us, 128 experts,
-// random routing, gate+up with Y1 and H stored (768 features, K = 2048) and down
-// (N = 2048, K = 768):
+// Tiles by the mean rows per expert (the host does not know more): with few rows
+// the work is reading the weights, so the row block is small and the ring three
+// stages deep; with many it is the MFMAs, the LDS reads that feed them and the
+// stores.  The row block is one that most experts' rows fit in, up to 256, where
+// blocks of 192 need two.  Measured kernel times in us (before any non-temporal
+// access), 128 experts, random routing, gate+up with Y1 and H stored (768
+// features, K = 2048) and down (N = 2048, K = 768):
 //   rows      gate+up, blocks of           down, blocks of
 //             32     64    192    256      32     64    192    256
 //    16     37.6   40.7   50.6   61.2    22.9   25.0   31.6   34.8
