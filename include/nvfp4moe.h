@@ -325,7 +325,7 @@ int moe_permute_mxfp4(const int32_t* topk_ids, int64_t T, int k, int E, const vo
 /*
  * moe_permute_int8 -- moe_permute_mx with 8-bit integer codes and one fp32 scale
  * per row: the activations of grouped_gemm_int8.  q [T*k][D] (16-byte aligned),
- * scales [T*k] fp32; D % 16 == 0.  Equal, bit for bit, to int8_quantize(x)
+ * scales [T*k] fp32; D % 16 == 0 (D == 0: scales of 0).  Equal, bit for bit, to int8_quantize(x)
  * followed by the row gather of codes and scales; rows past offsets[E] (skipped
  * assignments) are zeros with scale 0.  Other arguments and errors as
  * moe_permute_mx.
@@ -721,8 +721,9 @@ int int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* q
  *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).
  * Codes of -128 count as such (the quantizer gives none).  K % 16 == 0, K <=
  * 131072, N % 32 == 0, N <= 2^20, M_total < 2^31 - 256; a_q, b_q, c 16-byte
- * aligned, scales 4-byte aligned.  K == 0 gives zeros.  Errors: EINVAL (NULL,
- * negative, bad dtype), ESHAPE (shape and alignment rules).
+ * aligned, scales 4-byte aligned.  K == 0 gives zeros (where the scales are
+ * finite).  Errors: EINVAL (NULL, negative, bad dtype), ESHAPE (shape and
+ * alignment rules).
  */
 int grouped_gemm_int8(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s,
                       const int32_t* expert_offsets, int E, int64_t M_total, int64_t N, int64_t K, void* c,

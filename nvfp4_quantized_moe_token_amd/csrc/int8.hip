@@ -219,7 +219,8 @@ int launch(const Int8Params& p, bool bf16, hipStream_t st) {
 }  // namespace
 
 // Enqueue the quantize-scatter of T token rows of D elements into the permuted
-// rows given by dest (metadata already enqueued; T, D > 0, D % 16 == 0).
+// rows given by dest (metadata already enqueued; T > 0, D % 16 == 0; rows of no
+// elements get scales of 0).
 int int8_quantize_scatter_launch(const void* x, int x_dtype, int64_t T, int k, int64_t D, const int32_t* dest,
                                  const int32_t* offsets, int E, int8_t* q, float* scales, hipStream_t st) {
   Int8Params p{};

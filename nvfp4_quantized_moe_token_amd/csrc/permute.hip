@@ -1116,6 +1116,7 @@ int permute_codes_impl(const int32_t* topk_ids, int64_t T, int k, int E, const v
   if (E > kMaxExperts || k > 64) return NVFP4MOE_ESHAPE;
   if (!offsets || (T > 0 && (!topk_ids || !dest || !src))) return NVFP4MOE_EINVAL;
   if (T > 0 && D > 0 && (!x || !q || !scales)) return NVFP4MOE_EINVAL;
+  if (elem == kElemInt8 && T > 0 && !scales) return NVFP4MOE_EINVAL;  // (one per row, however wide)
   if (D % (elem == kElemInt8 ? 16 : 32) != 0) return NVFP4MOE_ESHAPE;
   if (T > 0 && D > 0 && (!aligned(x, 16) || !aligned(q, elem == NVFP4MOE_MX_E2M1 ? 8 : 16))) return NVFP4MOE_ESHAPE;
   if (elem == kElemInt8 && !aligned(scales, 4)) return NVFP4MOE_ESHAPE;
@@ -1131,10 +1132,10 @@ int permute_codes_impl(const int32_t* topk_ids, int64_t T, int k, int E, const v
   }
   const int rc = launch_metadata(topk_ids, R, E, nullptr, workspace, offsets, dest, src, status, st);
   if (rc != NVFP4MOE_OK) return rc;
-  if (D == 0) return NVFP4MOE_OK;
-  if (elem == kElemInt8)
+  if (elem == kElemInt8)  // (D == 0 too: scales of 0)
     return int8_quantize_scatter_launch(x, x_dtype, T, k, D, dest, offsets, E, reinterpret_cast<int8_t*>(q),
                                         reinterpret_cast<float*>(scales), st);
+  if (D == 0) return NVFP4MOE_OK;
   return mx_quantize_scatter_launch(x, x_dtype, T, k, D, elem, dest, offsets, E, q, reinterpret_cast<uint8_t*>(scales),
                                     st);
 }

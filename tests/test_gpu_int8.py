@@ -120,6 +120,30 @@ def test_permute_without_tokens():
     assert (r["offsets"] == 0).all() and r["q"].shape == (0, 64) and r["scales"].shape == (0,)
 
 
+@pytest.mark.parametrize("bad", [0, 3])
+def test_permute_of_rows_without_elements(bad):
+    """A row has its scale, 0, however wide it is: the products without a reduction are then zeros."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    T, k, E, N = 37, 2, 5, 64
+    rng = np.random.default_rng(bad)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids.reshape(-1)[:bad] = E
+    scales = torch.full((T * k,), float("nan"), device="cuda")
+    x = torch.zeros(T, 0, dtype=BF16, device="cuda")
+    r = ops.moe_permute_int8(to_gpu(ids, torch.int32), E, x, scales=scales)
+    assert r["scales"] is scales and (scales == 0).all()
+    assert (ops.int8_quantize(x)[1] == 0).all()
+    ref = ops.moe_permute(to_gpu(ids, torch.int32), E)
+    for n in ("offsets", "dest", "src"):
+        assert torch.equal(r[n], ref[n]), n
+    out = torch.full((T * k, N), 7.0, device="cuda")
+    ops.grouped_gemm_int8(r["q"], scales, torch.zeros(E, N, 0, dtype=torch.int8, device="cuda"),
+                          torch.ones(E, N, device="cuda"), r["offsets"], out=out)
+    end = T * k - bad
+    assert (out[:end] == 0).all() and (out[end:] == 7).all()
+
+
 def _operands(seed, M, N, K, E, full=False):
     """Codes and scales on the GPU; full: codes of the greatest magnitude."""
     g = torch.Generator(device="cuda").manual_seed(seed)

@@ -73,6 +73,13 @@ def test_int8_entry_points(lib):
         (13, ws - 1, -5), (12, None, -5)])
 
 
+def test_rows_without_elements_have_scales(lib):
+    T, k, E = 100, 8, 128
+    ws = lib.moe_permute_workspace_size(T, k, E)
+    ok = [FAKE, T, k, E, None, 1, 0, None, FAKE, FAKE, FAKE, FAKE, FAKE, ws, None, None]
+    _refused(lib.moe_permute_int8, ok, [(8, None, -1), (8, FAKE + 2, -2)])
+
+
 def test_checkpoint_entry_points(lib):
     q = lib.mx_quantize
     assert q(FAKE, 1, 4, 64, _lib.MX_INT8, FAKE + 8, FAKE, None) == -2
