@@ -597,16 +597,16 @@ def mx_quantize(x, elem=MX_E4M3, q=None, scales=None):
     elem MX_E4M3 (MXFP8, one byte per element), MX_E2M1 (MXFP4, packed
     pairs) or MX_INT8 (MXINT8, one two's complement byte per element: the
     form of activations kept for the backward pass).  Returns (q, scales)."""
-    _dev(x, q, scales)
+    _need(x, "x", _FLOATS, None, None)
     rows, K = x.shape
-    dev = x.device
     qcols = K // 2 if elem == MX_E2M1 else K
     if elem == MX_INT8:
         _need(q, "q", torch.uint8, rows, K)
         _need(scales, "scales", torch.uint8, rows, K // 32)
-    q = torch.empty((rows, qcols), dtype=torch.uint8, device=dev) if q is None else q
-    scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=dev) if scales is None else scales
-    rc = _lib.load().mx_quantize(_ptr(x), _DT[x.dtype], rows, K, elem, _ptr(q), _ptr(scales), _stream())
+    with _on_device(x, q, scales):
+        q = x.new_empty((rows, qcols), dtype=torch.uint8) if q is None else q
+        scales = x.new_empty((rows, K // 32), dtype=torch.uint8) if scales is None else scales
+        rc = _lib.load().mx_quantize(_ptr(x), _DT[x.dtype], rows, K, elem, _ptr(q), _ptr(scales), _stream())
     _check("mx_quantize", rc)
     return q, scales
 

@@ -174,6 +174,43 @@ def test_refused_in_python(launched, call):
     assert launched == []
 
 
+@pytest.mark.parametrize("elem", [ops.MX_E4M3, ops.MX_E2M1, ops.MX_INT8])
+def test_mx_quantizer_refuses_other_dtypes(launched, elem):
+    for x in (z(4, 64, dtype=torch.float16), z(4, 64, dtype=U8), z(2, 4, 64)):
+        with pytest.raises(ValueError):
+            ops.mx_quantize(x, elem)
+    assert launched == []
+
+
+@pytest.mark.parametrize("call", [
+    lambda: ops.mx_quantize(z(4, 64), ops.MX_E4M3),
+    lambda: ops.mx_quantize(z(4, 64), ops.MX_E2M1),
+    lambda: ops.mx_quantize(z(4, 64), ops.MX_INT8),
+    lambda: ops.mx_dequantize(z(4, 64, dtype=U8), z(4, 2, dtype=U8), ops.MX_INT8),
+    lambda: ops.int8_quantize(z(4, 32)),
+    lambda: ops.moe_permute_int8(z(4, 2, dtype=I32), 8, z(4, 32), workspace=z(64, dtype=U8)),
+    lambda: ops.grouped_gemm_int8(**GEMM),
+    lambda: ops.grouped_gemm_int8_silu_gate(**GEMM),
+    lambda: ops.silu_gate_bwd_mx(z(4, 128, dtype=U8), z(4, 4, dtype=U8), z(4, 64)),
+    lambda: ops.layer_norm(z(4, 8), f(8)),
+    lambda: ops.layer_norm_bwd(f(4, 8), z(4, 8), None, *STATS),
+])
+def test_launched_with_the_tensors_gpu_current(launched, monkeypatch, call):
+    """The stream is taken, and the library called, while the inputs' GPU is the current one."""
+    inside, stream = [], []
+
+    @contextlib.contextmanager
+    def on_device(first, *ts):
+        inside.append(first)
+        yield
+        inside.pop()
+
+    monkeypatch.setattr(ops, "_on_device", on_device)
+    monkeypatch.setattr(ops, "_stream", lambda: stream.append(len(inside)))
+    call()
+    assert len(launched) == 1 and stream == [1] and inside == []
+
+
 def test_cpu_tensors_are_refused():
     for call in (lambda: ops.layer_norm(z(4, 8)), lambda: ops.int8_quantize(z(4, 32)),
                  lambda: ops.silu_gate_bwd_mx(z(4, 128, dtype=U8), z(4, 4, dtype=U8), z(4, 64))):
