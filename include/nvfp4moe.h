@@ -714,8 +714,8 @@ int int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t K, int8_t* q
  * grouped_gemm_int8 -- the grouped GEMM of 8-bit integers (W8A8, a precision
  * beside [JA] third paragraph's; fourth: contiguous layout, grouped GEMM):
  *   C[r][n] = (float)(sum_k a[r][k] b[e][n][k]) * a_s[r] * b_s[e][n],
- * r in [offsets[e], offsets[e+1]), the sum exact in int32, then three fp32
- * roundings in that order.  Rows >= offsets[E] are not written.
+ * r in [offsets[e], offsets[e+1]), the sum exact, then three fp32 roundings in
+ * that order.  Rows >= offsets[E] are not written.
  *   a_q [M_total][K], a_s [M_total] fp32   (moe_permute_int8, int8_quantize)
  *   b_q [E][N][K],    b_s [E][N] fp32      (int8_quantize of the weights' rows)
  *   offsets [E+1] int32 on the device; c [M_total][N] F32 or BF16 (RNE).

@@ -156,6 +156,22 @@ __device__ __forceinline__ f32x4_t elements(const typename Operands<FMT>::Acc& a
   }
   return v;
 }
+// The integers' sums reach from -127 * 128 K to 128 * 128 K: with the longest K a
+// row and a column of -128 throughout give 2^31, one more than int32 holds, which
+// arrives as the lowest number (no other sum is as low).  The number below it,
+// 2^31 - 1, is 2^31 in fp32.
+constexpr int64_t kLongestInt8 = 1 << 17;
+__device__ __forceinline__ int32_t unwrapped(int32_t a) {
+  int32_t v;
+  asm volatile("v_accvgpr_read_b32 %1, %0\n\t"
+               "v_cmp_eq_u32 vcc, %2, %1\n\t"
+               "v_subbrev_co_u32 %1, vcc, 0, %1, vcc\n\t"
+               "v_accvgpr_write_b32 %0, %1"
+               : "+a"(a), "=&v"(v)
+               : "s"(0x80000000u)
+               : "vcc");
+  return a;
+}
 __device__ __forceinline__ void bf16x4(f32x4_t v, uint32_t* w) {
   w[0] = pack_bf16x2(v[0], v[1]);
   w[1] = pack_bf16x2(v[2], v[3]);
@@ -609,6 +625,16 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     // the wave exchange too and a store writes whole lines (skewed product 212
     // against 224 us).  Rows past the expert's end are past the store's region.
     settle();
+    if constexpr (FMT == INT8) {
+      if (p.K == kLongestInt8) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = unwrapped(acc[i][j][r]);
+      }
+    }
     int ln = lane;
     asm volatile("" : "+v"(ln));  // (what follows from it is not kept from tile to tile: registers)
     const int hh = ln >> 5;

@@ -2,7 +2,8 @@
 // one fp32 scale per row (token) of A and per row (output channel) of B_e,
 //   C[r][n] = (float)(sum_k a[r][k] b[n][k]) * as[r] * bs[e][n],
 // the sum exact in int32 (v_mfma_i32_32x32x32_i8; K <= 131072 keeps it below
-// 2^31), then three fp32 roundings: of the sum and of the two products.
+// 2^31, but for one sum that is told apart), then three fp32 roundings: of the
+// sum and of the two products.
 // The 8-bit integer form of the experts' products stands beside the report's
 // W4A8 and W4A4 ("miniTE報告、NVFP4強化学習の安定性を検証", third paragraph: the
 // precisions compared; fourth: grouped GEMM, op fusion).
@@ -83,7 +84,7 @@ int check_operands(const int8_t* a_q, const float* a_s, const int8_t* b_q, const
   if (M_total > 0 && N > 0 && (!a_s || !b_s || (K > 0 && (!a_q || !b_q)))) return NVFP4MOE_EINVAL;
   if (K % 16 != 0 || N % 32 != 0) return NVFP4MOE_ESHAPE;
   // a tile's operand region is read through 32-bit offsets; the sums stay exact
-  if (M_total >= 0x7FFFFF00LL || N > (1 << 20) || K > (1 << 17)) return NVFP4MOE_ESHAPE;
+  if (M_total >= 0x7FFFFF00LL || N > (1 << 20) || K > kLongestInt8) return NVFP4MOE_ESHAPE;
   if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(expert_offsets, 4))
     return NVFP4MOE_ESHAPE;
   p = Params{};

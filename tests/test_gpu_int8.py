@@ -214,6 +214,49 @@ def test_largest_sums(M, N, K):
     assert _same(got, want)
 
 
+@pytest.mark.parametrize("M,E", [(1, 1), (40, 1), (100, 3), (300, 3), (400, 3), (600, 3), (900, 3), (1200, 3)])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_the_sum_that_int32_does_not_hold(M, E, out_dtype):
+    """A row and a channel of -128 throughout with the longest K: 128 * 128 * 131072 = 2^31; with its neighbours."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    N, K = 64, 131072
+    aq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    bq = torch.full((E, N, K), -128, dtype=torch.int8, device="cuda")
+    bq[:, 1::4] = 127        # the lowest sum
+    bq[:, 2::4, 77] = -127   # 128 less than 2^31
+    aq[1::3, 131071] = 0
+    a_s, b_s = torch.rand(M, device="cuda") + 0.5, torch.rand(E, N, device="cuda") + 0.5
+    off = [0] + [M * (e + 1) // E for e in range(E)]
+    got = ops.grouped_gemm_int8(aq, a_s, bq, b_s, to_gpu(np.array(off), torch.int32), out_dtype=out_dtype)
+    assert (got[0, 0::4] > 0).all()
+    # whole numbers by hand: the products in fp64 would read 8-byte copies of the codes
+    n = torch.full((M, N), 1 << 31, dtype=torch.int64, device="cuda")
+    n[:, 1::4] = -127 * 128 * K
+    n[:, 2::4] -= 128
+    n[1::3] -= torch.where(torch.arange(N, device="cuda") % 4 == 1, -127 * 128, 128 * 128)
+    e = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(off, device="cuda").diff())
+    assert _same(got, (n.float() * a_s[:, None] * b_s[e]).to(out_dtype))
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_the_sum_that_int32_does_not_hold_in_the_gate(M):
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    F, K = 128, 131072
+    aq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    bq = torch.full((1, 2 * F, K), -128, dtype=torch.int8, device="cuda")
+    bq[:, 1::2] = 127
+    a = aq, torch.full((M,), 2.0 ** -31, device="cuda"), bq, torch.rand(1, 2 * F, device="cuda") + 0.5
+    off = to_gpu(np.array([0, M]), torch.int32)
+    y1 = ops.grouped_gemm_int8(*a, off, out_dtype=BF16)
+    assert (y1[:, 0::2] > 0).all() and (y1[:, 1::2] < 0).all()
+    r = ops.grouped_gemm_int8_silu_gate(*a, off, want_ckpt=True)
+    assert torch.equal(r["y1"], y1) and torch.equal(r["h"], ops.silu_gate_fwd(y1)[0])
+    q, s = ops.mx_quantize(y1, ops.MX_INT8)
+    assert torch.equal(r["q_y1"], q) and torch.equal(r["s_y1"], s)
+
+
 def test_scales_that_are_not_finite_and_no_reduction():
     require_gpu()
     from nvfp4_quantized_moe_token_amd import ops
