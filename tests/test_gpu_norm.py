@@ -80,6 +80,44 @@ def test_forward_by_length(D):
         _check_forward(x, w, b, 1e-5, kind, r, out)
 
 
+@pytest.mark.parametrize("D", [500, 512, 1024, 2047, 2048, 4096, 8192, 16383, 16384])
+@pytest.mark.parametrize("power", [10, 16, 20])
+def test_forward_of_a_large_mean(D, power):
+    """The rounding of the mean's sum leaves no trace: elements of mean 2^power and deviation 1 (fp32 holds them
+    to 2^(power - 23)).  The differences d from the first mean are off by nothing (it is off by less than 2^(power -
+    15), so an element and it lie within a factor of 2 of each other) or by half a step of d; their sums by a chain
+    of roundings; and the mean of d, which the second sum takes out, is off by that of the second sum alone."""
+    require_gpu()
+    from nvfp4_quantized_moe_token_amd import ops
+    rng = np.random.default_rng(D + power)
+    x = to_gpu((2.0 ** power + rng.standard_normal((33, D))).astype(np.float32), F32)
+    x[3] = 2.0 ** power + 0.125 if power < 20 else 2.0 ** power + 1  # a row without deviation
+    x[4] = -x[4]
+    w, b = _weights(rng, D, 2, F32)
+    xn = _f64(x)
+    y, mean, rstd = norm.forward(xn, _f64(w), _f64(b), 1e-5, False)
+    r = ops.layer_norm(x, w, b, eps=1e-5)
+    n = _chain(D)
+    # the first mean's error, and what its correction leaves
+    dm = (n + 3) * U * np.abs(xn).mean(1)
+    v = np.abs(xn - mean[:, None])
+    dc = (n + 3) * U * (v.mean(1) + dm)
+    # the mean square of d, (n + 4) roundings of something as large as it, less the square of d's mean
+    ms, big = (v * v).mean(1), ((v + dm[:, None]) ** 2).mean(1)
+    er = 0.5 * ((n + 8) * U * big + 2 * dm * dc + dc * dc) / (ms + 1e-5) + 6 * U
+    live = np.arange(33) != 3
+    assert er[live].max() < 0.002
+    assert (np.abs(_f64(r["rstd"]) - rstd) <= 1.01 * er * rstd)[live].all()
+    assert (np.abs(_f64(r["mean"]) - mean) <= dc + U * np.abs(mean))[live].all()
+    wa = np.abs(_f64(w))
+    tol = 1.01 * ((v + dm[:, None]) * rstd[:, None] * wa * (er[:, None] + 5 * U) + dc[:, None] * rstd[:, None] * wa)
+    tol = tol + U * 2 * (np.abs(y) + tol) + 1e-38
+    assert (np.abs(_f64(r["y"]) - y) <= tol)[live].all()
+    # without deviation: the variance is at most what the sums' roundings make of dm^2
+    assert np.isfinite(_f64(r["y"])[3]).all() and (np.abs(_f64(r["mean"])[3] - xn[3, 0]) <= dc[3] + U * xn[3, 0])
+    assert (np.abs(_f64(r["y"])[3] - _f64(b)) <= 1.01 * dc[3] / np.sqrt(1e-5) * wa + U * 2 * np.abs(_f64(b)) + 1e-6).all()
+
+
 def _check_backward(dy, x, w, mean, rstd, kind, r, blocks, groups):
     T, D = x.shape
     want = norm.backward(_f64(dy), _f64(x), _f64(w), _f64(mean), _f64(rstd), kind == 1)
