@@ -134,8 +134,8 @@ def backward(dy, topk_w, w_gu, w_dn, meta, buf, wgrad_stream=None, x=None, d_top
     must still hold the forward's).
 
     With buffers that keep Y1 in 8 bits (``checkpoint``), dY1 and H come from
-    there (silu_gate_bwd_mx writes buf.h again), and the down projection's
-    weight gradient follows that."""
+    there (silu_gate_bwd_mx writes buf.h again, also where an int8 forward
+    left its own H), and the down projection's weight gradient follows that."""
     main = torch.cuda.current_stream()
     off = meta["offsets"]
 
@@ -285,8 +285,10 @@ def backward_nvfp4(dy, topk_w, wt_gu, wt_dn, meta, buf, nb, amax_x=None, d_topk_
 
 def _backward_buffers(buf, e, dx_dtype, checkpoint):
     """What ``backward`` reads and writes besides a forward's own buffers:
-    Y1 in bf16, or with ``checkpoint`` in 8 bits (a third of Y1's and H's
-    bytes; H is then made again by the backward pass)."""
+    Y1 in bf16, or with ``checkpoint`` in 8 bits.  H is then made again by the
+    backward pass, so what has to outlive the forward pass is a third of Y1's
+    and H's bytes; the buffers hold two thirds, since H has its place among
+    them (buf.h) either way."""
     T, E, D, F, R = buf.T, buf.E, buf.D, buf.F, buf.T * buf.k
     f32, u8 = torch.float32, torch.uint8
     buf.y1 = buf.q_y1 = buf.s_y1 = None

@@ -232,3 +232,14 @@ def test_checkpoint_buffers_hold_a_third():
         bytes_ = lambda *ts: sum(t.numel() * t.element_size() for t in ts)  # noqa: E731
         assert a.q_y1 is None and b.y1 is None
         assert bytes_(b.q_y1, b.s_y1) / bytes_(a.y1, a.h) == pytest.approx(33 / 96)
+
+
+def test_what_the_checkpoint_takes_from_the_buffers():
+    """All of the buffers: Y1's bytes less those of its codes and scales, and nothing else (H keeps its place)."""
+    T, k, E, D, F = 64, 2, 4, 128, 128
+    for cls in (moe_layer.BuffersMXFP4, moe_layer.BuffersInt8):
+        a, b = (cls(T, k, E, D, F, torch.device("cpu"), backward=True, checkpoint=c) for c in (False, True))
+        size = lambda o: sum(t.numel() * t.element_size() for t in vars(o).values() if torch.is_tensor(t))  # noqa: E731
+        y1, h = T * k * 2 * F * 2, T * k * F * 2
+        assert size(a) - size(b) == y1 - y1 // 2 * 33 // 32
+        assert (b.q_y1.numel() + b.s_y1.numel() + b.h.numel() * 2) / (y1 + h) == pytest.approx(65 / 96)
