@@ -568,8 +568,7 @@ extern "C" int layer_norm(const void* x, int x_dtype, int64_t T, int64_t D, cons
 
 extern "C" size_t layer_norm_bwd_workspace_size(int64_t T, int64_t D) {
   if (T <= kNormFewRows || D < 1 || D > kNormMaxD) return 0;
-  const int64_t n = T < kNormBwdBlocks ? T : kNormBwdBlocks;
-  return (size_t)(2 * n * D * 4);
+  return (size_t)(2 * kNormBwdBlocks * D * 4);
 }
 
 extern "C" int layer_norm_bwd(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t T, int64_t D,
