@@ -58,9 +58,9 @@ struct Params {
 constexpr int kRowB = 128;          // code bytes per row and stage: one cache line
 constexpr int kOffsetsInLds = 512;  // experts whose offsets are kept in LDS
 constexpr int kTiles = 64;          // tiles looked up at a time
-// C, or Y1, of so many bytes is stored non-temporally: the 256 MB cache behind the
-// L2s would not hold it for whoever reads it next, and the operands stay there
-// instead.  Measured (us, down of 16384 skewed tokens, 537 MB, other inputs each
+// C, or Y1, of so many bytes (352 MB) is stored non-temporally: the 256 MB cache
+// behind the L2s would not hold it for whoever reads it next, and the operands stay
+// there instead.  Measured (us, down of 16384 skewed tokens, 537 MB, other inputs each
 // time): MXFP4 210 -> 199, fp32 output 289 -> 269, int8 306 -> 295 (of the same
 // inputs, which the cache then holds, 207 -> 161 and 303 -> 266).  Layer forward, whose combine reads C
 // next, MXFP4 and int8, cached and non-temporal: 8192 tokens (268 MB) 367, 370 and
@@ -82,6 +82,18 @@ constexpr int64_t kStreamBytes = 336LL << 20;
 //    384  209   238   | 137  147      129.5 125.4 | 94.2  93.1
 // (16384 skewed tokens, 1024 rows, the same inputs: 270, 314 | MXFP4 169, 220.)  Skewed
 // routing of up to 256 rows in the mean: -6 to +2%.
+// The rule does not ask for the weights' bytes: a model of several layers finds them
+// in HBM whatever their size.  Products of 16, 64, 200 rows per expert (us, cached and
+// non-temporal), several sets of weights in turn | the same ones again and again, which
+// a cache may then hold (what a single small layer gives up):
+//   int8   32 x 1536 x 2048, 101 MB  22.3 20.4  27.3 25.1  40.5 38.9 | 18.8 18.9  22.2 24.0  33.5 37.9
+//          64 x 1536 x 2048, 201 MB  41.0 36.8  49.7 48.1  79.1 72.2 | 32.8 35.1  40.8 45.0  66.3 72.0
+//          4 x 8192 x 8192, 268 MB   65.0 60.6  73.3 68.5 112.0 102  | 47.6 59.0  57.2 67.0  94.8 101
+//   MXFP4  32 x 1536 x 2048, 50 MB   15.7 14.7  23.9 23.0  27.7 26.7 | 12.8 12.5  20.0 21.4  22.7 25.0
+//          128 x 2048 x 768, 101 MB  26.0 24.3  35.5 34.5  56.2 53.8 | 22.5 22.6  32.0 37.1  44.4 53.1
+//          4 x 8192 x 8192, 134 MB   43.1 40.0  45.2 43.4  69.7 65.7 | 26.8 38.3  31.2 41.5  51.0 64.7
+// Layer forward of 512 tokens, MXFP4, 32 experts, top-4: 59.0 58.7 | 52.5 57.7; 128 experts, top-8
+// (302 MB): 99.0 91.7 | 97.4 91.6.
 constexpr int64_t kOnceRows = 240;
 
 typedef __attribute__((address_space(3))) const i32x4_t lds_i32x4_t;
@@ -642,7 +654,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
     const int r4 = ln & 14, u8 = ((ln >> 4) & 1) * 4 + u4;  // and after line()
     const uint32_t tile_rows = (uint32_t)(cur.w - cur.z);
     // The integers' scales of this lane's row of row block i, and of its columns
-    // 8 g + 4 hh + 0..3 of column block j.
+    // 16 hh + 4 g + 0..3 of column block j (rows 8 g + 4 hh + 0..3 of B in LDS).
     auto row_scale = [&](int i) __attribute__((always_inline)) {
       if constexpr (FMT == INT8) return *(lds_f32_t*)(uintptr_t)(scales + so + (wm * WTM + i * 32 + (ln & 31)) * 4);
       else return 0.0f;
@@ -682,7 +694,7 @@ __global__ __launch_bounds__(WM* WN * 64, WM* WN / 4) void codes_kernel(Params p
 #pragma unroll
         for (int j = 0; j < FN; j += 2 * P) {
           // Y1 is rounded to bf16 first: H is the gate of the stored values.
-          uint32_t gv[P][8], uv[P][8], hv[P][8];  // columns 8 g + 4 hh + 0..3 in words 2 g and 2 g + 1
+          uint32_t gv[P][8], uv[P][8], hv[P][8];  // columns 16 hh + 4 g + 0..3 in words 2 g and 2 g + 1
 #pragma unroll
           for (int q = 0; q < P; ++q) {
 #pragma unroll

@@ -12,11 +12,12 @@
 //
 // Bounds and measurements (us of the kernel, several sets of inputs in turn; 128
 // experts, top-8).
-//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      287 (1.4 PFLOP/s)
-//   the same, H stored alone                                       272
-//   the same, H and Y1 in 8 bits                                   296
+//   gate+up, 8192 tokens (65536 rows, 768 features, K = 2048)      288 to 295 (1.4 PFLOP/s)
+//   the same, H stored alone                                       263 to 272
+//   the same, H and Y1 in 8 bits                                   297
 //   down, 8192 tokens (N = 2048, K = 768)                          175
-//   down, 16384 tokens, skewed routing                             295 (1.4 PFLOP/s)
+//   down, 16384 tokens, skewed routing                             293 to 298 (1.4 PFLOP/s)
+//   the same, fp32 output                                          372 to 377
 //   dense, 4096 x 8192 x 8192                                      228 (2.4 PFLOP/s)
 //   N = 1536, K = 2048, 16 tokens, which reach 84 of the experts
 //                                  (264 MB of weights)             40 to 41 (6.4 to 6.6 TB/s)
@@ -46,24 +47,36 @@ namespace {
 // the work is reading the weights: small row blocks and a ring three stages deep.
 // Then it is the MFMAs, the operands' way to LDS and the stores; blocks of 192
 // where most experts' rows fit in one, or in two of them where they take two of
-// 256 as well.  Measured kernel times in us (before any non-temporal access), 128
-// experts, gate+up with H stored (768 features, K = 2048) and down (N = 2048, K =
-// 768):
-//   rows      gate+up, blocks of                  down, blocks of
-//             32     64    128    192    256      32     64    128    192    256
-//    16     73.3   75.4   78.6                  33.8   36.1   39.9
-//    24     82.2   75.7   79.2                  37.1   36.5   40.7
-//    32     82.8   76.9   80.2                  37.2   37.1   41.1
-//    48     92.7   91.0   83.1                  42.8   43.4   44.3
-//    64    110.1   93.4   84.7   99.3  111.1    51.2   46.1   45.0   52.2   58.9
-//    96    134.4  106.4   91.0  102.4  111.3    59.9   53.7   48.9   54.0   60.7
-//   128    160.2  125.7  113.0  107.4  112.8    90.9   70.5   64.2   62.2   66.5
-//   160           137.2  129.4  127.1  117.1           87.1   85.1   77.4   73.6
-//   256           193.7  162.6  166.3  168.8          126.1  102.7  112.1  104.8
-//   320           230.7  185.1  177.2  197.7          149.3  120.9  120.9  133.2
-//   384           263.5  218.7  220.0  207.7          177.8  140.1  143.2  135.7
-//   512           337.4  278.7  262.8  265.4          243.2  181.8  176.3  171.4
-//  1024           627.4  505.1  479.6  462.9          424.9  355.4  330.7  317.1
+// 256 as well.  Measured kernel times in us (weights non-temporal up to 240 rows),
+// 128 experts, random routing, three sets of inputs in turn, gate+up with H stored
+// (768 features, K = 2048) and down (N = 2048, K = 768):
+//   rows     gate+up, blocks of                   down, blocks of
+//              32     64    128    192    256       32     64    128    192    256
+//    16     65.7   67.9   70.9                   39.0   39.5   42.6
+//    20     68.9   68.2   71.6                   41.0   40.4   43.4
+//    24     75.1   69.1   72.2                   43.9   41.2   44.1
+//    32     79.0   70.3   73.3                   46.1   41.8   44.5
+//    40     88.6   71.5   75.8                   53.5   43.5   46.0
+//    48     94.7   84.0   76.4                   55.2   49.3   46.7
+//    64    122.5   93.5   78.8   90.8   99.8     64.5   55.6   48.4   57.5   62.3
+//    96    155.0  105.4   85.3   96.1  104.9     80.5   62.1   52.0   60.4   65.3
+//   112    151.3  115.7   98.0   96.2  104.5     87.9   69.2   60.5   61.6   68.0
+//   128    173.1  134.0  115.7   98.1  105.5     98.2   75.0   66.9   63.2   68.1
+//   144    182.6  150.2  131.3   99.4  109.4    108.8   86.4   82.6   63.6   69.8
+//   152    190.5  155.1  132.5  101.3  108.8    114.2   86.6   84.1   65.4   70.5
+//   160    200.1  153.5  129.4  107.6  107.3    118.6   89.6   83.1   68.0   70.4
+//   200           171.6  127.6  149.5  115.3           106.9   82.5   93.0   75.7
+//   256           196.2  163.0  169.2  166.9           127.2  100.9  110.3  106.6
+//   272           202.6  179.3  170.8  188.1           131.5  107.8  110.3  121.6
+//   288           208.4  183.7  172.5  190.9           135.7  114.3  110.9  125.4
+//   320           229.2  189.5  177.2  195.3           149.0  117.0  115.1  126.8
+//   352           245.2  197.3  197.4  200.6           163.2  127.8  130.2  129.0
+//   384           262.2  219.1  221.6  201.8           178.7  139.8  141.5  134.3
+//   512           343.9  277.6  256.5  261.9           244.7  180.2  172.6  175.7
+//  1024           625.7  503.5  474.8  454.1           408.2  330.0  312.6  300.2
+// The borders are those of an earlier table, without non-temporal accesses.  By this
+// one they cost at most 2% but from 145 to 159 rows (blocks of 192: up to 7% less)
+// and from 241 to 272 (blocks of 128 or 192: up to 11% less).
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   const int64_t E = p.E, M = p.M;

@@ -39,24 +39,37 @@ namespace {
 // the work is reading the weights, so the row block is small and the ring three
 // stages deep; with many it is the MFMAs, the LDS reads that feed them and the
 // stores.  The row block is one that most experts' rows fit in, up to 256, where
-// blocks of 192 need two.  Measured kernel times in us (before any non-temporal
-// access), 128 experts, random routing, gate+up with Y1 and H stored (768
-// features, K = 2048) and down (N = 2048, K = 768):
-//   rows      gate+up, blocks of           down, blocks of
-//             32     64    192    256      32     64    192    256
-//    16     37.6   40.7   50.6   61.2    22.9   25.0   31.6   34.8
-//    32     44.0   42.5   51.7   60.6    25.4   25.9   31.6   35.3
-//    64     59.7   56.1   56.9   65.9    35.4   32.3   36.1   39.0
-//    80     71.0   63.7   59.9   68.0    40.6   38.2   36.6   39.7
-//    96     89.6   68.0   64.9   71.3    43.0   37.6   38.0   41.5
-//   128    112.5   88.1   75.5   79.2    52.8   44.1   40.6   44.8
-//   160    130.1   97.8   94.0   85.0    63.0   52.2   46.8   46.2
-//   208    162.1  123.9  116.9   92.3    80.3   62.4   64.1   48.8
-//   512    354.1  268.9  210.0  210.1   220.4  176.0  126.2  125.3
-// Near the end of the blocks of 192 (other inputs each time; 192, 256):
-//   144                   78.8   81.7                   45.1   47.6
-//   152                   81.0   83.4                   45.4   48.4
-//   160                   91.8   85.2                   49.1   49.2
+// blocks of 192 need two.  Measured kernel times in us (weights non-temporal up to
+// 240 rows), 128 experts, random routing, three sets of inputs in turn, gate+up with
+// Y1 and H stored (768 features, K = 2048) and down (N = 2048, K = 768):
+//   rows     gate+up, blocks of            down, blocks of
+//              32     64    192    256       32     64    192    256
+//    16     44.2   46.2                   25.1   26.5
+//    20     45.5   46.2                   26.3   26.9
+//    24     50.2   47.0                   28.2   27.1
+//    32     54.7   48.1                   29.9   27.7
+//    48     62.9   57.4                   35.5   32.4
+//    64     74.1   62.2   62.9   65.9     40.9   35.0   36.6   39.3
+//    72     81.3   69.4   63.3   66.6     46.1   40.3   37.6   40.3
+//    80     85.4   69.7   63.8   67.8     47.8   40.1   37.7   40.6
+//    96     96.4   69.8   67.0   70.3     52.4   40.6   39.1   42.2
+//   112    102.6   78.8   66.8   70.1     59.4   45.7   40.7   43.9
+//   128    117.6   88.2   69.7   73.1     65.2   49.1   41.4   45.5
+//   144    127.0   98.0   71.6   75.0     72.8   57.3   42.2   46.5
+//   152    135.5   98.3   73.3   76.2     75.5   57.6   42.9   46.5
+//   160    141.6  100.7   78.0   76.9     79.7   59.3   44.6   46.6
+//   200           121.7  104.8   81.7            72.4   61.5   54.7
+//   256           144.8  122.0  119.3            86.2   70.0   66.3
+//   272           151.3  125.9  130.7            89.1   71.7   76.4
+//   288           155.6  128.9  131.7            92.3   73.7   80.2
+//   320           170.9  134.0  137.6           101.9   78.1   80.1
+//   352           183.9  150.5  144.5           112.6   87.5   85.9
+//   384           200.8  164.3  149.9           124.3   95.2   91.9
+//   512           266.0  199.1  192.8           171.7  121.2  117.0
+//  1024           477.8  372.9  333.3           290.1  224.5  205.9
+// The borders are those of an earlier table, without non-temporal accesses.  By this
+// one they cost at most 2% but at 21 to 24 rows (blocks of 64: up to 6% less), 65 to 72
+// (192: 9%) and 257 to 320 (192: up to 8%).
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   if (p.M <= 24 * (int64_t)p.E) return launch_tiles<MXFP4, 32, 256, 1, 4, 3, true, EPI, OUT32>(p, st);

@@ -30,7 +30,8 @@
 // 256 added 32 of them one after another); of the same inputs together 27, 31 when
 // the next row's loads branch on its type (each branch then waits for the other's),
 // 29 with two rows in flight; a wave for rows of 2048 with twice the columns a lane
-// 49.  16 rows of 2048: 3.5.
+// 49.  16 rows of 2048: 3.5.  Odd lengths, by single elements: 16384 x 2047 bf16
+// forward 85 to 90, 4096 x 6001 fp32 59 to 66.
 #include <type_traits>
 
 #include "common.hpp"
@@ -44,8 +45,10 @@ constexpr int kNormBwdBlocks = 256;  // rows of partial sums at most
 // is at most 86 roundings (a thread's 64 elements, then the lanes and waves), 2^-17
 // of it: below this ratio that adds no more than 2^-26 to the variance.
 constexpr float kNormFar = 256.0f;
-// Up to so many rows the gradient takes one launch.  Measured (us through the C
-// entry point, both gradients; one launch and two):
+// Up to so many rows the gradient takes one launch, whatever their length and type:
+// a compromise, since the two are level near 330 rows at 512 columns, 400 at 2048,
+// and past 1024 at an odd length.  Measured (us through the C entry point, both
+// gradients; one launch and two):
 //   rows   512 columns   2048         2557 fp32    8192
 //     16   3.7   6.9     3.5   8.0    4.8   9.1    3.6   7.5
 //    256   5.9   7.2     5.8   8.7    5.2  11.1   10.7  17.0
