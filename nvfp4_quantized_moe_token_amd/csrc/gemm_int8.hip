@@ -75,8 +75,8 @@ namespace {
 //   512           343.9  277.6  256.5  261.9           244.7  180.2  172.6  175.7
 //  1024           625.7  503.5  474.8  454.1           408.2  330.0  312.6  300.2
 // The borders are those of an earlier table, without non-temporal accesses.  By this
-// one they cost at most 2% but from 145 to 159 rows (blocks of 192: up to 7% less)
-// and from 241 to 272 (blocks of 128 or 192: up to 11% less).
+// one they cost at most 5% but from 145 to 159 rows (blocks of 192: up to 9% less)
+// and from 257 to 272 (blocks of 128 or 192: up to 12% less).
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
   const int64_t E = p.E, M = p.M;

@@ -68,7 +68,7 @@ namespace {
 //   512           266.0  199.1  192.8           171.7  121.2  117.0
 //  1024           477.8  372.9  333.3           290.1  224.5  205.9
 // The borders are those of an earlier table, without non-temporal accesses.  By this
-// one they cost at most 2% but at 21 to 24 rows (blocks of 64: up to 6% less), 65 to 72
+// one they cost at most 5% but at 21 to 24 rows (blocks of 64: up to 6% less), 65 to 72
 // (192: 9%) and 257 to 320 (192: up to 8%).
 template <int EPI, bool OUT32>
 int launch_epi(const Params& p, hipStream_t st) {
